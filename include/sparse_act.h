@@ -496,6 +496,102 @@ size_t sa_nm_shared_spmm_workspace_bytes(int64_t T, int64_t d_in, int n, int m, 
 int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
                int64_t d_out, uint16_t* y, void* stream);
 
+/* ---- dense linear layers: epilogues, gated projections, gradients ------------ */
+
+/*
+ * The dense half of the layers above: prompts, training batches and single
+ * tokens through the same transposed weights WT[d_in][d_out].  Common to the
+ * four calls below:
+ * - `dtype` is the type of every matrix and of bias: SA_F16 or SA_BF16.
+ *   Products, activations and sums are fp32; an output is rounded once.
+ * - Every matrix has a row stride `ld*` in elements: a multiple of 8, at
+ *   least the row length, at most 2^21.  Matrix and bias pointers are
+ *   16-byte aligned.  Strides allow gate and up stored side by side, or
+ *   outputs written into column blocks.
+ * - Requires 0 <= T <= 2^22 (any T, odd ones too), d_in and d_out positive
+ *   multiples of 8, at most 2^21.
+ * - T == 0: the forward calls do nothing; the backward calls write zero
+ *   weight and bias gradients.  Matrices of T rows may then be NULL.
+ * - Outputs must not overlap inputs, except y and residual of dense_linear,
+ *   which may be the same matrix.
+ * - `ws` is a device workspace of at least the bytes the call's
+ *   *_workspace_bytes function names (16-byte aligned; its contents on entry
+ *   do not matter; NULL allowed when that is 0).  Calls that share one must
+ *   be ordered on one stream.
+ * - Inf and NaN in a row of x reach that row's outputs only.
+ * - Sums run in a fixed order: equal calls give equal bits.
+ * - act: SA_ACT_*.  sigma(z) = 1 / (1 + e^-z), Phi the normal distribution
+ *   function.  The slope of relu and relu2 at 0 is 0.
+ */
+#define SA_F16 0
+#define SA_BF16 1
+#define SA_ACT_NONE 0
+#define SA_ACT_RELU 1      /* max(z, 0) */
+#define SA_ACT_RELU2 2     /* max(z, 0)^2 */
+#define SA_ACT_SILU 3      /* z sigma(z) */
+#define SA_ACT_GELU 4      /* z Phi(z) */
+#define SA_ACT_GELU_TANH 5 /* z sigma(2 sqrt(2/pi) (z + 0.044715 z^3)) */
+
+/*
+ * dense_linear -- pre = x W^T + bias, y = act(pre) + residual.
+ *   x [T][d_in]; wt [d_in][d_out]; bias [d_out] or NULL; residual [T][d_out]
+ *   or NULL; y [T][d_out]; pre [T][d_out] or NULL (rounded pre-activation,
+ *   for the backward call).
+ */
+int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
+                 int64_t d_in, int64_t d_out, const void* bias, int act, const void* residual,
+                 int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldpre, void* ws,
+                 size_t ws_bytes, void* stream);
+size_t dense_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
+
+/*
+ * dense_linear_backward -- the gradients of dense_linear from dy:
+ *   d = dy * act'(pre)  (act none: d = dy, pre not read)
+ *   dx = d W;  dwt = x^T d (the transposed layout);  dbias = sum over rows
+ *   of d.  The residual's gradient is dy itself.
+ * d is rounded to `dtype` before the two products (dbias sums it unrounded).
+ *   dy, pre [T][d_out] (pre NULL allowed when act is none); dx [T][d_in],
+ *   dwt [d_in][d_out], dbias [d_out]: each NULL when not wanted.
+ */
+int dense_linear_backward(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          int64_t T, const void* wt, int64_t ldw, int64_t d_in, int64_t d_out,
+                          int act, const void* pre, int64_t ldpre, void* dx, int64_t lddx,
+                          void* dwt, int64_t lddwt, void* dbias, void* ws, size_t ws_bytes,
+                          void* stream);
+size_t dense_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int act,
+                                             int with_dbias);
+
+/*
+ * gated_linear -- both projections of a gated feed-forward block and their
+ * product: g = x Wg^T, u = x Wu^T, h = act(g) * u, in one pass over x.
+ * h feeds a down projection (dense_linear, or sparse_gemv_threshold and its
+ * kin); g and u feed masked_swiglu_down.
+ *   x [T][d_in]; wgt, wut [d_in][d_out]; SA_ACT_NONE gives
+ *   h = g * u; h [T][d_out]; g, u [T][d_out], both or neither
+ *   NULL (rounded projections, for the backward call; h is computed from
+ *   the unrounded ones).
+ */
+int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
+                 const void* wut, int64_t ldwu, int64_t d_in, int64_t d_out, int act, void* h,
+                 int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
+                 size_t ws_bytes, void* stream);
+size_t gated_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
+
+/*
+ * gated_linear_backward -- the gradients of gated_linear from dh:
+ *   dg = dh * u * act'(g), du = dh * act(g), rounded to `dtype`;
+ *   dx = dg Wg + du Wu;  dwgt = x^T dg;  dwut = x^T du.
+ *   dh, g, u [T][d_out]; dx [T][d_in] or NULL; dwgt, dwut [d_in][d_out],
+ *   both or neither NULL.
+ */
+int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x, int64_t ldx,
+                          int64_t T, const void* wgt, int64_t ldwg, const void* wut, int64_t ldwu,
+                          int64_t d_in, int64_t d_out, int act, const void* g, int64_t ldg,
+                          const void* u, int64_t ldu, void* dx, int64_t lddx, void* dwgt,
+                          int64_t lddwg, void* dwut, int64_t lddwu, void* ws, size_t ws_bytes,
+                          void* stream);
+size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
+
 /* ---- roofline calibration ----------------------------------------------- */
 
 /* Words of `sink` that sa_read_stream writes (one per wave of its grid). */

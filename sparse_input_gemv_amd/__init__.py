@@ -17,6 +17,7 @@ GPU, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -31,8 +32,8 @@ __all__ = [
     "sparse_gemv_threshold_noalloc", "rana_adapter_gemv",
     "masked_gemv",
     "dense_gemv", "masked_swiglu_down", "weight_col_norms", "nm_act_spmm", "nm_shared_spmm",
-    "dense_gemm",
-    "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
+    "dense_gemm", "dense_linear", "dense_linear_backward", "gated_linear", "gated_linear_backward",
+    "ACTIVATIONS", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
     "workspace_zero_bytes", "scratch", "MAX_BATCH",
 ]
 
@@ -83,6 +84,19 @@ _SIGNATURES = {
     "sa_read_stream_grid": (_i32, [_vp, _sz, _vp, _i32, _vp]),
     "dense_gemm": (_i32, [_vp, _i64, _i64, _vp, _i64, _vp, _vp]),
     "sa_set_gemv_tuning": (_i32, [_i32, _i32, _i32]),
+    "dense_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp,
+                            _i64, _vp, _i64, _vp, _sz, _vp]),
+    "dense_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dense_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32,
+                                     _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "dense_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "gated_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64,
+                            _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "gated_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "gated_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64,
+                                     _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                     _i64, _vp, _sz, _vp]),
+    "gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "sa_set_gemm_tuning": (_i32, [_i32, _i32, _i32]),
     "sa_gemv_tiling_info": (_i32, [_i32, _vp, _vp, _vp]),
     "sa_gemv_plan": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
@@ -638,6 +652,201 @@ def dense_gemm(x: torch.Tensor, wt: torch.Tensor, y: torch.Tensor | None = None)
         y = torch.empty((T, d_out), dtype=torch.float16, device=wt.device)
     _check(lib().dense_gemm(_ptr(x), T, d_in, _ptr(wt), d_out, _ptr(y), _stream(wt)), "dense_gemm")
     return y
+
+
+# ---- dense linear layers -------------------------------------------------------
+
+ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}  # SA_ACT_*
+_LIN_DTYPES = {torch.float16: 0, torch.bfloat16: 1}  # SA_F16, SA_BF16
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _lin_x(x: torch.Tensor, name: str, d: int | None = None) -> torch.Tensor:
+    """``x`` as ``[T][d]`` (a vector is one row)."""
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise ValueError(f"{name} must be a torch tensor on a GPU")
+    if x.dtype not in _LIN_DTYPES:
+        raise ValueError(f"{name} must be float16 or bfloat16, got {x.dtype}")
+    if x.dim() == 1:
+        x = x[None]
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a vector or [rows][d], got {tuple(x.shape)}")
+    return x
+
+
+def _lin_mat(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: int) -> int:
+    """Checks a ``[rows][cols]`` operand (a vector serves as one row) and
+    returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.device != like.device:
+        raise ValueError(f"{name} must be a torch tensor on {like.device}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    shape = t.shape
+    if shape != (rows, cols) and not (rows == 1 and shape == (cols,)):
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and cols > 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return st[0] if rows > 1 else cols
+
+
+def _lin_vec(t: torch.Tensor, name: str, like: torch.Tensor, n: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.device != like.device or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if t.shape != (n,) or (t.stride(0) != 1 and n > 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
+
+
+def _lin_out(t, name: str, like: torch.Tensor, rows: int, cols: int):
+    """``(tensor, row stride)`` of an output, allocated when not given."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device), cols
+    return t, _lin_mat(t, name, like, rows, cols)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lin_ws_bytes(fn: str, *args) -> int:
+    return int(getattr(lib(), fn + "_workspace_bytes")(*args))
+
+
+def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
+    """Runs ``fn`` on the current stream of ``like``'s device, with scratch
+    of its own from torch's allocator: calls on other streams and captured
+    graphs share none."""
+    need = _lin_ws_bytes(fn, *sizes)
+    dev = like.device
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _ptr(ws), need, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _ptr(ws), need, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, fn)
+
+
+def dense_linear(x: torch.Tensor, wt: torch.Tensor, bias: torch.Tensor | None = None,
+                 act: str = "none", residual: torch.Tensor | None = None,
+                 y: torch.Tensor | None = None, with_pre: bool = False,
+                 pre: torch.Tensor | None = None):
+    """``y = act(x W^T + bias) + residual`` for fp16 or bf16 ``x`` (a vector or
+    ``[T][d_in]``) and ``wt[d_in][d_out]``; ``act`` is a key of
+    ``ACTIVATIONS``.  Rows may be strided.  ``y`` may be ``residual``.
+    Returns ``y``, or ``(y, pre)`` with the pre-activation when ``with_pre``
+    or ``pre`` is given (``dense_linear_backward`` reads it)."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    x = _lin_x(x, "x")
+    T, d_in = x.shape
+    d_out = wt.shape[-1]
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldw = _lin_mat(wt, "wt", x, d_in, d_out)
+    if bias is not None:
+        _lin_vec(bias, "bias", x, d_out)
+    ldr = 0 if residual is None else _lin_mat(residual, "residual", x, T, d_out)
+    y, ldy = _lin_out(y, "y", x, T, d_out)
+    ldp = 0
+    if with_pre or pre is not None:
+        pre, ldp = _lin_out(pre, "pre", x, T, d_out)
+    _lin_call("dense_linear", x, (T, d_in, d_out), _LIN_DTYPES[x.dtype], x.data_ptr(), ldx, T,
+              wt.data_ptr(), ldw, d_in, d_out, _ptr(bias), _act(act), _ptr(residual), ldr,
+              y.data_ptr(), ldy, _ptr(pre), ldp)
+    y = _ret(y, squeeze)
+    return y if pre is None else (y, _ret(pre, squeeze))
+
+
+def dense_linear_backward(dy: torch.Tensor, x: torch.Tensor, wt: torch.Tensor, act: str = "none",
+                          pre: torch.Tensor | None = None, with_dbias: bool = False,
+                          with_dx: bool = True, with_dwt: bool = True,
+                          dx: torch.Tensor | None = None, dwt: torch.Tensor | None = None):
+    """Gradients of ``dense_linear`` from ``dy``: ``(dx, dwt, dbias)``, None
+    where not asked for.  ``pre`` is the forward call's (not read when ``act``
+    is "none"); the residual's gradient is ``dy`` itself."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    x = _lin_x(x, "x")
+    T, d_in = x.shape
+    d_out = wt.shape[-1]
+    a = _act(act)
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldw = _lin_mat(wt, "wt", x, d_in, d_out)
+    lddy = _lin_mat(dy, "dy", x, T, d_out)
+    ldp = 0
+    if a != 0:
+        if pre is None:
+            raise ValueError(f"pre is needed for act {act!r}")
+        ldp = _lin_mat(pre, "pre", x, T, d_out)
+    else:
+        pre = None
+    lddx = lddw = 0
+    if with_dx or dx is not None:
+        dx, lddx = _lin_out(dx, "dx", x, T, d_in)
+    if with_dwt or dwt is not None:
+        dwt, lddw = _lin_out(dwt, "dwt", x, d_in, d_out)
+    dbias = torch.empty(d_out, dtype=x.dtype, device=x.device) if with_dbias else None
+    _lin_call("dense_linear_backward", x, (T, d_in, d_out, a, int(with_dbias)),
+              _LIN_DTYPES[x.dtype], dy.data_ptr(), lddy, x.data_ptr(), ldx, T, wt.data_ptr(), ldw,
+              d_in, d_out, a, _ptr(pre), ldp, _ptr(dx), lddx, _ptr(dwt), lddw, _ptr(dbias))
+    return None if dx is None else _ret(dx, squeeze), dwt, dbias
+
+
+def gated_linear(x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor, act: str = "silu",
+                 h: torch.Tensor | None = None, with_gu: bool = False,
+                 g: torch.Tensor | None = None, u: torch.Tensor | None = None):
+    """``h = act(x Wg^T) * (x Wu^T)``, both projections in one pass; fp16 or
+    bf16.  ``wgt`` and ``wut`` may be column blocks of one side-by-side
+    weight.  Returns ``h``, or ``(h, g, u)`` with the rounded projections when
+    ``with_gu`` (or both ``g`` and ``u``) is given."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    x = _lin_x(x, "x")
+    T, d_in = x.shape
+    d_out = wgt.shape[-1]
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldg_w = _lin_mat(wgt, "wgt", x, d_in, d_out)
+    ldu_w = _lin_mat(wut, "wut", x, d_in, d_out)
+    h, ldh = _lin_out(h, "h", x, T, d_out)
+    ldg = ldu = 0
+    if with_gu or g is not None or u is not None:
+        g, ldg = _lin_out(g, "g", x, T, d_out)
+        u, ldu = _lin_out(u, "u", x, T, d_out)
+    _lin_call("gated_linear", x, (T, d_in, d_out), _LIN_DTYPES[x.dtype], x.data_ptr(), ldx, T,
+              wgt.data_ptr(), ldg_w, wut.data_ptr(), ldu_w, d_in, d_out, _act(act), h.data_ptr(),
+              ldh, _ptr(g), ldg, _ptr(u), ldu)
+    h = _ret(h, squeeze)
+    return h if g is None else (h, _ret(g, squeeze), _ret(u, squeeze))
+
+
+def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor,
+                          g: torch.Tensor, u: torch.Tensor, act: str = "silu",
+                          with_dx: bool = True, with_dw: bool = True,
+                          dx: torch.Tensor | None = None, dwgt: torch.Tensor | None = None,
+                          dwut: torch.Tensor | None = None):
+    """Gradients of ``gated_linear`` from ``dh`` and the forward call's ``g``
+    and ``u``: ``(dx, dwgt, dwut)``, None where not asked for."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    x = _lin_x(x, "x")
+    T, d_in = x.shape
+    d_out = wgt.shape[-1]
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldg_w = _lin_mat(wgt, "wgt", x, d_in, d_out)
+    ldu_w = _lin_mat(wut, "wut", x, d_in, d_out)
+    lddh = _lin_mat(dh, "dh", x, T, d_out)
+    ldg = _lin_mat(g, "g", x, T, d_out)
+    ldu = _lin_mat(u, "u", x, T, d_out)
+    lddx = lddg = lddu = 0
+    if with_dx or dx is not None:
+        dx, lddx = _lin_out(dx, "dx", x, T, d_in)
+    if with_dw or dwgt is not None or dwut is not None:
+        dwgt, lddg = _lin_out(dwgt, "dwgt", x, d_in, d_out)
+        dwut, lddu = _lin_out(dwut, "dwut", x, d_in, d_out)
+    _lin_call("gated_linear_backward", x, (T, d_in, d_out), _LIN_DTYPES[x.dtype], dh.data_ptr(),
+              lddh, x.data_ptr(), ldx, T, wgt.data_ptr(), ldg_w, wut.data_ptr(), ldu_w, d_in, d_out,
+              _act(act), g.data_ptr(), ldg, u.data_ptr(), ldu, _ptr(dx), lddx, _ptr(dwgt), lddg,
+              _ptr(dwut), lddu)
+    return None if dx is None else _ret(dx, squeeze), dwgt, dwut
 
 
 # ---- tuning -------------------------------------------------------------------

@@ -645,4 +645,248 @@ int sa_gemv_tiling_info(int i, int* tile_o, int* threads, int* unroll) {
   return SA_OK;
 }
 
+// ---- dense linear layers --------------------------------------------------------
+
+static int run_linear(const sa::LinearCall& c, bool backward, const char* fn, void* stream) {
+  hipError_t e = backward ? sa::launch_linear_backward(c, as_stream(stream))
+                          : sa::launch_linear(c, as_stream(stream));
+  if (e == hipErrorNotSupported) {
+    sa::set_error("%s: shape not supported by the compiled kernels", fn);
+    return SA_ERR_UNSUPPORTED;
+  }
+  return hip_status(e, fn);
+}
+
+static const uint16_t* in16(const void* p) { return static_cast<const uint16_t*>(p); }
+static uint16_t* out16(const void* p) { return static_cast<uint16_t*>(const_cast<void*>(p)); }
+
+size_t dense_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, 0) != SA_OK) return 0;
+  return sa::linear_workspace_bytes(false, T, d_in, d_out);
+}
+
+size_t gated_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, 0) != SA_OK) return 0;
+  return sa::linear_workspace_bytes(true, T, d_in, d_out);
+}
+
+size_t dense_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int act,
+                                             int with_dbias) {
+  if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, act) != SA_OK) return 0;
+  return sa::linear_backward_workspace_bytes(false, T, d_in, d_out, act, with_dbias != 0);
+}
+
+size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
+  if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, 0) != SA_OK) return 0;
+  return sa::linear_backward_workspace_bytes(true, T, d_in, d_out, 0, false);
+}
+
+int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
+                 int64_t d_in, int64_t d_out, const void* bias, int act, const void* residual,
+                 int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldpre, void* ws,
+                 size_t ws_bytes, void* stream) {
+  const char* fn = "dense_linear";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wt", wt, ldw, d_out, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "residual", residual, ldr, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "y", y, ldy, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "pre", pre, ldpre, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "bias", bias);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "y", y, "x", x);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "y", y, "wt", wt);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "x", x);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "wt", wt);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "y", y);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "residual", residual);
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes, sa::linear_workspace_bytes(false, T, d_in, d_out));
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  sa::LinearCall c;
+  c.dtype = dtype;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wt);
+  c.ldw[0] = ldw;
+  c.bias = in16(bias);
+  c.res = in16(residual);
+  c.ldr = ldr;
+  c.y = out16(y);
+  c.ldy = ldy;
+  c.pre[0] = out16(pre);
+  c.ldpre[0] = ldpre;
+  c.ws = ws;
+  return run_linear(c, false, fn, stream);
+}
+
+int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
+                 const void* wut, int64_t ldwu, int64_t d_in, int64_t d_out, int act, void* h,
+                 int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
+                 size_t ws_bytes, void* stream) {
+  const char* fn = "gated_linear";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wgt", wgt, ldwg, d_out, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wut", wut, ldwu, d_out, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "h", h, ldh, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_both(fn, "g", g, "u", u);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "g", g, ldg, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "u", u, ldu, d_out, true);
+  const void* outs[3] = {h, g, u};
+  const char* names[3] = {"h", "g", "u"};
+  for (int i = 0; i < 3; ++i) {
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "x", x);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "wgt", wgt);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "wut", wut);
+    for (int j = 0; j < i; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], names[j], outs[j]);
+  }
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes, sa::linear_workspace_bytes(true, T, d_in, d_out));
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  sa::LinearCall c;
+  c.dtype = dtype;
+  c.gated = true;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wgt);
+  c.ldw[0] = ldwg;
+  c.w[1] = in16(wut);
+  c.ldw[1] = ldwu;
+  c.y = out16(h);
+  c.ldy = ldh;
+  c.pre[0] = out16(g);
+  c.ldpre[0] = ldg;
+  c.pre[1] = out16(u);
+  c.ldpre[1] = ldu;
+  c.ws = ws;
+  return run_linear(c, false, fn, stream);
+}
+
+int dense_linear_backward(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          int64_t T, const void* wt, int64_t ldw, int64_t d_in, int64_t d_out,
+                          int act, const void* pre, int64_t ldpre, void* dx, int64_t lddx,
+                          void* dwt, int64_t lddwt, void* dbias, void* ws, size_t ws_bytes,
+                          void* stream) {
+  const char* fn = "dense_linear_backward";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dy", dy, lddy, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, dwt == nullptr || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wt", wt, ldw, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "pre", pre, ldpre, d_out,
+                                                    act == SA_ACT_NONE || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dx", dx, lddx, d_in, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwt", dwt, lddwt, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "dbias", dbias);
+  const void* ins[4] = {dy, x, wt, pre};
+  const char* names[4] = {"dy", "x", "wt", "pre"};
+  for (int i = 0; i < 4; ++i) {
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dx", dx, names[i], ins[i]);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dwt", dwt, names[i], ins[i]);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dbias", dbias, names[i], ins[i]);
+  }
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "dx", dx, "dwt", dwt);
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes,
+                             sa::linear_backward_workspace_bytes(false, T, d_in, d_out, act,
+                                                                 dbias != nullptr));
+  if (st != SA_OK) return st;
+  sa::LinearCall c;
+  c.dtype = dtype;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.dy = in16(dy);
+  c.lddy = lddy;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wt);
+  c.ldw[0] = ldw;
+  c.pre[0] = out16(pre);
+  c.ldpre[0] = ldpre;
+  c.dx = out16(dx);
+  c.lddx = lddx;
+  c.dw[0] = out16(dwt);
+  c.lddw[0] = lddwt;
+  c.dbias = out16(dbias);
+  c.ws = ws;
+  return run_linear(c, true, fn, stream);
+}
+
+int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x, int64_t ldx,
+                          int64_t T, const void* wgt, int64_t ldwg, const void* wut, int64_t ldwu,
+                          int64_t d_in, int64_t d_out, int act, const void* g, int64_t ldg,
+                          const void* u, int64_t ldu, void* dx, int64_t lddx, void* dwgt,
+                          int64_t lddwg, void* dwut, int64_t lddwu, void* ws, size_t ws_bytes,
+                          void* stream) {
+  const char* fn = "gated_linear_backward";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_linear_both(fn, "dwgt", dwgt, "dwut", dwut);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dh", dh, lddh, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, dwgt == nullptr || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wgt", wgt, ldwg, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wut", wut, ldwu, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "g", g, ldg, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "u", u, ldu, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dx", dx, lddx, d_in, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwgt", dwgt, lddwg, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwut", dwut, lddwu, d_out, true);
+  const void* ins[6] = {dh, x, wgt, wut, g, u};
+  const char* in_names[6] = {"dh", "x", "wgt", "wut", "g", "u"};
+  const void* outs[3] = {dx, dwgt, dwut};
+  const char* names[3] = {"dx", "dwgt", "dwut"};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], in_names[j], ins[j]);
+    for (int j = 0; j < i; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], names[j], outs[j]);
+  }
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes,
+                             sa::linear_backward_workspace_bytes(true, T, d_in, d_out, act, false));
+  if (st != SA_OK) return st;
+  sa::LinearCall c;
+  c.dtype = dtype;
+  c.gated = true;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.dy = in16(dh);
+  c.lddy = lddh;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wgt);
+  c.ldw[0] = ldwg;
+  c.w[1] = in16(wut);
+  c.ldw[1] = ldwu;
+  c.pre[0] = out16(g);
+  c.ldpre[0] = ldg;
+  c.pre[1] = out16(u);
+  c.ldpre[1] = ldu;
+  c.dx = out16(dx);
+  c.lddx = lddx;
+  c.dw[0] = out16(dwgt);
+  c.lddw[0] = lddwg;
+  c.dw[1] = out16(dwut);
+  c.lddw[1] = lddwu;
+  c.ws = ws;
+  return run_linear(c, true, fn, stream);
+}
+
 }  // extern "C"

@@ -149,4 +149,40 @@ hipError_t launch_nm_shared_spmm(const uint16_t* xval, const uint32_t* mask, int
                                  hipStream_t s);
 int gemm_set_tuning(int bm, int engine, int stages);
 
+// ---- dense linear layers (linear.hip) -----------------------------------------
+// Forward (x, w -> y) and backward (dy, x, w, pre -> dx, dw, dbias) of one
+// projection (w[0]) or of the gated pair (w[0] gate, w[1] up).
+struct LinearCall {
+  int dtype = 0;  // SA_F16, SA_BF16
+  bool gated = false;
+  int act = 0;    // SA_ACT_*
+  int64_t T = 0, d_in = 0, d_out = 0;
+  const uint16_t* x = nullptr;
+  int64_t ldx = 0;
+  const uint16_t* w[2] = {nullptr, nullptr};
+  int64_t ldw[2] = {0, 0};
+  const uint16_t* bias = nullptr;
+  const uint16_t* res = nullptr;
+  int64_t ldr = 0;
+  uint16_t* y = nullptr;
+  int64_t ldy = 0;
+  // forward: written when not NULL; backward: read
+  uint16_t* pre[2] = {nullptr, nullptr};
+  int64_t ldpre[2] = {0, 0};
+  // backward
+  const uint16_t* dy = nullptr;
+  int64_t lddy = 0;
+  uint16_t* dx = nullptr;  // NULL: not computed
+  int64_t lddx = 0;
+  uint16_t* dw[2] = {nullptr, nullptr};  // dw[0] NULL: not computed
+  int64_t lddw[2] = {0, 0};
+  uint16_t* dbias = nullptr;
+  void* ws = nullptr;
+};
+size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out);
+size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
+                                       bool dbias);
+hipError_t launch_linear(const LinearCall& c, hipStream_t s);
+hipError_t launch_linear_backward(const LinearCall& c, hipStream_t s);
+
 }  // namespace sa

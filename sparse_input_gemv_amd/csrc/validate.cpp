@@ -314,4 +314,61 @@ int check_dense_gemm(const void* x, int64_t T, int64_t d_in, const void* wt, int
   return SA_OK;
 }
 
+int check_linear_sizes(const char* fn, int dtype, int64_t T, int64_t d_in, int64_t d_out,
+                       int act) {
+  REQUIRE(dtype == SA_F16 || dtype == SA_BF16, SA_ERR_INVALID_ARG,
+          "%s: dtype must be SA_F16 or SA_BF16", fn);
+  REQUIRE(act >= SA_ACT_NONE && act <= SA_ACT_GELU_TANH, SA_ERR_INVALID_ARG,
+          "%s: unknown activation %d", fn, act);
+  REQUIRE(T >= 0, SA_ERR_INVALID_ARG, "%s: T must be >= 0 (got %lld)", fn, (long long)T);
+  REQUIRE(d_in >= 8 && d_in % 8 == 0, SA_ERR_INVALID_ARG,
+          "%s: d_in must be a positive multiple of 8", fn);
+  REQUIRE(d_out >= 8 && d_out % 8 == 0, SA_ERR_INVALID_ARG,
+          "%s: d_out must be a positive multiple of 8", fn);
+  REQUIRE(d_in <= kMaxLinDim && d_out <= kMaxLinDim, SA_ERR_UNSUPPORTED,
+          "%s: d_in and d_out must be at most %lld", fn, (long long)kMaxLinDim);
+  REQUIRE(T <= kMaxLinRows, SA_ERR_UNSUPPORTED, "%s: T must be at most %lld", fn,
+          (long long)kMaxLinRows);
+  return SA_OK;
+}
+
+int check_linear_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t len,
+                        bool optional) {
+  if (optional && p == nullptr) return SA_OK;
+  REQUIRE(p != nullptr, SA_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  REQUIRE(aligned(p, 16), SA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  REQUIRE(ld >= len && ld % 8 == 0, SA_ERR_INVALID_ARG,
+          "%s: the row stride of %s must be a multiple of 8 and at least %lld (got %lld)", fn, name,
+          (long long)len, (long long)ld);
+  REQUIRE(ld <= kMaxLinDim, SA_ERR_UNSUPPORTED, "%s: the row stride of %s must be at most %lld", fn,
+          name, (long long)kMaxLinDim);
+  return SA_OK;
+}
+
+int check_linear_vector(const char* fn, const char* name, const void* p) {
+  REQUIRE(aligned(p, 16), SA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  return SA_OK;
+}
+
+int check_linear_distinct(const char* fn, const char* out, const void* o, const char* in,
+                          const void* i) {
+  REQUIRE(o == nullptr || o != i, SA_ERR_INVALID_ARG, "%s: %s must not be %s", fn, out, in);
+  return SA_OK;
+}
+
+int check_linear_both(const char* fn, const char* a, const void* pa, const char* b,
+                      const void* pb) {
+  REQUIRE((pa == nullptr) == (pb == nullptr), SA_ERR_INVALID_ARG,
+          "%s: %s and %s must be given together", fn, a, b);
+  return SA_OK;
+}
+
+int check_linear_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return SA_OK;
+  REQUIRE(ws != nullptr && ws_bytes >= need, SA_ERR_WORKSPACE,
+          "%s: workspace of %zu bytes needed, %zu given", fn, need, ws ? ws_bytes : (size_t)0);
+  REQUIRE(aligned(ws, 16), SA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+  return SA_OK;
+}
+
 }  // namespace sa

@@ -49,6 +49,20 @@ int check_nm_spmm(const void* xval, const void* mask, int64_t T, int64_t d_in, i
                   const void* wt, int64_t d_out, const void* y);
 int check_nm_shared_spmm(const void* xval, const void* mask, int64_t T, int64_t d_in, int n,
                          int m, int tt, const void* wt, int64_t d_out, const void* y);
+
+// Dense linear layers.  A matrix argument: its pointer, row stride and row
+// length; `rows` only for messages.
+constexpr int64_t kMaxLinDim = (int64_t)1 << 21;   // d_in, d_out, strides
+constexpr int64_t kMaxLinRows = (int64_t)1 << 22;  // T
+int check_linear_sizes(const char* fn, int dtype, int64_t T, int64_t d_in, int64_t d_out, int act);
+int check_linear_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t len,
+                        bool optional);
+int check_linear_vector(const char* fn, const char* name, const void* p);
+int check_linear_distinct(const char* fn, const char* out, const void* o, const char* in,
+                          const void* i);
+int check_linear_both(const char* fn, const char* a, const void* pa, const char* b,
+                      const void* pb);
+int check_linear_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need);
 int check_dense_gemm(const void* x, int64_t T, int64_t d_in, const void* wt, int64_t d_out,
                      const void* y);
 
