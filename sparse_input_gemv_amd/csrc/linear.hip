@@ -16,6 +16,9 @@
 //   dWT      P = x, read as m = d_in, k = T: NC,  Q = d [T][d_out]: NC.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "../../include/sparse_act.h"
 #include "common.hpp"
 #include "launch.hpp"
@@ -27,7 +30,6 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 // ---- element types ---------------------------------------------------------
@@ -41,15 +43,23 @@ __device__ __forceinline__ uint16_t from_f(float f) {  // round to nearest even
   if constexpr (DT == SA_F16) return f2h(f);
   else return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
+// acc += a b on one 16 x 16 block, K = 32, in place in accumulation registers.
+// Inline asm ties the result to the sum's registers: with 256 of them in use
+// the compiler's own choice moves sums between registers in the K loop.
+// Nothing reads a sum inside the loop; acc_settle() makes it readable.
 template <int DT>
-__device__ __forceinline__ f4v mfma16(s8v a, s8v b, f4v c) {
+__device__ __forceinline__ void mfma16(f4v& acc, s8v a, s8v b) {
   if constexpr (DT == SA_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
-                                                  __builtin_bit_cast(half8, b), c, 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8v, a),
-                                                   __builtin_bit_cast(bf8v, b), c, 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
+// Wait states that the compiler does not place around inline asm: after the
+// last product, before other instructions read a sum (18 for a 16-pass
+// product; this one takes 4 passes), and between other instructions' writes
+// and a product (2).
+__device__ __forceinline__ void acc_wait() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+__device__ __forceinline__ void acc_settle(f4v& acc) { asm volatile("" : "+a"(acc)); }
 
 // ---- activations and their slopes (fp32) -------------------------------------
 // sigma(z) = 1 / (1 + e^-z).  gelu's normal distribution function goes
@@ -100,36 +110,32 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
 }
-__device__ __forceinline__ i4v make_rsrc(const void* base, int64_t bytes) {
-  const uint64_t a = (uint64_t)(uintptr_t)base;
-  if (bytes < 0) bytes = 0;
-  if (bytes > 0x7fffffffLL) bytes = 0x7fffffffLL;
-  i4v r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu));
-  r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
-  r[3] = 0x00020000;
-  return r;
+// A value the whole wave shares, in a scalar register.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uni(const void* p) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return (uint64_t)(uint32_t)uni((int)(a >> 32)) << 32 | (uint32_t)uni((int)a);
 }
 constexpr uint32_t kOutOfRange = 0x80000000u;  // past every resource
-__device__ __forceinline__ void load_lds16(uint32_t voff, i4v rsrc, uint32_t lds) {
-  asm volatile(
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %0, %1, 0 offen lds"
-      :
-      : "v"(voff), "s"(rsrc), "{m0}"(lds)
-      : "memory");
+// The LDS base goes in M0, which nothing else in these kernels uses.  The
+// write needs one instruction between it and the load: the K loop puts a
+// product there, load_lds16_now a no-op.
+__device__ __forceinline__ void set_lds(uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0" : : "s"(lds) : "memory");
+}
+__device__ __forceinline__ void load_lds16(uint32_t voff, i4v rsrc) {
+  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc) : "memory");
 }
 
-// Waits until at most VM loads and no LDS reads are outstanding, then the
-// workgroup barrier.  s_waitcnt encoding: vmcnt bits 3:0 and 15:14, expcnt
-// 6:4 (7: no wait), lgkmcnt 11:8.
-template <int VM>
+// Waits until at most VM loads and LG LDS reads are outstanding (63, 15: no
+// wait), then the workgroup barrier.  s_waitcnt encoding: vmcnt bits 3:0 and
+// 15:14, expcnt 6:4 (7: no wait), lgkmcnt 11:8.
+template <int VM, int LG>
 __device__ __forceinline__ void stage_barrier() {
-  static_assert(VM >= 0 && VM < 64, "vmcnt range");
+  static_assert(VM >= 0 && VM < 64 && LG >= 0 && LG < 16, "counter ranges");
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | (LG << 8) | ((VM >> 4) << 14));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -166,8 +172,8 @@ enum Layout { kFwd = 0, kDx = 1, kDw = 2 };
 struct LinP {
   const uint16_t* p[2];  // row operand (per K segment)
   const uint16_t* q[2];  // column operand (per K segment, gated half or output)
-  int64_t ldp, ldq[2];
-  int64_t M, N, K;       // K per segment
+  int ldp, ldq[2];
+  int M, N, K;           // K per segment
   int segs;              // K segments (dx of the gated pair: 2)
   int outs;              // outputs side by side (dW of the gated pair: 2)
   int slices;            // split of the K steps over workgroups
@@ -176,50 +182,101 @@ struct LinP {
   int act;
   const uint16_t* bias;
   const uint16_t* res;
-  int64_t ldr;
+  int ldr;
   uint16_t* y[2];        // output (per outs)
-  int64_t ldy[2];
+  int ldy[2];
   uint16_t* pre[2];      // pre-activation, or g and u
-  int64_t ldpre[2];
+  int ldpre[2];
 };
 
-template <int DT>
-__device__ __forceinline__ void store4(uint16_t* p, f4v v) {
-  u16x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = from_f<DT>(v[i]);
-  *reinterpret_cast<u16x4*>(p) = o;
+// f(0), ..., f(N - 1) with compile-time arguments.
+template <class F, int... I>
+__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_(std::make_integer_sequence<int, N>{}, f);
 }
 
-// Four outputs of row m from column n on (all within N).
+struct F8 {
+  float v[8];
+};
 template <int DT>
-__device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, int64_t n, f4v v) {
-  if (p.bias) {
-    const u16x4 b = *reinterpret_cast<const u16x4*>(p.bias + n);
+__device__ __forceinline__ F8 load8(const uint16_t* p) {
+  const u16x8 r = *reinterpret_cast<const u16x8*>(p);
+  F8 f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += to_f<DT>(b[i]);
-  }
-  if (p.pre[0]) store4<DT>(p.pre[0] + m * p.ldpre[0] + n, v);
-  if (p.act != SA_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_value(p.act, v[i]);
-  }
-  if (p.res) {
-    const u16x4 r = *reinterpret_cast<const u16x4*>(p.res + m * p.ldr + n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += to_f<DT>(r[i]);
-  }
-  store4<DT>(p.y[o] + m * p.ldy[o] + n, v);
+  for (int i = 0; i < 8; ++i) f.v[i] = to_f<DT>(r[i]);
+  return f;
 }
 template <int DT>
-__device__ __forceinline__ void finish_gated(const LinP& p, int64_t m, int64_t n, f4v g, f4v u) {
+__device__ __forceinline__ void store8(uint16_t* p, const F8& f) {
+  u16x8 o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = from_f<DT>(f.v[i]);
+  *reinterpret_cast<u16x8*>(p) = o;
+}
+
+// Eight outputs of row m from column n on (n a multiple of 8 below N).
+template <int DT>
+__device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, int n, F8 f) {
+  if (p.bias) {
+    const F8 b = load8<DT>(p.bias + n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] += b.v[i];
+  }
+  if (p.pre[0]) store8<DT>(p.pre[0] + m * p.ldpre[0] + n, f);
+  if (p.act != SA_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = act_value(p.act, f.v[i]);
+  }
+  if (p.res) {
+    const F8 r = load8<DT>(p.res + m * p.ldr + n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] += r.v[i];
+  }
+  store8<DT>(p.y[o] + m * p.ldy[o] + n, f);
+}
+template <int DT>
+__device__ __forceinline__ void finish_gated(const LinP& p, int64_t m, int n, F8 g, const F8& u) {
   if (p.pre[0]) {
-    store4<DT>(p.pre[0] + m * p.ldpre[0] + n, g);
-    store4<DT>(p.pre[1] + m * p.ldpre[1] + n, u);
+    store8<DT>(p.pre[0] + m * p.ldpre[0] + n, g);
+    store8<DT>(p.pre[1] + m * p.ldpre[1] + n, u);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = act_value(p.act, g[i]) * u[i];
-  store4<DT>(p.y[0] + m * p.ldy[0] + n, g);
+  for (int i = 0; i < 8; ++i) g.v[i] = act_value(p.act, g.v[i]) * u.v[i];
+  store8<DT>(p.y[0] + m * p.ldy[0] + n, g);
+}
+
+// Two neighbouring blocks' sums of one row: lane group g holds columns
+// 4g..4g+3 of each.  Swapping the odd groups of the first with the even
+// groups of the second leaves every lane 8 consecutive columns: of the first
+// block (g even) or the second (g odd), from column 8 (g / 2) on.
+__device__ __forceinline__ F8 pair8(const f4v& a, const f4v& b) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = a[i], y = b[i];
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                    __builtin_bit_cast(uint32_t, y), false, false);
+    const uint32_t lo = s[0], hi = s[1];
+    f.v[i] = __builtin_bit_cast(float, lo);
+    f.v[4 + i] = __builtin_bit_cast(float, hi);
+  }
+  return f;
+}
+__device__ __forceinline__ void store_part(float* p, const F8& f) {
+  *reinterpret_cast<f4v*>(p) = f4v{f.v[0], f.v[1], f.v[2], f.v[3]};
+  *reinterpret_cast<f4v*>(p + 4) = f4v{f.v[4], f.v[5], f.v[6], f.v[7]};
+}
+__device__ __forceinline__ void add_part(F8& f, const float* p) {
+  const f4v a = *reinterpret_cast<const f4v*>(p), b = *reinterpret_cast<const f4v*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.v[i] += a[i];
+    f.v[4 + i] += b[i];
+  }
 }
 
 // The tile of workgroup b: the hardware deals workgroups over the 8 XCDs in
@@ -227,22 +284,26 @@ __device__ __forceinline__ void finish_gated(const LinP& p, int64_t m, int64_t n
 // tiles across all column tiles); tiles that run together on one XCD share
 // their operands in its L2.  A bijection.
 constexpr int kGroupM = 4;
-__device__ __forceinline__ void tile_of(int64_t b, int64_t total, int64_t mt, int64_t nt,
-                                        int64_t& m, int64_t& n, int64_t& slice) {
-  const int64_t x = b % 8, l = b / 8;
-  const int64_t per = total / 8, rem = total % 8;
-  int64_t t = x * per + (x < rem ? x : rem) + l;
-  slice = t / (mt * nt);
-  t %= mt * nt;
-  const int64_t gsz = kGroupM * nt;
-  const int64_t first = (t / gsz) * kGroupM;
-  const int64_t gm = (mt - first < kGroupM) ? mt - first : kGroupM;
-  m = first + (t % gsz) % gm;
-  n = (t % gsz) / gm;
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t total, uint32_t mt, uint32_t nt, int& m,
+                                        int& n, int& slice) {
+  const uint32_t x = b % 8, l = b / 8;
+  const uint32_t per = total / 8, rem = total % 8;
+  uint32_t t = x * per + (x < rem ? x : rem) + l;
+  const uint32_t tiles = mt * nt;
+  slice = uni((int)(t / tiles));
+  t -= (uint32_t)slice * tiles;
+  const uint32_t gsz = kGroupM * nt;
+  const uint32_t grp = t / gsz, first = grp * kGroupM;
+  const uint32_t gm = (mt - first < kGroupM) ? mt - first : kGroupM;
+  const uint32_t in = t - grp * gsz;
+  n = uni((int)(in / gm));
+  m = uni((int)(first + in - (uint32_t)n * gm));
 }
 
 // One operand's tile: R rows (KC) or columns (NC) by 64 k, loaded by four
-// waves with I instructions of 1 KB each.
+// waves with I instructions of 1 KB each.  start() places it at a K step;
+// every next() moves one step on, and after `left` k has run out the loads
+// read zeros.
 template <bool NC, int R>
 struct Operand {
   static constexpr int kRows = NC ? R : (R < 32 ? 32 : R);
@@ -251,8 +312,13 @@ struct Operand {
   static_assert(!NC || R % 128 == 0, "NC tiles come in halves of 128 columns");
   static_assert(I >= 1, "one load per wave at least");
   uint32_t voff[I];
-  __device__ __forceinline__ void init(int w, int64_t ld) {
+  int kc[2];              // KC: the lane's first k (even and odd instructions)
+  uint64_t base;          // address of the step
+  int64_t step;           // bytes per step
+  int span, cols, ld;     // KC: bytes of the rows before the last; NC: columns left, row stride
+  __device__ __forceinline__ void init(int w, int ldv) {
     const int lane = lane_id();
+    ld = ldv;
 #pragma unroll
     for (int j = 0; j < I; ++j) {
       const int id = w * I + j;
@@ -264,57 +330,70 @@ struct Operand {
         const int r = id * 8 + lane / 8;
         const int c = (lane % 8) ^ swz_kc(r);
         voff[j] = (uint32_t)(r * ld * 2 + c * 16);
+        if (j < 2) kc[j] = 8 * c;
       }
+    }
+    if constexpr (!NC && I == 1) kc[1] = kc[0];
+  }
+  // The tile that starts at row (column) r0 of `rows`, at k0 of matrix m.
+  __device__ __forceinline__ void start(const uint16_t* m, int r0, int rows, int k0, int w) {
+    if constexpr (NC) {
+      const int c0 = r0 + 128 * ((w * I) / 16);  // the wave's loads lie in one half tile
+      cols = uni(rows - c0 > 0 ? rows - c0 : 0);
+      base = uni(m + (int64_t)k0 * ld + c0);
+      step = (int64_t)BK * 2 * ld;
+    } else {
+      const int left = rows - r0 < R ? rows - r0 : R;
+      span = uni((left - 1) * ld * 2);
+      base = uni(m + (int64_t)r0 * ld + k0);
+      step = BK * 2;
     }
   }
-  // K step starting at k0 (k0 >= K: zeros) of the operand whose tile starts
-  // at row or column r0 of `rows` (KC: rows; NC: columns).
-  __device__ __forceinline__ void issue(const uint16_t* base, int64_t ld, int64_t r0, int64_t rows,
-                                        int64_t k0, int64_t K, uint32_t lds, int w) const {
-    if constexpr (NC) {
-      // the wave's loads lie in one half tile
-      const int64_t c0 = r0 + 128 * ((w * I) / 16);
-      int64_t left = K - k0;
-      if (left > BK) left = BK;
-      const int64_t bytes = (left > 0 && c0 < rows) ? ((left - 1) * ld + (rows - c0)) * 2 : 0;
-      const i4v rs = make_rsrc(base + k0 * ld + c0, bytes);
-#pragma unroll
-      for (int j = 0; j < I; ++j) load_lds16(voff[j], rs, lds + (w * I + j) * 1024);
-    } else {
-      int64_t left = rows - r0;
-      if (left > R) left = R;
-      const int64_t bytes = (left > 0 && k0 < K) ? ((left - 1) * ld + (K - k0)) * 2 : 0;
-      const i4v rs = make_rsrc(base + r0 * ld + k0, bytes);
-      if (K - k0 >= BK) {
-#pragma unroll
-        for (int j = 0; j < I; ++j) load_lds16(voff[j], rs, lds + (w * I + j) * 1024);
-      } else {
-        // the row's end lies inside the step: chunks past it are zeros, not
-        // the next row
-        const int lane = lane_id();
-#pragma unroll
-        for (int j = 0; j < I; ++j) {
-          const int r = (w * I + j) * 8 + lane / 8;
-          const int c = (lane % 8) ^ swz_kc(r);
-          load_lds16(k0 + 8 * c < K ? voff[j] : kOutOfRange, rs, lds + (w * I + j) * 1024);
-        }
-      }
-    }
+  // The step's resource: the bytes from its base to the operand's end.
+  __device__ __forceinline__ i4v rsrc(int left) const {
+    int bytes;
+    if constexpr (NC)
+      bytes = (left > 0 && cols > 0) ? (((left < BK ? left : BK) - 1) * ld + cols) * 2 : 0;
+    else
+      bytes = left > 0 ? span + left * 2 : 0;
+    return i4v{uni((int)(uint32_t)base), uni((int)((uint32_t)(base >> 32) & 0xffffu)), uni(bytes),
+               0x00020000};
+  }
+  __device__ __forceinline__ void next() { base += step; }
+  // Load j of the step, in two parts: its place in LDS (M0), then the load.
+  // KC chunks past the row's end are zeros, not the next row.
+  __device__ __forceinline__ static void place(int j, uint32_t lds, int w) {
+    set_lds(lds + (w * I + j) * 1024);
+  }
+  __device__ __forceinline__ void load(int j, i4v rs, int left) const {
+    uint32_t v = voff[j];
+    if constexpr (!NC) v = kc[j & 1] < left ? v : kOutOfRange;
+    load_lds16(v, rs);
   }
 };
 
-// C tile of BM x BN (gated: BN / 2 columns of g and of u), 256 threads as WM
-// x WN waves.  The K loop steps through NS LDS stages; operands are double
-// buffered in registers by half steps of 32 k: while the MFMAs of one half
-// run, the reads of the next half are in flight.  One barrier per step, in
-// its middle: every wave has then read all of stage t, so its buffer takes
-// the loads of stage t + NS; and stage t + 1 is complete.  Loads past the
-// last step read zeros, so the load count per step never changes.
+// C tiles of BM x BN (gated: BN / 2 columns of g and of u), 256 threads as
+// WM x WN waves.  A workgroup takes the (tile, slice) items blockIdx.x,
+// blockIdx.x + gridDim.x, ... and runs one K loop over all their steps: the
+// loads of the next item's first steps are under way while an item's outputs
+// are written.
+//
+// A step is two halves of 32 k, each N products per wave.  Operands are
+// double buffered in registers by halves: half 0 carries the LDS reads of
+// half 1 in its first RS products, half 1 those of the next step's half 0.
+// After REL products of half 0 every wave has read all of the stage (one
+// barrier), and its buffer takes the loads of stage t + NS, spread evenly over
+// the products up to product X of the next step's half 0: a CU's loads share
+// one address path that takes 16 cycles per load, and the waves issue them
+// together.  After RDY products of half 1 (the other barrier) stage t + 1 has
+// arrived.  Loads past the last item read zeros, so counts never change.
+// gfx950 at 256 x 256: 64 KB per stage, two stages, one wave per SIMD with
+// 256 sums in accumulation registers.
 template <int DT, int LAY, bool GATED, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   constexpr bool PNC = LAY == kDw, QNC = LAY != kDx;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
-  static_assert(WM * WN == 4 && MB >= 1 && NB >= 1, "four waves");
+  static_assert(WM * WN == 4 && MB >= 1 && NB >= 2 && NB % (GATED ? 4 : 2) == 0, "four waves");
   using OP = Operand<PNC, BM>;
   using OQ = Operand<QNC, BN>;
   constexpr int L = OP::I + OQ::I;
@@ -322,44 +401,106 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   __shared__ __align__(16) uint8_t S[NS * kStage];
   const uint32_t lp = lds_addr(S), lq = lp + NS * OP::kBytes;
 
+  constexpr int N = MB * NB, R = MB + NB;
+  constexpr int RS = N * 5 / 8 > 0 ? N * 5 / 8 : 1;
+  constexpr int REL = RS + N / 16, RDY = N * 5 / 16, X = N * 5 / 16;
+  constexpr int SPAN = 2 * N + X - REL;
+  static_assert(REL < N && RDY + RS <= N && X <= REL, "schedule");
+  // Load j's position is REL + j * SPAN / L products from the start of the
+  // step; loads at positions below q:
+  constexpr auto before = [](int q) constexpr {
+    int c = 0;
+    for (int j = 0; j < L; ++j) c += (REL + j * SPAN / L) < q;
+    return c;
+  };
+  constexpr int J1 = before(2 * N);       // loads within the step; the others in the next
+  constexpr int CR = before(N + RDY);     // loads issued when stage t + 1 must have arrived
+
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int wm = w / WN, wn = w % WN;
   constexpr int BNO = GATED ? BN / 2 : BN;  // output columns per tile
-  const int64_t mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO;
-  const int64_t nt = nt1 * p.outs;
-  int64_t mi, ni, slice;
-  tile_of(blockIdx.x, gridDim.x, mt, nt, mi, ni, slice);
-  const int out = ni >= nt1;
-  const int64_t m0 = mi * BM, n0 = (ni - (out ? nt1 : 0)) * BNO;
-
-  const int64_t ks = (p.K + BK - 1) / BK;  // steps per segment
-  const int64_t steps = ks * p.segs;
-  const int64_t s0 = steps * slice / p.slices, s1 = steps * (slice + 1) / p.slices;
-
-  OP op;
-  OQ oq;
-  op.init(w, p.ldp);
-  // gated: the waves of the second half load u's weight
-  const int qh = GATED ? (w * OQ::I) / 16 : 0;
-  oq.init(w, (LAY == kFwd && GATED && qh) ? p.ldq[1] : LAY == kDw ? p.ldq[out] : p.ldq[0]);
-  auto issue = [&](int64_t t, int buf) {
-    const int seg = t >= ks;
-    const int64_t k0 = t < s1 ? (t - (seg ? ks : 0)) * BK : p.K;
-    if constexpr (LAY == kFwd) {
-      op.issue(p.p[0], p.ldp, m0, p.M, k0, p.K, lp + buf * OP::kBytes, w);
-      // gated: half 0 is g's columns, half 1 u's, both from n0 on
-      const int64_t c0 = GATED ? n0 - 128 * qh : n0;
-      oq.issue(p.q[qh], p.ldq[qh], c0, p.N, k0, p.K, lq + buf * OQ::kBytes, w);
-    } else if constexpr (LAY == kDx) {
-      op.issue(p.p[seg], p.ldp, m0, p.M, k0, p.K, lp + buf * OP::kBytes, w);
-      oq.issue(p.q[seg], p.ldq[seg], n0, p.N, k0, p.K, lq + buf * OQ::kBytes, w);
-    } else {
-      op.issue(p.p[0], p.ldp, m0, p.M, k0, p.K, lp + buf * OP::kBytes, w);
-      oq.issue(p.q[out], p.ldq[out], n0, p.N, k0, p.K, lq + buf * OQ::kBytes, w);
-    }
+  const int mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO;
+  const int nt = nt1 * p.outs;
+  const int total = mt * nt * p.slices;
+  const int ks = (p.K + BK - 1) / BK;  // steps per segment
+  const int steps = ks * p.segs;
+  struct Item {
+    int m0, n0, slice, out, s0, s1;
+  };
+  auto item_of = [&](int id) {
+    Item it;
+    int mi, ni;
+    tile_of(id, total, mt, nt, mi, ni, it.slice);
+    it.out = ni >= nt1;
+    it.m0 = mi * BM;
+    it.n0 = (ni - (it.out ? nt1 : 0)) * BNO;
+    it.s0 = uni((int)((int64_t)steps * it.slice / p.slices));
+    it.s1 = uni((int)((int64_t)steps * (it.slice + 1) / p.slices));
+    return it;
   };
 
+  // ---- the loading side: the stage under way
+  OP op;
+  OQ oq;
+  // gated: the waves of the second half load u's weight
+  const int qh = GATED ? (w * OQ::I) / 16 : 0;
+  op.init(w, p.ldp);
+  oq.init(w, p.ldq[qh]);
+  int load_id = blockIdx.x;
+  Item li = item_of(load_id);
+  int at = li.s0;  // its step
+  int left = 0;    // k left in its segment (0: past the last item)
+  i4v rp, rq;
+  auto place = [&](int seg) {  // at step `at`, in segment seg
+    const int k0 = (at - seg * ks) * BK;
+    left = p.K - k0;
+    if (LAY == kDx && p.segs == 2) oq.init(w, p.ldq[seg]);
+    const int qi = GATED ? qh : LAY == kDx ? seg : LAY == kDw ? li.out : 0;
+    op.start(p.p[LAY == kDx ? seg : 0], li.m0, p.M, k0, w);
+    // gated: half 0 is g's columns, half 1 u's, both from n0 on
+    oq.start(p.q[qi], GATED ? li.n0 - 128 * qh : li.n0, p.N, k0, w);
+  };
+  // The wait states cover a vector instruction's write of a scalar register
+  // that a load reads (5), which the compiler does not place around inline
+  // asm.
+  auto resources = [&]() {
+    rp = op.rsrc(left);
+    rq = oq.rsrc(left);
+    asm volatile("s_nop 4" : "+s"(rp), "+s"(rq));
+  };
+  auto next_stage = [&]() {
+    ++at;
+    left -= BK;
+    op.next();
+    oq.next();
+    if (at == li.s1) {
+      load_id += gridDim.x;
+      if (load_id < total) {
+        li = item_of(load_id);
+        at = li.s0;
+        place(at >= ks ? 1 : 0);
+      } else {
+        left = 0;
+        li.s1 = 0;  // never reached again
+      }
+    } else if (LAY == kDx && at == ks && li.s1) {
+      place(1);
+    } else if (!li.s1) {
+      left = 0;
+    }
+    resources();
+  };
+  auto set_one = [&](int j, int buf) {
+    if (j < OP::I) OP::place(j, lp + buf * OP::kBytes, w);
+    else OQ::place(j - OP::I, lq + buf * OQ::kBytes, w);
+  };
+  auto load_one = [&](int j) {
+    if (j < OP::I) op.load(j, rp, left);
+    else oq.load(j - OP::I, rq, left);
+  };
+
+  // ---- the computing side
   // LDS addresses of a lane's operands: KC one per half step (blocks are 16
   // rows, a constant apart), NC one per block of 16 columns (the swizzle
   // acts on the block's bits; half steps are a constant apart).
@@ -389,101 +530,152 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   }
 
   f4v acc[MB][NB];
-#pragma unroll
-  for (int a = 0; a < MB; ++a)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) acc[a][b] = f4v{0.f, 0.f, 0.f, 0.f};
-  s8v fp[2][MB], fq[2][NB];
-  auto read_half = [&](int kk, int buf) {
-    const uint32_t po = buf * OP::kBytes, qo = buf * OQ::kBytes;
+  auto clear = [&]() {
 #pragma unroll
     for (int a = 0; a < MB; ++a)
-      fp[kk][a] = PNC ? read_nc(pa[PNC ? a : 0] + po + kk * 32 * 256)
-                      : read_kc(pa[PNC ? 0 : kk] + po + a * 16 * 128);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      fq[kk][b] = QNC ? read_nc(qa[QNC ? b : 0] + qo + kk * 32 * 256)
-                      : read_kc(qa[QNC ? 0 : kk] + qo + b * 16 * 128);
-  };
-  auto mma_half = [&](int kk) {
-#pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) acc[a][b] = mfma16<DT>(fq[kk][b], fp[kk][a], acc[a][b]);
-  };
-
-  if (s0 < s1) {
-#pragma unroll
-    for (int j = 0; j < NS; ++j) issue(s0 + j, j);
-    stage_barrier<(NS - 1) * L>();
-    read_half(0, 0);
-    int buf = 0;
-    for (int64_t t = s0; t < s1; ++t) {
-      read_half(1, buf);
-      mma_half(0);
-      stage_barrier<(NS - 2) * L>();
-      issue(t + NS, buf);
-      buf = buf + 1 == NS ? 0 : buf + 1;
-      read_half(0, buf);
-      mma_half(1);
-    }
-    stage_barrier<0>();  // no load may land in LDS after the workgroup's end
-  }
-
-  // lane: row 16 a + i, columns 16 b + 4 g .. + 3
-#pragma unroll
-  for (int a = 0; a < MB; ++a) {
-    const int64_t m = m0 + (wm * MB + a) * 16 + i;
-    if (m >= p.M) continue;
-    if constexpr (GATED) {
-#pragma unroll
-      for (int b = 0; b < NB / 2; ++b) {
-        const int64_t n = n0 + (wn * (NB / 2) + b) * 16 + 4 * g;
-        if (n >= p.N) continue;
-        if (p.slices > 1) {
-          float* q = p.part + ((slice * p.M + m) * 2) * p.N + n;
-          *reinterpret_cast<f4v*>(q) = acc[a][b];
-          *reinterpret_cast<f4v*>(q + p.N) = acc[a][b + NB / 2];
-        } else {
-          finish_gated<DT>(p, m, n, acc[a][b], acc[a][b + NB / 2]);
-        }
-      }
-    } else {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int64_t n = n0 + (wn * NB + b) * 16 + 4 * g;
-        if (n >= p.N) continue;
-        if (p.slices > 1)
-          *reinterpret_cast<f4v*>(p.part + ((slice * p.outs + out) * p.M + m) * p.N + n) = acc[a][b];
-        else
-          finish_linear<DT>(p, out, m, n, acc[a][b]);
+        acc[a][b] = f4v{0.f, 0.f, 0.f, 0.f};
+        acc_settle(acc[a][b]);
+      }
+    acc_wait();
+  };
+  s8v fp[2][MB], fq[2][NB];
+  // operand r of a half step, in the order of their first use: Q, then P
+  auto read_one = [&](int r, int kk, int buf) {
+    const uint32_t po = buf * OP::kBytes, qo = buf * OQ::kBytes;
+    if (r < NB)
+      fq[kk][r] = QNC ? read_nc(qa[QNC ? r : 0] + qo + kk * 32 * 256)
+                      : read_kc(qa[QNC ? 0 : kk] + qo + r * 16 * 128);
+    else
+      fp[kk][r - NB] = PNC ? read_nc(pa[PNC ? r - NB : 0] + po + kk * 32 * 256)
+                           : read_kc(pa[PNC ? 0 : kk] + po + (r - NB) * 16 * 128);
+  };
+  // Half kk of a step on stage buffer `buf` (before: pbuf, next: nbuf).  The
+  // order is pinned product by product.
+  auto half = [&](auto KK, int pbuf, int buf, int nbuf) {
+    constexpr int kk = decltype(KK)::value;
+    static_for<N>([&](auto M) {
+      constexpr int m = decltype(M)::value;
+      if constexpr (kk == 0 && m == REL) {
+        stage_barrier<63, 0>();
+        next_stage();
+      }
+      if constexpr (kk == 1 && m == RDY) stage_barrier<CR + (NS - 2) * L, 15>();
+      constexpr int rs = kk == 0 ? m : m - RDY;  // reads r with r * RS / R == rs
+      static_for<(rs >= 0 && rs < RS ? ((rs + 1) * R + RS - 1) / RS - (rs * R + RS - 1) / RS : 0)>(
+          [&](auto I) {
+            read_one((rs * R + RS - 1) / RS + decltype(I)::value, 1 - kk, kk == 0 ? buf : nbuf);
+          });
+      // the loads at this position, or left over from the step before
+      constexpr int q = kk == 1 ? N + m : m < X ? 2 * N + m : m;
+      constexpr int j0 = before(q), jn = before(q + 1) - j0;
+      const int lbuf = kk == 0 && m < X ? pbuf : buf;
+      if constexpr (jn > 0) set_one(j0, lbuf);
+      mfma16<DT>(acc[m / NB][m % NB], fq[kk][m % NB], fp[kk][m / NB]);
+      if constexpr (jn > 0) load_one(j0);
+      static_for<(jn > 1 ? jn - 1 : 0)>([&](auto I) {
+        set_one(j0 + 1 + decltype(I)::value, lbuf);
+        asm volatile("s_nop 0" ::: "memory");
+        load_one(j0 + 1 + decltype(I)::value);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // Writes an item's outputs (or its partial sums) and clears the sums.
+  auto finish = [&](const Item& it) {
+    acc_wait();
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc_settle(acc[a][b]);
+#pragma unroll
+    for (int a = 0; a < MB; ++a) {
+      const int m = it.m0 + (wm * MB + a) * 16 + i;
+      constexpr int NO = GATED ? NB / 2 : NB;  // output blocks
+#pragma unroll
+      for (int b = 0; b < NO; b += 2) {
+        const F8 f = pair8(acc[a][b], acc[a][b + 1]);
+        const int n = it.n0 + (wn * NO + b + (g & 1)) * 16 + 8 * (g >> 1);
+        if constexpr (GATED) {
+          const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
+          if (m >= p.M || n >= p.N) continue;
+          if (p.slices > 1) {
+            float* q = p.part + (((int64_t)it.slice * p.M + m) * 2) * p.N + n;
+            store_part(q, f);
+            store_part(q + p.N, u);
+          } else {
+            finish_gated<DT>(p, m, n, f, u);
+          }
+        } else {
+          if (m >= p.M || n >= p.N) continue;
+          if (p.slices > 1)
+            store_part(p.part + ((int64_t)(it.slice * p.outs + it.out) * p.M + m) * p.N + n, f);
+          else
+            finish_linear<DT>(p, it.out, m, n, f);
+        }
       }
     }
-  }
-}
+    clear();
+  };
 
+  clear();
+  if (steps > 0) {
+    place(at >= ks ? 1 : 0);
+    resources();
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      if (j > 0) next_stage();
+#pragma unroll
+      for (int l = 0; l < (j < NS - 1 ? L : J1); ++l) {
+        set_one(l, j);
+        asm volatile("s_nop 0" ::: "memory");
+        load_one(l);
+      }
+    }
+    stage_barrier<(NS - 2) * L + J1, 0>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) read_one(r, 0, 0);
+  }
+  int pbuf = NS - 1, buf = 0;
+  for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    const Item it = item_of(id);
+    for (int t = it.s0; t < it.s1; ++t) {
+      const int nbuf = buf + 1 == NS ? 0 : buf + 1;
+      half(std::integral_constant<int, 0>{}, pbuf, buf, nbuf);
+      half(std::integral_constant<int, 1>{}, pbuf, buf, nbuf);
+      pbuf = buf;
+      buf = nbuf;
+    }
+    finish(it);
+  }
+  stage_barrier<0, 0>();  // no load may land in LDS after the workgroup's end
+}
 // Sums the slices' partials in slice order and finishes the outputs: one
-// thread per 4 columns of a row.
+// thread per 8 columns of a row.
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void k_lin_reduce(LinP p) {
-  const int64_t n4 = p.N / 4;
+  const int64_t n8 = p.N / 8, rows = (int64_t)p.M * p.outs;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= p.M * p.outs * n4) return;
-  const int64_t n = (id % n4) * 4, mo = id / n4;
+  if (id >= rows * n8) return;
+  const int n = (int)(id % n8) * 8;
+  const int64_t mo = id / n8;
+  F8 f = {};
   if constexpr (GATED) {
-    f4v gs = {0.f, 0.f, 0.f, 0.f}, us = gs;
+    F8 u = {};
+#pragma unroll 4
     for (int s = 0; s < p.slices; ++s) {
-      const float* q = p.part + ((s * p.M + mo) * 2) * p.N + n;
-      gs += *reinterpret_cast<const f4v*>(q);
-      us += *reinterpret_cast<const f4v*>(q + p.N);
+      const float* q = p.part + (((int64_t)s * p.M + mo) * 2) * p.N + n;
+      add_part(f, q);
+      add_part(u, q + p.N);
     }
-    finish_gated<DT>(p, mo, n, gs, us);
+    finish_gated<DT>(p, mo, n, f, u);
   } else {
-    f4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int s = 0; s < p.slices; ++s)
-      v += *reinterpret_cast<const f4v*>(p.part + ((int64_t)s * p.outs * p.M + mo) * p.N + n);
+      add_part(f, p.part + (s * rows + mo) * p.N + n);
     const int o = mo >= p.M;
-    finish_linear<DT>(p, o, mo - (o ? p.M : 0), n, v);
+    finish_linear<DT>(p, o, mo - (o ? p.M : 0), n, f);
   }
 }
 
@@ -581,29 +773,35 @@ size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int outs) {
   return pl.slices > 1 ? (size_t)pl.slices * M * N * outs * 4 : 0;
 }
 
+template <int DT, int LAY, bool GATED, int BM, int BN, int WM, int WN, int NS>
+void launch_tile(const LinP& p, int64_t items, hipStream_t s) {
+  constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes + Operand<LAY != kDx, BN>::kBytes);
+  constexpr int64_t most = kCus * (160 * 1024 / lds);  // workgroups that run at once
+  const dim3 grid((unsigned)(items < most ? items : most));
+  hipLaunchKernelGGL((k_lin<DT, LAY, GATED, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+}
+
 template <int DT, int LAY, bool GATED>
 hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
   const Plan pl = lin_plan(LAY, GATED, p.M, p.N, p.K, p.segs, p.outs);
   if (p.M == 0 || p.N == 0) return hipSuccess;
   p.slices = pl.slices;
   p.part = reinterpret_cast<float*>(ws);
-  const int64_t grid = tiles_of(pl.tile, GATED, p.M, p.N, p.outs) * pl.slices;
-  if (grid > 0x7fffffffLL) return hipErrorNotSupported;
-  const dim3 gr((unsigned)grid), th(256);
+  const int64_t items = tiles_of(pl.tile, GATED, p.M, p.N, p.outs) * pl.slices;
+  if (items > 0x7fffffffLL) return hipErrorNotSupported;
   constexpr int SB = GATED ? 256 : 128;
   if (pl.tile == 0) {
-    hipLaunchKernelGGL((k_lin<DT, LAY, GATED, 256, 256, 2, 2, 2>), gr, th, 0, s, p);
+    launch_tile<DT, LAY, GATED, 256, 256, 2, 2, 2>(p, items, s);
   } else if (pl.tile == 1) {
-    hipLaunchKernelGGL((k_lin<DT, LAY, GATED, 128, SB, 2, 2, 2>), gr, th, 0, s, p);
+    launch_tile<DT, LAY, GATED, 128, SB, 2, 2, 2>(p, items, s);
   } else {
-    if constexpr (LAY != kDw)
-      hipLaunchKernelGGL((k_lin<DT, LAY, GATED, 16, SB, 1, 4, 3>), gr, th, 0, s, p);
+    if constexpr (LAY != kDw) launch_tile<DT, LAY, GATED, 16, SB, 1, 4, 3>(p, items, s);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slices == 1) return e;
-  const int64_t n = (p.M * p.outs * (p.N / 4) + 255) / 256;
+  const int64_t n = ((int64_t)p.M * p.outs * (p.N / 8) + 255) / 256;
   if (n > 0x7fffffffLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), th, 0, s, p);
+  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -618,24 +816,24 @@ template <int DT>
 hipError_t fwd_dt(const LinearCall& c, hipStream_t s) {
   LinP p{};
   p.p[0] = c.x;
-  p.ldp = c.ldx;
+  p.ldp = (int)c.ldx;
   p.q[0] = c.w[0];
   p.q[1] = c.w[1];
-  p.ldq[0] = c.ldw[0];
-  p.ldq[1] = c.ldw[1];
-  p.M = c.T;
-  p.N = c.d_out;
-  p.K = c.d_in;
+  p.ldq[0] = (int)c.ldw[0];
+  p.ldq[1] = (int)c.ldw[1];
+  p.M = (int)c.T;
+  p.N = (int)c.d_out;
+  p.K = (int)c.d_in;
   p.segs = p.outs = 1;
   p.act = c.act;
   p.bias = c.bias;
   p.res = c.res;
-  p.ldr = c.ldr;
+  p.ldr = (int)c.ldr;
   p.y[0] = c.y;
-  p.ldy[0] = c.ldy;
+  p.ldy[0] = (int)c.ldy;
   for (int i = 0; i < 2; ++i) {
     p.pre[i] = c.pre[i];
-    p.ldpre[i] = c.ldpre[i];
+    p.ldpre[i] = (int)c.ldpre[i];
   }
   return c.gated ? launch_lin<DT, kFwd, true>(p, c.ws, s) : launch_lin<DT, kFwd, false>(p, c.ws, s);
 }
@@ -696,34 +894,34 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
     LinP p{};
     p.p[0] = d[0];
     p.p[1] = d[1];
-    p.ldp = ldd;
+    p.ldp = (int)ldd;
     for (int i = 0; i < 2; ++i) {
       p.q[i] = c.w[i];
-      p.ldq[i] = c.ldw[i];
+      p.ldq[i] = (int)c.ldw[i];
     }
-    p.M = c.T;
-    p.N = c.d_in;
-    p.K = c.d_out;
+    p.M = (int)c.T;
+    p.N = (int)c.d_in;
+    p.K = (int)c.d_out;
     p.segs = c.gated ? 2 : 1;
     p.outs = 1;
     p.y[0] = c.dx;
-    p.ldy[0] = c.lddx;
+    p.ldy[0] = (int)c.lddx;
     e = launch_lin<DT, kDx, false>(p, ws, s);
     if (e != hipSuccess) return e;
   }
   if (c.dw[0]) {
     LinP p{};
     p.p[0] = c.x;
-    p.ldp = c.ldx;
+    p.ldp = (int)c.ldx;
     for (int i = 0; i < 2; ++i) {
       p.q[i] = d[i];
-      p.ldq[i] = ldd;
+      p.ldq[i] = (int)ldd;
       p.y[i] = c.dw[i];
-      p.ldy[i] = c.lddw[i];
+      p.ldy[i] = (int)c.lddw[i];
     }
-    p.M = c.d_in;
-    p.N = c.d_out;
-    p.K = c.T;
+    p.M = (int)c.d_in;
+    p.N = (int)c.d_out;
+    p.K = (int)c.T;
     p.segs = 1;
     p.outs = c.gated ? 2 : 1;
     e = launch_lin<DT, kDw, false>(p, ws, s);

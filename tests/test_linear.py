@@ -116,7 +116,8 @@ def test_gated_backward_exact(dims, dtype):
 
 
 @pytest.mark.parametrize("shape", [(2000, 4096, 1024), (1024, 1024, 4096), (260, 2056, 11008),
-                                   (1, 11008, 4096), (8, 4096, 14336), (48, 14336, 4096)], ids=str)
+                                   (1, 11008, 4096), (8, 4096, 14336), (48, 14336, 4096),
+                                   (2500, 4104, 4168), (4100, 200, 8200)], ids=str)
 def test_layer_sizes_exact(shape):
     t, d_in, d_out = shape
     dtype = torch.bfloat16
@@ -309,6 +310,20 @@ def test_strided_operands_among_nan(t, dims):
     same(dwt, x.double().T @ dy.double())
     same(db, dy.double().sum(0))
     assert frame_kept(dxb) and frame_kept(dwb)
+
+
+@pytest.mark.parametrize("t", [5, 150])
+def test_gate_and_up_of_different_strides(t):
+    dt = torch.bfloat16
+    x, dh = ints((t, 200), -2, 2, dt, 76), ints((t, 136), -1, 1, dt, 77)
+    wg, wu = framed(ints((200, 136), -2, 2, dt, 78), 16)[0], framed(ints((200, 136), -1, 1, dt, 79), 40)[0]
+    g, u = ints((t, 136), -2, 2, dt, 74), framed(ints((t, 136), -2, 2, dt, 75))[0]
+    same(sa.gated_linear(x, wg, wu, act="relu"),
+         (x.double() @ wg.double()).clamp(min=0) * (x.double() @ wu.double()))
+    dx, _, _ = sa.gated_linear_backward(dh, x, wg, wu, g, u, act="relu", with_dw=False)
+    dg = dh.double() * u.double() * (g > 0).double()
+    du = dh.double() * g.double().clamp(min=0)
+    same(dx, dg @ wg.double().T + du @ wu.double().T)
 
 
 @pytest.mark.parametrize("t", [6, 200])
