@@ -157,6 +157,7 @@ constexpr int kHalfTile = BK * 128 * 2;  // bytes of an NC half tile
 __device__ __forceinline__ int swz_kc(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 __device__ __forceinline__ int swz_nc(int k) { return 2 * ((k & 3) + 4 * ((k >> 3) & 1)); }
 
+#define SA_INLINE __attribute__((always_inline))
 #define SA_LDS(T, a) ((const __attribute__((address_space(3))) T*)(uintptr_t)(a))
 
 __device__ __forceinline__ s8v read_kc(uint32_t a) { return *SA_LDS(s8v, a); }
@@ -168,6 +169,10 @@ __device__ __forceinline__ s8v read_nc(uint32_t a) {
 }
 
 enum Layout { kFwd = 0, kDx = 1, kDw = 2 };
+// Epilogues, each compiled by itself (the general one needs registers that
+// the plain one's K loop would have to give up): the sums as they are (gated:
+// h alone), plus the residual, or everything.
+enum Epilogue { kPlain = 0, kResidual = 1, kGeneral = 2 };
 
 struct LinP {
   const uint16_t* p[2];  // row operand (per K segment)
@@ -218,6 +223,36 @@ __device__ __forceinline__ void store8(uint16_t* p, const F8& f) {
   *reinterpret_cast<u16x8*>(p) = o;
 }
 
+// Eight values of the element type.
+template <int DT>
+__device__ __forceinline__ F8 widen8(u32x4 r) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = r[i];
+    f.v[2 * i] = to_f<DT>((uint16_t)(u & 0xffffu));
+    f.v[2 * i + 1] = to_f<DT>((uint16_t)(u >> 16));
+  }
+  return f;
+}
+template <int DT>
+__device__ __forceinline__ u32x4 round8(const F8& f) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = (uint32_t)from_f<DT>(f.v[2 * i]) | (uint32_t)from_f<DT>(f.v[2 * i + 1]) << 16;
+  return o;
+}
+
+// A matrix's rows from m0 on as a buffer resource: rows past the last lie
+// out of range (stores are dropped, loads read zeros).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* m, int64_t ld, int m0,
+                                                            int rows, int N) {
+  const uint64_t base = uni(m + (int64_t)m0 * ld);
+  const int bytes = uni((rows - 1) * (int)ld * 2 + N * 2);
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+}
+
 // Eight outputs of row m from column n on (n a multiple of 8 below N).
 template <int DT>
 __device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, int n, F8 f) {
@@ -236,7 +271,7 @@ __device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) f.v[i] += r.v[i];
   }
-  store8<DT>(p.y[o] + m * p.ldy[o] + n, f);
+  store8<DT>((o ? p.y[1] : p.y[0]) + m * (o ? p.ldy[1] : p.ldy[0]) + n, f);
 }
 template <int DT>
 __device__ __forceinline__ void finish_gated(const LinP& p, int64_t m, int n, F8 g, const F8& u) {
@@ -319,8 +354,8 @@ struct Operand {
   __device__ __forceinline__ void init(int w, int ldv) {
     const int lane = lane_id();
     ld = ldv;
-#pragma unroll
-    for (int j = 0; j < I; ++j) {
+    static_for<I>([&](auto J) {
+      constexpr int j = decltype(J)::value;
       const int id = w * I + j;
       if constexpr (NC) {
         const int k = (id % 16) * 4 + lane / 16;
@@ -330,16 +365,16 @@ struct Operand {
         const int r = id * 8 + lane / 8;
         const int c = (lane % 8) ^ swz_kc(r);
         voff[j] = (uint32_t)(r * ld * 2 + c * 16);
-        if (j < 2) kc[j] = 8 * c;
+        if constexpr (j < 2) kc[j] = 8 * c;
       }
-    }
+    });
     if constexpr (!NC && I == 1) kc[1] = kc[0];
   }
   // The tile that starts at row (column) r0 of `rows`, at k0 of matrix m.
   __device__ __forceinline__ void start(const uint16_t* m, int r0, int rows, int k0, int w) {
     if constexpr (NC) {
       const int c0 = r0 + 128 * ((w * I) / 16);  // the wave's loads lie in one half tile
-      cols = uni(rows - c0 > 0 ? rows - c0 : 0);
+      cols = uni(rows - c0 > 0 ? rows - c0 : -(1 << 29));  // none left: no bytes at any step
       base = uni(m + (int64_t)k0 * ld + c0);
       step = (int64_t)BK * 2 * ld;
     } else {
@@ -349,13 +384,16 @@ struct Operand {
       step = BK * 2;
     }
   }
-  // The step's resource: the bytes from its base to the operand's end.
+  // The step's resource: the bytes from its base to the operand's end, with
+  // `left` k to come (0 or less: none).
   __device__ __forceinline__ i4v rsrc(int left) const {
     int bytes;
-    if constexpr (NC)
-      bytes = (left > 0 && cols > 0) ? (((left < BK ? left : BK) - 1) * ld + cols) * 2 : 0;
-    else
+    if constexpr (NC) {
+      bytes = (((left < BK ? left : BK) - 1) * ld + cols) * 2;  // cols <= ld
+      bytes = bytes > 0 ? bytes : 0;
+    } else {
       bytes = left > 0 ? span + left * 2 : 0;
+    }
     return i4v{uni((int)(uint32_t)base), uni((int)((uint32_t)(base >> 32) & 0xffffu)), uni(bytes),
                0x00020000};
   }
@@ -389,7 +427,7 @@ struct Operand {
 // arrived.  Loads past the last item read zeros, so counts never change.
 // gfx950 at 256 x 256: 64 KB per stage, two stages, one wave per SIMD with
 // 256 sums in accumulation registers.
-template <int DT, int LAY, bool GATED, int BM, int BN, int WM, int WN, int NS>
+template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   constexpr bool PNC = LAY == kDw, QNC = LAY != kDx;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
@@ -413,6 +451,11 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
     for (int j = 0; j < L; ++j) c += (REL + j * SPAN / L) < q;
     return c;
   };
+  // product of half 0 that carries piece i of the move to the next stage:
+  // after the loads left over from the step before, up to 6 before REL
+  constexpr auto piece = [](int i) constexpr {
+    return REL - X > 12 ? X + i * (REL - 6 - X) / 6 : X;
+  };
   constexpr int J1 = before(2 * N);       // loads within the step; the others in the next
   constexpr int CR = before(N + RDY);     // loads issued when stage t + 1 must have arrived
 
@@ -428,7 +471,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   struct Item {
     int m0, n0, slice, out, s0, s1;
   };
-  auto item_of = [&](int id) {
+  auto item_of = [&](int id) SA_INLINE {
     Item it;
     int mi, ni;
     tile_of(id, total, mt, nt, mi, ni, it.slice);
@@ -446,56 +489,53 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   // gated: the waves of the second half load u's weight
   const int qh = GATED ? (w * OQ::I) / 16 : 0;
   op.init(w, p.ldp);
-  oq.init(w, p.ldq[qh]);
+  oq.init(w, qh ? p.ldq[1] : p.ldq[0]);
   int load_id = blockIdx.x;
   Item li = item_of(load_id);
   int at = li.s0;  // its step
-  int left = 0;    // k left in its segment (0: past the last item)
+  int stop = 0;    // the step at which the segment or the item ends
+  int left = 0;    // k left in the segment (0 or less: past the last item)
   i4v rp, rq;
-  auto place = [&](int seg) {  // at step `at`, in segment seg
+  auto place = [&]() SA_INLINE {  // at step `at` of item li
+    const int seg = at >= ks;
     const int k0 = (at - seg * ks) * BK;
-    left = p.K - k0;
-    if (LAY == kDx && p.segs == 2) oq.init(w, p.ldq[seg]);
-    const int qi = GATED ? qh : LAY == kDx ? seg : LAY == kDw ? li.out : 0;
-    op.start(p.p[LAY == kDx ? seg : 0], li.m0, p.M, k0, w);
+    left = uni(p.K - k0);
+    stop = uni(!seg && ks < li.s1 ? ks : li.s1);
+    if (LAY == kDx && p.segs == 2) oq.init(w, seg ? p.ldq[1] : p.ldq[0]);
+    const bool second = GATED ? qh : LAY == kDx ? seg : LAY == kDw ? li.out : 0;
+    op.start(LAY == kDx && seg ? p.p[1] : p.p[0], li.m0, p.M, k0, w);
     // gated: half 0 is g's columns, half 1 u's, both from n0 on
-    oq.start(p.q[qi], GATED ? li.n0 - 128 * qh : li.n0, p.N, k0, w);
+    oq.start(second ? p.q[1] : p.q[0], GATED ? li.n0 - 128 * qh : li.n0, p.N, k0, w);
   };
-  // The wait states cover a vector instruction's write of a scalar register
-  // that a load reads (5), which the compiler does not place around inline
-  // asm.
-  auto resources = [&]() {
-    rp = op.rsrc(left);
-    rq = oq.rsrc(left);
-    asm volatile("s_nop 4" : "+s"(rp), "+s"(rq));
-  };
-  auto next_stage = [&]() {
+  // The move to the next stage, in pieces that the K loop spreads over its
+  // products.  The resources' scalar registers must be written 5 instructions
+  // before a load reads them (the compiler places no wait states around
+  // inline asm); settle() fixes them there.
+  auto advance = [&]() SA_INLINE {
     ++at;
     left -= BK;
-    op.next();
-    oq.next();
-    if (at == li.s1) {
-      load_id += gridDim.x;
-      if (load_id < total) {
-        li = item_of(load_id);
-        at = li.s0;
-        place(at >= ks ? 1 : 0);
-      } else {
-        left = 0;
-        li.s1 = 0;  // never reached again
-      }
-    } else if (LAY == kDx && at == ks && li.s1) {
-      place(1);
-    } else if (!li.s1) {
-      left = 0;
-    }
-    resources();
   };
-  auto set_one = [&](int j, int buf) {
+  auto turn = [&]() SA_INLINE {
+    if (__builtin_expect(at == stop, 0)) {
+      if (at == li.s1) {
+        load_id += gridDim.x;
+        if (load_id < total) {
+          li = item_of(load_id);
+          at = li.s0;
+        } else {
+          left = 0;
+          stop = -1;  // never reached
+        }
+      }
+      if (stop >= 0) place();
+    }
+  };
+  auto settle = [&]() SA_INLINE { asm volatile("" : "+s"(rp), "+s"(rq)); };
+  auto set_one = [&](int j, int buf) SA_INLINE {
     if (j < OP::I) OP::place(j, lp + buf * OP::kBytes, w);
     else OQ::place(j - OP::I, lq + buf * OQ::kBytes, w);
   };
-  auto load_one = [&](int j) {
+  auto load_one = [&](int j) SA_INLINE {
     if (j < OP::I) op.load(j, rp, left);
     else oq.load(j - OP::I, rq, left);
   };
@@ -505,10 +545,10 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   // rows, a constant apart), NC one per block of 16 columns (the swizzle
   // acts on the block's bits; half steps are a constant apart).
   const int g = lane / 16, i = lane % 16;
-  auto kc_addr = [&](int row0, int kk) {
+  auto kc_addr = [&](int row0, int kk) SA_INLINE {
     return (uint32_t)((row0 + i) * 128 + (((4 * kk + g) ^ swz_kc(i)) * 16));
   };
-  auto nc_addr = [&](int blk) {  // block of 16 columns
+  auto nc_addr = [&](int blk) SA_INLINE {  // block of 16 columns
     const int s = (i >> 2) + 4 * (g & 1);
     return (uint32_t)((blk >> 3) * kHalfTile + (8 * g + (i >> 2)) * 256 +
                       ((2 * ((blk & 7) ^ s) + ((i >> 1) & 1)) * 16) + (i & 1) * 8);
@@ -530,7 +570,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   }
 
   f4v acc[MB][NB];
-  auto clear = [&]() {
+  auto clear = [&]() SA_INLINE {
 #pragma unroll
     for (int a = 0; a < MB; ++a)
 #pragma unroll
@@ -542,7 +582,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   };
   s8v fp[2][MB], fq[2][NB];
   // operand r of a half step, in the order of their first use: Q, then P
-  auto read_one = [&](int r, int kk, int buf) {
+  auto read_one = [&](int r, int kk, int buf) SA_INLINE {
     const uint32_t po = buf * OP::kBytes, qo = buf * OQ::kBytes;
     if (r < NB)
       fq[kk][r] = QNC ? read_nc(qa[QNC ? r : 0] + qo + kk * 32 * 256)
@@ -553,13 +593,22 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   };
   // Half kk of a step on stage buffer `buf` (before: pbuf, next: nbuf).  The
   // order is pinned product by product.
-  auto half = [&](auto KK, int pbuf, int buf, int nbuf) {
+  auto half = [&](auto KK, int pbuf, int buf, int nbuf) SA_INLINE {
     constexpr int kk = decltype(KK)::value;
     static_for<N>([&](auto M) {
       constexpr int m = decltype(M)::value;
-      if constexpr (kk == 0 && m == REL) {
-        stage_barrier<63, 0>();
-        next_stage();
+      if constexpr (kk == 0 && m == REL) stage_barrier<63, 0>();
+      if constexpr (kk == 0) {
+        if constexpr (m == piece(0)) advance();
+        if constexpr (m == piece(1)) op.next();
+        if constexpr (m == piece(2)) oq.next();
+        if constexpr (m == piece(3)) turn();
+        if constexpr (m == piece(4)) rp = op.rsrc(left);
+        if constexpr (m == piece(5)) rq = oq.rsrc(left);
+        if constexpr (m == piece(6)) {
+          settle();
+          if constexpr (REL - piece(6) < 5) asm volatile("s_nop 4" ::: "memory");
+        }
       }
       if constexpr (kk == 1 && m == RDY) stage_barrier<CR + (NS - 2) * L, 15>();
       constexpr int rs = kk == 0 ? m : m - RDY;  // reads r with r * RS / R == rs
@@ -583,16 +632,21 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
     });
   };
   // Writes an item's outputs (or its partial sums) and clears the sums.
-  auto finish = [&](const Item& it) {
-    acc_wait();
+  // Lane: row 16 a + i, 8 columns from 16 (b + g % 2) + 8 (g / 2) on of every
+  // pair (b, b + 1) of output blocks.
+  constexpr int NO = GATED ? NB / 2 : NB;  // output blocks
+  // Row by row, as few registers are free beside the next item's operands: a
+  // spill's reload would wait for the stores before it.
+  auto take_row = [&](int a) SA_INLINE {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int a = 0; a < MB; ++a)
-#pragma unroll
-      for (int b = 0; b < NB; ++b) acc_settle(acc[a][b]);
-#pragma unroll
-    for (int a = 0; a < MB; ++a) {
+    for (int b = 0; b < NB; ++b) acc_settle(acc[a][b]);
+  };
+  auto finish_parts = [&](const Item& it) SA_INLINE {
+    static_for<MB>([&](auto A) {
+      constexpr int a = decltype(A)::value;
+      take_row(a);
       const int m = it.m0 + (wm * MB + a) * 16 + i;
-      constexpr int NO = GATED ? NB / 2 : NB;  // output blocks
 #pragma unroll
       for (int b = 0; b < NO; b += 2) {
         const F8 f = pair8(acc[a][b], acc[a][b + 1]);
@@ -600,42 +654,136 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
         if constexpr (GATED) {
           const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
           if (m >= p.M || n >= p.N) continue;
-          if (p.slices > 1) {
-            float* q = p.part + (((int64_t)it.slice * p.M + m) * 2) * p.N + n;
-            store_part(q, f);
-            store_part(q + p.N, u);
-          } else {
-            finish_gated<DT>(p, m, n, f, u);
-          }
+          float* q = p.part + (((int64_t)it.slice * p.M + m) * 2) * p.N + n;
+          store_part(q, f);
+          store_part(q + p.N, u);
         } else {
           if (m >= p.M || n >= p.N) continue;
-          if (p.slices > 1)
-            store_part(p.part + ((int64_t)(it.slice * p.outs + it.out) * p.M + m) * p.N + n, f);
-          else
-            finish_linear<DT>(p, it.out, m, n, f);
+          store_part(p.part + ((int64_t)(it.slice * p.outs + it.out) * p.M + m) * p.N + n, f);
         }
       }
+    });
+  };
+  auto finish_rows = [&](const Item& it) SA_INLINE {
+    constexpr int mode = EPI;
+    const int rows = p.M - it.m0 < BM ? p.M - it.m0 : BM;
+    const int ldy = it.out ? p.ldy[1] : p.ldy[0];
+    const auto yr = rows_rsrc(it.out ? p.y[1] : p.y[0], ldy, it.m0, rows, p.N);
+    const int row = wm * MB * 16 + i;
+    uint32_t col[NO / 2];  // byte offset of the lane's columns, or out of range
+#pragma unroll
+    for (int b = 0; b < NO / 2; ++b) {
+      const int n = it.n0 + (wn * NO + 2 * b + (g & 1)) * 16 + 8 * (g >> 1);
+      col[b] = n < p.N ? (uint32_t)n * 2 : kOutOfRange;
     }
+    const uint32_t yo = (uint32_t)(row * ldy * 2);
+    const int ystep = 16 * ldy * 2;  // added to the lane's offset: the range check covers that
+    if constexpr (GATED) {
+      const bool gu = mode == kGeneral && p.pre[0];
+      const auto gr = rows_rsrc(gu ? p.pre[0] : p.y[0], gu ? p.ldpre[0] : 0, it.m0, gu ? rows : 1, gu ? p.N : 0);
+      const auto ur = rows_rsrc(gu ? p.pre[1] : p.y[0], gu ? p.ldpre[1] : 0, it.m0, gu ? rows : 1, gu ? p.N : 0);
+      static_for<MB>([&](auto A) {
+        constexpr int a = decltype(A)::value;
+        take_row(a);
+#pragma unroll
+        for (int b = 0; b < NO; b += 2) {
+          F8 f = pair8(acc[a][b], acc[a][b + 1]);
+          const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
+          if constexpr (mode == kGeneral) {
+            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), gr,
+                (uint32_t)((row + 16 * a) * p.ldpre[0] * 2) + col[b / 2], 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(u), ur,
+                (uint32_t)((row + 16 * a) * p.ldpre[1] * 2) + col[b / 2], 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f.v[e] = act_value(p.act, f.v[e]) * u.v[e];
+          __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
+        }
+      });
+    } else {
+      const bool hr = mode >= kResidual && p.res, hp = mode == kGeneral && p.pre[0], hb = mode == kGeneral && p.bias;
+      const auto rr = rows_rsrc(hr ? p.res : p.y[0], hr ? p.ldr : 0, it.m0, hr ? rows : 1, hr ? p.N : 0);
+      const auto pr = rows_rsrc(hp ? p.pre[0] : p.y[0], hp ? p.ldpre[0] : 0, it.m0, hp ? rows : 1, hp ? p.N : 0);
+      const auto br = __builtin_amdgcn_make_buffer_rsrc((void*)uni(hb ? p.bias : p.y[0]), 0,
+                                                        uni(hb ? p.N * 2 : 0), 0x00020000);
+      const uint32_t ro = hr ? (uint32_t)(row * p.ldr * 2) : 0;
+      const int rstep = hr ? 16 * p.ldr * 2 : 0;
+      const uint32_t po = hp ? (uint32_t)(row * p.ldpre[0] * 2) : 0;
+      const int pstep = hp ? 16 * p.ldpre[0] * 2 : 0;
+      u32x4 rv[2][NO / 2], bv[NO / 2];  // the residual's rows, one row of blocks ahead
+      if constexpr (mode == kGeneral) {
+#pragma unroll
+        for (int b = 0; b < NO / 2; ++b) bv[b] = __builtin_amdgcn_raw_buffer_load_b128(br, col[b], 0, 0);
+      }
+      if constexpr (mode >= kResidual) {
+#pragma unroll
+        for (int b = 0; b < NO / 2; ++b)
+          rv[0][b] = __builtin_amdgcn_raw_buffer_load_b128(rr, ro + col[b], 0, 0);
+      }
+      static_for<MB>([&](auto A) {
+        constexpr int a = decltype(A)::value;
+        take_row(a);
+        if constexpr (mode >= kResidual) {
+          if constexpr (a + 1 < MB) {
+#pragma unroll
+            for (int b = 0; b < NO / 2; ++b)
+              rv[(a + 1) & 1][b] =
+                  __builtin_amdgcn_raw_buffer_load_b128(rr, ro + (uint32_t)((a + 1) * rstep) + col[b], 0, 0);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < NO; b += 2) {
+          F8 f = pair8(acc[a][b], acc[a][b + 1]);
+          if constexpr (mode == kGeneral) {
+            const F8 bias = widen8<DT>(bv[b / 2]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
+            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
+            if (p.act != SA_ACT_NONE) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f.v[e] = act_value(p.act, f.v[e]);
+            }
+          }
+          if constexpr (mode >= kResidual) {
+            const F8 r = widen8<DT>(rv[a & 1][b / 2]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] += r.v[e];
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
+        }
+      });
+    }
+  };
+  auto finish = [&](const Item& it) SA_INLINE {
+    acc_wait();
+    if (p.slices > 1) finish_parts(it);
+    else finish_rows(it);
     clear();
   };
 
   clear();
   if (steps > 0) {
-    place(at >= ks ? 1 : 0);
-    resources();
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      if (j > 0) next_stage();
-#pragma unroll
-      for (int l = 0; l < (j < NS - 1 ? L : J1); ++l) {
-        set_one(l, j);
-        asm volatile("s_nop 0" ::: "memory");
-        load_one(l);
+    place();
+    static_for<NS>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      if constexpr (j > 0) {
+        advance();
+        op.next();
+        oq.next();
+        turn();
       }
-    }
+      rp = op.rsrc(left);
+      rq = oq.rsrc(left);
+      settle();
+      asm volatile("s_nop 4" ::: "memory");
+      static_for<(j < NS - 1 ? L : J1)>([&](auto I) {
+        set_one(decltype(I)::value, j);
+        asm volatile("s_nop 0" ::: "memory");
+        load_one(decltype(I)::value);
+      });
+    });
     stage_barrier<(NS - 2) * L + J1, 0>();
-#pragma unroll
-    for (int r = 0; r < R; ++r) read_one(r, 0, 0);
+    static_for<R>([&](auto I) { read_one(decltype(I)::value, 0, 0); });
   }
   int pbuf = NS - 1, buf = 0;
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
@@ -773,12 +921,24 @@ size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int outs) {
   return pl.slices > 1 ? (size_t)pl.slices * M * N * outs * 4 : 0;
 }
 
-template <int DT, int LAY, bool GATED, int BM, int BN, int WM, int WN, int NS>
+template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const LinP& p, int64_t items, hipStream_t s) {
   constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes + Operand<LAY != kDx, BN>::kBytes);
   constexpr int64_t most = kCus * (160 * 1024 / lds);  // workgroups that run at once
   const dim3 grid((unsigned)(items < most ? items : most));
-  hipLaunchKernelGGL((k_lin<DT, LAY, GATED, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+  hipLaunchKernelGGL((k_lin<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+}
+
+template <int DT, int LAY, bool GATED, int EPI>
+void launch_plan(const LinP& p, const Plan& pl, int64_t items, hipStream_t s) {
+  constexpr int SB = GATED ? 256 : 128;
+  if (pl.tile == 0) {
+    launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, items, s);
+  } else if (pl.tile == 1) {
+    launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, 2>(p, items, s);
+  } else {
+    if constexpr (LAY != kDw) launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 3>(p, items, s);
+  }
 }
 
 template <int DT, int LAY, bool GATED>
@@ -789,13 +949,15 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
   p.part = reinterpret_cast<float*>(ws);
   const int64_t items = tiles_of(pl.tile, GATED, p.M, p.N, p.outs) * pl.slices;
   if (items > 0x7fffffffLL) return hipErrorNotSupported;
-  constexpr int SB = GATED ? 256 : 128;
-  if (pl.tile == 0) {
-    launch_tile<DT, LAY, GATED, 256, 256, 2, 2, 2>(p, items, s);
-  } else if (pl.tile == 1) {
-    launch_tile<DT, LAY, GATED, 128, SB, 2, 2, 2>(p, items, s);
-  } else {
-    if constexpr (LAY != kDw) launch_tile<DT, LAY, GATED, 16, SB, 1, 4, 3>(p, items, s);
+  // split products finish in k_lin_reduce
+  if (LAY != kFwd || pl.slices > 1 ||
+      (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res)) {
+    launch_plan<DT, LAY, GATED, kPlain>(p, pl, items, s);
+  } else if constexpr (LAY == kFwd) {
+    if (!GATED && !p.bias && !p.pre[0] && p.act == SA_ACT_NONE)
+      launch_plan<DT, LAY, GATED, GATED ? kGeneral : kResidual>(p, pl, items, s);
+    else
+      launch_plan<DT, LAY, GATED, kGeneral>(p, pl, items, s);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slices == 1) return e;
