@@ -734,6 +734,35 @@ int sa_gemv_plan(int op, int64_t d_out, int64_t d_in, int64_t batch, int cus, in
 int sa_gemm_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int n, int m, int cus,
                  int* engine, int* tile_rows, int* tile_cols, int64_t* tiles);
 
+/* The products of the dense linear layers, as named by sa_linear_plan. */
+enum {
+  SA_LINEAR_FORWARD = 0,  /* dense_linear */
+  SA_LINEAR_GATED = 1,    /* gated_linear */
+  SA_LINEAR_DX = 2,       /* dense_linear_backward, dx */
+  SA_LINEAR_DW = 3,       /* dense_linear_backward, dwt */
+  SA_LINEAR_GATED_DX = 4, /* gated_linear_backward, dx */
+  SA_LINEAR_GATED_DW = 5  /* gated_linear_backward, dwgt and dwut */
+};
+/*
+ * The decomposition a product of the dense linear layers would use, under the
+ * current sa_set_linear_tuning choices.  It computes nothing on the GPU.
+ * Outputs (HOST pointers, none NULL): output tile rows x cols (gated: cols of
+ * g and as many of u), slices of the summed index, items = tiles x slices.
+ * Returns SA_ERR_INVALID_ARG for an unknown op, sizes the calls refuse or a
+ * NULL output.
+ */
+int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols,
+                   int* slices, int64_t* items);
+/*
+ * Process-wide choices of the dense linear layers, for tuning sweeps and
+ * cross-checks: tile -1 = automatic, or 0..4 (256 x 256, 128 x 128, and 64,
+ * 32 or 16 rows x 128; weight gradients take 0 and 1 only); slices 0 =
+ * automatic, or up to 64.  Workspace sizes follow the choices: query them
+ * again.  Every choice computes the same result up to fp32 summation order.
+ * Returns SA_ERR_INVALID_ARG for other values.  Not thread-safe.
+ */
+int sa_set_linear_tuning(int tile, int slices);
+
 #ifdef __cplusplus
 }
 #endif

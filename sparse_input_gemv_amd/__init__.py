@@ -33,7 +33,7 @@ __all__ = [
     "masked_gemv",
     "dense_gemv", "masked_swiglu_down", "weight_col_norms", "nm_act_spmm", "nm_shared_spmm",
     "dense_gemm", "dense_linear", "dense_linear_backward", "gated_linear", "gated_linear_backward",
-    "ACTIVATIONS", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
+    "ACTIVATIONS", "set_linear_tuning", "linear_plan", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
     "workspace_zero_bytes", "scratch", "MAX_BATCH",
 ]
 
@@ -97,6 +97,8 @@ _SIGNATURES = {
                                      _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                      _i64, _vp, _sz, _vp]),
     "gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sa_set_linear_tuning": (_i32, [_i32, _i32]),
+    "sa_linear_plan": (_i32, [_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "sa_set_gemm_tuning": (_i32, [_i32, _i32, _i32]),
     "sa_gemv_tiling_info": (_i32, [_i32, _vp, _vp, _vp]),
     "sa_gemv_plan": (_i32, [_i32, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
@@ -891,6 +893,26 @@ def gemm_plan(op: str, T: int, d_in: int, d_out: int, n: int = 0, m: int = 0, cu
                               *[ctypes.addressof(o) for o in (e, r, c, t)]), "sa_gemm_plan")
     return {"engine": {1: "staged", 2: "pipelined", 3: "wide"}[e.value], "tile_rows": r.value,
             "tile_cols": c.value, "tiles": t.value}
+
+
+def set_linear_tuning(tile: int = -1, slices: int = 0) -> None:
+    """Tile and split of the dense linear layers' products (see the C
+    declaration); -1 and 0 are the automatic choices."""
+    _check(lib().sa_set_linear_tuning(tile, slices), "sa_set_linear_tuning")
+    _lin_ws_bytes.cache_clear()
+
+
+LINEAR_OPS = {"forward": 0, "gated": 1, "dx": 2, "dw": 3, "gated_dx": 4, "gated_dw": 5}
+
+
+def linear_plan(op: str, T: int, d_in: int, d_out: int):
+    """The decomposition a product of the dense linear layers would use: a
+    dict with ``tile_rows``, ``tile_cols``, ``slices`` and ``items``."""
+    r, c, sl = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    it = ctypes.c_int64()
+    _check(lib().sa_linear_plan(LINEAR_OPS[op], T, d_in, d_out,
+                                *[ctypes.addressof(o) for o in (r, c, sl, it)]), "sa_linear_plan")
+    return {"tile_rows": r.value, "tile_cols": c.value, "slices": sl.value, "items": it.value}
 
 
 def gemv_tiling_info(i: int):

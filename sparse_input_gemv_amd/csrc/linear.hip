@@ -98,6 +98,31 @@ __device__ __forceinline__ float act_slope(int act, float v) {
   }
 }
 
+// Both, sharing their transcendental part.
+__device__ __forceinline__ void act_both(int act, float v, float& f, float& df) {
+  switch (act) {
+    case SA_ACT_SILU: {
+      const float s = sigmoid(v);
+      f = v * s;
+      df = s * (1.f + v * (1.f - s));
+      return;
+    }
+    case SA_ACT_GELU: {
+      const float c = 0.5f * erfcf(-0.70710678118654752f * v);
+      f = v * c;
+      df = c + v * 0.3989422804014327f * __expf(-0.5f * v * v);
+      return;
+    }
+    case SA_ACT_GELU_TANH: {
+      const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
+      f = v * s;
+      df = s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
+      return;
+    }
+    default: f = act_value(act, v); df = act_slope(act, v);
+  }
+}
+
 // ---- global memory to LDS ------------------------------------------------------
 // Buffer loads straight into LDS: lane l's 16 bytes land at the LDS base +
 // 16 l; a lane whose offset is not below the resource's size reads zeros.
@@ -799,39 +824,66 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   }
   stage_barrier<0, 0>();  // no load may land in LDS after the workgroup's end
 }
-// Sums the slices' partials in slice order and finishes the outputs: one
-// thread per 8 columns of a row.
+// Sums the slices' partials and finishes the outputs, 8 columns of a row per
+// thread.  With few rows there are few threads and each waits for its loads
+// in turn, so `groups` threads share an output: group k adds slices k, k +
+// groups, ..., and the groups' sums are added in order.
 template <int DT, bool GATED>
-__global__ __launch_bounds__(256) void k_lin_reduce(LinP p) {
+__global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups) {
+  __shared__ float part[256][GATED ? 17 : 9];  // odd rows: lanes in different banks
   const int64_t n8 = p.N / 8, rows = (int64_t)p.M * p.outs;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= rows * n8) return;
-  const int n = (int)(id % n8) * 8;
-  const int64_t mo = id / n8;
-  F8 f = {};
-  if constexpr (GATED) {
-    F8 u = {};
+  const int per = 256 / groups;
+  const int o = (int)threadIdx.x % per, k = (int)threadIdx.x / per;
+  const int64_t id = (int64_t)blockIdx.x * per + o;
+  const bool in = id < rows * n8;
+  const int n = in ? (int)(id % n8) * 8 : 0;
+  const int64_t mo = in ? id / n8 : 0;
+  F8 f = {}, u = {};
+  if (in) {
+    if constexpr (GATED) {
 #pragma unroll 4
-    for (int s = 0; s < p.slices; ++s) {
-      const float* q = p.part + (((int64_t)s * p.M + mo) * 2) * p.N + n;
-      add_part(f, q);
-      add_part(u, q + p.N);
+      for (int s = k; s < p.slices; s += groups) {
+        const float* q = p.part + (((int64_t)s * p.M + mo) * 2) * p.N + n;
+        add_part(f, q);
+        add_part(u, q + p.N);
+      }
+    } else {
+#pragma unroll 4
+      for (int s = k; s < p.slices; s += groups) add_part(f, p.part + (s * rows + mo) * p.N + n);
     }
+  }
+  if (groups > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      part[threadIdx.x][e] = f.v[e];
+      if constexpr (GATED) part[threadIdx.x][8 + e] = u.v[e];
+    }
+    __syncthreads();
+    if (k > 0) return;
+    for (int j = 1; j < groups; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        f.v[e] += part[j * per + o][e];
+        if constexpr (GATED) u.v[e] += part[j * per + o][8 + e];
+      }
+    }
+  }
+  if (!in) return;
+  if constexpr (GATED) {
     finish_gated<DT>(p, mo, n, f, u);
   } else {
-#pragma unroll 8
-    for (int s = 0; s < p.slices; ++s)
-      add_part(f, p.part + (s * rows + mo) * p.N + n);
-    const int o = mo >= p.M;
-    finish_linear<DT>(p, o, mo - (o ? p.M : 0), n, f);
+    const int out = mo >= p.M;
+    finish_linear<DT>(p, out, mo - (out ? p.M : 0), n, f);
   }
 }
 
 // ---- the gradients' elementwise half --------------------------------------------
 // d = dy * act'(pre) (linear) or dg = dh u act'(g), du = dh act(g) (gated),
 // rounded to the element type for the products, and per strip of rows the
-// fp32 column sums of the unrounded d (dbias).  A thread owns 8 columns of a
-// strip.  Bound by memory: reads 2 (3) values and writes 1 (2) per entry.
+// fp32 column sums of the unrounded d (dbias).  Bound by memory: reads 2 (3)
+// values and writes 1 (2) per entry.  A wave takes 512 columns (8 per lane:
+// 16-byte accesses) of a quarter of a strip, kDactRows rows at a time so that
+// their loads are in flight together; the four waves' sums meet in LDS.
 struct DactP {
   const uint16_t *dy, *a, *b;  // a: pre or g; b: u
   int64_t lddy, lda, ldb;
@@ -840,80 +892,120 @@ struct DactP {
   int64_t T, N, strip;
   int act;
 };
+constexpr int kDactRows = 4;
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void k_lin_dact(DactP p) {
-  const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (n >= p.N) return;
-  const int64_t t0 = blockIdx.y * p.strip;
-  const int64_t t1 = t0 + p.strip < p.T ? t0 + p.strip : p.T;
+  __shared__ float part[4][64][9];  // 9: the lanes' rows in different banks
+  const int lane = lane_id(), w = (int)threadIdx.x / kWave;
+  const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 8;
+  const bool in = n < p.N;
+  const int64_t quarter = (p.strip + 3) / 4;
+  const int64_t s0 = blockIdx.y * p.strip, send = s0 + p.strip < p.T ? s0 + p.strip : p.T;
+  const int64_t t0 = s0 + w * quarter, t1 = t0 + quarter < send ? t0 + quarter : send;
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    const u16x8 dy = *reinterpret_cast<const u16x8*>(p.dy + t * p.lddy + n);
-    u16x8 a = {}, b = {}, o0, o1;
-    if (p.a) a = *reinterpret_cast<const u16x8*>(p.a + t * p.lda + n);
-    if constexpr (GATED) b = *reinterpret_cast<const u16x8*>(p.b + t * p.ldb + n);
+  if (in) {
+    for (int64_t t = t0; t < t1; t += kDactRows) {
+      u16x8 dy[kDactRows], a[kDactRows], b[kDactRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = to_f<DT>(dy[e]), z = to_f<DT>(a[e]);
-      if constexpr (GATED) {
-        o0[e] = from_f<DT>(v * to_f<DT>(b[e]) * act_slope(p.act, z));
-        o1[e] = from_f<DT>(v * act_value(p.act, z));
-      } else {
-        const float d = p.a ? v * act_slope(p.act, z) : v;
-        sum[e] += d;
-        o0[e] = from_f<DT>(d);
+      for (int r = 0; r < kDactRows; ++r) {
+        const int64_t tr = t + r < t1 ? t + r : t1 - 1;
+        dy[r] = *reinterpret_cast<const u16x8*>(p.dy + tr * p.lddy + n);
+        if (p.a) a[r] = *reinterpret_cast<const u16x8*>(p.a + tr * p.lda + n);
+        if constexpr (GATED) b[r] = *reinterpret_cast<const u16x8*>(p.b + tr * p.ldb + n);
+      }
+#pragma unroll
+      for (int r = 0; r < kDactRows; ++r) {
+        if (t + r >= t1) break;
+        u16x8 o0, o1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = to_f<DT>(dy[r][e]);
+          if constexpr (GATED) {
+            float f, df;
+            act_both(p.act, to_f<DT>(a[r][e]), f, df);
+            o0[e] = from_f<DT>(v * to_f<DT>(b[r][e]) * df);
+            o1[e] = from_f<DT>(v * f);
+          } else {
+            const float d = p.a ? v * act_slope(p.act, to_f<DT>(a[r][e])) : v;
+            sum[e] += d;
+            o0[e] = from_f<DT>(d);
+          }
+        }
+        if (p.d0) *reinterpret_cast<u16x8*>(p.d0 + (t + r) * p.N + n) = o0;
+        if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + (t + r) * p.N + n) = o1;
       }
     }
-    if (p.d0) *reinterpret_cast<u16x8*>(p.d0 + t * p.N + n) = o0;
-    if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + t * p.N + n) = o1;
   }
   if constexpr (!GATED) {
-    if (p.sums) {
-      float* s = p.sums + blockIdx.y * p.N + n;
-      *reinterpret_cast<f4v*>(s) = f4v{sum[0], sum[1], sum[2], sum[3]};
-      *reinterpret_cast<f4v*>(s + 4) = f4v{sum[4], sum[5], sum[6], sum[7]};
+    if (!p.sums) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[w][lane][e] = sum[e];
+    __syncthreads();
+    // 512 columns by 256 threads, the waves' sums in order
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = h * 256 + (int)threadIdx.x;
+      const int64_t col = (int64_t)blockIdx.x * 512 + c;
+      if (col < p.N)
+        p.sums[blockIdx.y * p.N + col] = (part[0][c / 8][c % 8] + part[1][c / 8][c % 8]) +
+                                         (part[2][c / 8][c % 8] + part[3][c / 8][c % 8]);
     }
   }
 }
-// dbias[n] = the strips' sums, in strip order.
+// dbias[n]: the strips' sums.  64 columns per workgroup; wave w adds strips
+// w, w + 4, ..., then the waves' four sums are added in order.
 template <int DT>
 __global__ __launch_bounds__(256) void k_lin_colsum(const float* sums, int64_t strips, int64_t N,
                                                     uint16_t* out) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float part[4][64];
+  const int lane = lane_id(), w = (int)threadIdx.x / kWave;
+  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
-  for (int64_t i = 0; i < strips; ++i) s += sums[i * N + n];
-  out[n] = from_f<DT>(s);
+  if (n < N) {
+#pragma unroll 8
+    for (int64_t i = w; i < strips; i += 4) s += sums[i * N + n];
+  }
+  part[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && n < N)
+    out[n] = from_f<DT>((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
 }
 
 // ---- plans -----------------------------------------------------------------------
 constexpr int64_t kCus = 256;  // compute units of an MI355X
 
+// The compiled tiles: rows and columns (of g and of u each: 128 at most),
+// and LDS stages.
+constexpr int kTiles = 5;
+constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16}, kTileN[kTiles] = {256, 128, 128, 128, 128};
+int g_lin_tile = -1, g_lin_slices = 0;  // overrides (linear_set_tuning)
+
 struct Plan {
-  int tile;    // index into the compiled tiles (0: 256 x 256, 1: 128 x 128, 2: 16 rows)
-  int slices;
+  int tile, slices;
+  int64_t items;
 };
-constexpr int kTileM[3] = {256, 128, 16}, kTileN[3] = {256, 128, 128};
 
 int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
-  // the gated small tiles hold 128 columns of g and of u
   const int64_t bn = gated ? 128 : kTileN[tile];
   return ((M + kTileM[tile] - 1) / kTileM[tile]) * ((N + bn - 1) / bn) * outs;
 }
 
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  Plan pl{0, 1};
+  Plan pl{0, 1, 0};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
-  if (lay != kDw && M <= 16) pl.tile = 2;
+  if (lay != kDw && M <= 64) pl.tile = M <= 16 ? 4 : M <= 32 ? 3 : 2;
   else if (tiles_of(0, gated, M, N, outs) < kCus) pl.tile = 1;
+  if (g_lin_tile >= 0 && (lay != kDw || g_lin_tile < 2)) pl.tile = g_lin_tile;
   const int64_t tiles = tiles_of(pl.tile, gated, M, N, outs);
-  const int64_t want = pl.tile == 0 ? 1 : (2 * kCus) / (tiles > 0 ? tiles : 1);
-  int64_t s = want < 1 ? 1 : want;
+  int64_t s = 1;
+  if (pl.tile > 0 && tiles > 0) s = (2 * kCus) / tiles;
   if (s > steps / 2) s = steps / 2;
+  if (g_lin_slices > 0) s = g_lin_slices < steps ? g_lin_slices : steps;
   if (s > 64) s = 64;
   pl.slices = s < 1 ? 1 : (int)s;
+  pl.items = tiles * pl.slices;
   return pl;
 }
 
@@ -929,47 +1021,46 @@ void launch_tile(const LinP& p, int64_t items, hipStream_t s) {
   hipLaunchKernelGGL((k_lin<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
 }
 
-template <int DT, int LAY, bool GATED, int EPI>
-void launch_plan(const LinP& p, const Plan& pl, int64_t items, hipStream_t s) {
-  constexpr int SB = GATED ? 256 : 128;
-  if (pl.tile == 0) {
-    launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, items, s);
-  } else if (pl.tile == 1) {
-    launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, 2>(p, items, s);
-  } else {
-    if constexpr (LAY != kDw) launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 3>(p, items, s);
-  }
-}
-
 template <int DT, int LAY, bool GATED>
 hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
-  const Plan pl = lin_plan(LAY, GATED, p.M, p.N, p.K, p.segs, p.outs);
   if (p.M == 0 || p.N == 0) return hipSuccess;
+  const Plan pl = lin_plan(LAY, GATED, p.M, p.N, p.K, p.segs, p.outs);
+  if (pl.items > 0x7fffffffLL) return hipErrorNotSupported;
   p.slices = pl.slices;
   p.part = reinterpret_cast<float*>(ws);
-  const int64_t items = tiles_of(pl.tile, GATED, p.M, p.N, p.outs) * pl.slices;
-  if (items > 0x7fffffffLL) return hipErrorNotSupported;
-  // split products finish in k_lin_reduce
-  if (LAY != kFwd || pl.slices > 1 ||
-      (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res)) {
-    launch_plan<DT, LAY, GATED, kPlain>(p, pl, items, s);
-  } else if constexpr (LAY == kFwd) {
-    if (!GATED && !p.bias && !p.pre[0] && p.act == SA_ACT_NONE)
-      launch_plan<DT, LAY, GATED, GATED ? kGeneral : kResidual>(p, pl, items, s);
+  constexpr int SB = GATED ? 256 : 128;
+  constexpr int EPI = LAY == kFwd ? kGeneral : kPlain;
+  if (pl.tile == 0) {
+    // split products finish in k_lin_reduce
+    if (LAY != kFwd || pl.slices > 1 ||
+        (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res))
+      launch_tile<DT, LAY, GATED, kPlain, 256, 256, 2, 2, 2>(p, pl.items, s);
+    else if (!GATED && !p.bias && !p.pre[0] && p.act == SA_ACT_NONE)
+      launch_tile<DT, LAY, GATED, LAY == kFwd && !GATED ? kResidual : EPI, 256, 256, 2, 2, 2>(p, pl.items, s);
     else
-      launch_plan<DT, LAY, GATED, kGeneral>(p, pl, items, s);
+      launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, pl.items, s);
+  } else if (pl.tile == 1) {
+    launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, GATED ? 3 : 2>(p, pl.items, s);
+  } else if constexpr (LAY != kDw) {
+    if (pl.tile == 2) launch_tile<DT, LAY, GATED, EPI, 64, SB, 1, 4, 3>(p, pl.items, s);
+    else if (pl.tile == 3) launch_tile<DT, LAY, GATED, EPI, 32, SB, 1, 4, GATED ? 4 : 3>(p, pl.items, s);
+    else launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 4>(p, pl.items, s);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slices == 1) return e;
-  const int64_t n = ((int64_t)p.M * p.outs * (p.N / 8) + 255) / 256;
+  const int64_t octets = (int64_t)p.M * p.outs * (p.N / 8);
+  int groups = 1;  // up to 8 threads per output while there is less than a workgroup per CU
+  while (groups < 8 && groups * 2 <= pl.slices && octets * groups < kCus * 256) groups *= 2;
+  const int64_t n = (octets * groups + 255) / 256;
   if (n > 0x7fffffffLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups);
   return hipGetLastError();
 }
 
-// Rows per strip of the elementwise kernel: 64, more where that would give
-// over 1024 strips.
-int64_t strip_rows(int64_t T) { return T <= 64 * 1024 ? 64 : (T + 1023) / 1024; }
+// Rows per strip of the elementwise kernel (a workgroup's): 16 for small T
+// (a latency-bound kernel wants workgroups), 64 from 2048 rows on (fewer
+// partial sums), more where that would give over 1024 strips.
+int64_t strip_rows(int64_t T) { return T < 2048 ? 16 : T <= 64 * 1024 ? 64 : (T + 1023) / 1024; }
 int64_t strips_of(int64_t T) { return (T + strip_rows(T) - 1) / strip_rows(T); }
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -1038,7 +1129,7 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
     a.N = c.d_out;
     a.strip = strip_rows(c.T);
     a.act = c.act;
-    const dim3 gr((unsigned)((c.d_out / 8 + 255) / 256), (unsigned)strips);
+    const dim3 gr((unsigned)((c.d_out + 511) / 512), (unsigned)strips);
     if (c.gated)
       hipLaunchKernelGGL((k_lin_dact<DT, true>), gr, dim3(256), 0, s, a);
     else
@@ -1047,7 +1138,7 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (c.dbias) {
-    hipLaunchKernelGGL((k_lin_colsum<DT>), dim3((unsigned)((c.d_out + 255) / 256)), dim3(256), 0, s,
+    hipLaunchKernelGGL((k_lin_colsum<DT>), dim3((unsigned)((c.d_out + 63) / 64)), dim3(256), 0, s,
                        sums, strips, c.d_out, c.dbias);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1106,6 +1197,32 @@ size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int6
   const size_t px = part_bytes(lin_plan(kDx, false, T, d_in, d_out, n, 1), T, d_in, 1);
   const size_t pw = part_bytes(lin_plan(kDw, false, d_in, d_out, T, 1, n), d_in, d_out, n);
   return b + (px > pw ? px : pw);
+}
+
+int linear_set_tuning(int tile, int slices) {
+  if (tile < -1 || tile >= kTiles || slices < 0 || slices > 64) return 1;
+  g_lin_tile = tile;
+  g_lin_slices = slices;
+  return 0;
+}
+
+int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* slices,
+                int64_t* items) {
+  Plan pl;
+  switch (op) {
+    case SA_LINEAR_FORWARD: pl = lin_plan(kFwd, false, T, d_out, d_in, 1, 1); break;
+    case SA_LINEAR_GATED: pl = lin_plan(kFwd, true, T, d_out, d_in, 1, 1); break;
+    case SA_LINEAR_DX: pl = lin_plan(kDx, false, T, d_in, d_out, 1, 1); break;
+    case SA_LINEAR_DW: pl = lin_plan(kDw, false, d_in, d_out, T, 1, 1); break;
+    case SA_LINEAR_GATED_DX: pl = lin_plan(kDx, false, T, d_in, d_out, 2, 1); break;
+    case SA_LINEAR_GATED_DW: pl = lin_plan(kDw, false, d_in, d_out, T, 1, 2); break;
+    default: return 1;
+  }
+  *rows = kTileM[pl.tile];
+  *cols = op == SA_LINEAR_GATED ? 128 : kTileN[pl.tile];
+  *slices = pl.slices;
+  *items = pl.items;
+  return 0;
 }
 
 hipError_t launch_linear(const LinearCall& c, hipStream_t s) {
