@@ -747,21 +747,25 @@ enum {
  * The decomposition a product of the dense linear layers would use, under the
  * current sa_set_linear_tuning choices.  It computes nothing on the GPU.
  * Outputs (HOST pointers, none NULL): output tile rows x cols (gated: cols of
- * g and as many of u), slices of the summed index, items = tiles x slices.
+ * g and as many of u); tiles; split = the workgroups that share all tiles'
+ * steps of the summed index evenly (their partial sums go through the
+ * workspace), 0 where workgroups take whole tiles.
  * Returns SA_ERR_INVALID_ARG for an unknown op, sizes the calls refuse or a
  * NULL output.
  */
 int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols,
-                   int* slices, int64_t* items);
+                   int* split, int64_t* tiles);
 /*
  * Process-wide choices of the dense linear layers, for tuning sweeps and
  * cross-checks: tile -1 = automatic, or 0..4 (256 x 256, 128 x 128, and 64,
- * 32 or 16 rows x 128; weight gradients take 0 and 1 only); slices 0 =
- * automatic, or up to 64.  Workspace sizes follow the choices: query them
- * again.  Every choice computes the same result up to fp32 summation order.
+ * 32 or 16 rows x 128; weight gradients take 0 and 1 only); split -1 =
+ * automatic, 0 = whole tiles, or that many shares (up to 512, rounded down to
+ * a power of two).  Workspace
+ * sizes follow the choices: query them again.  Every choice computes the
+ * same result up to fp32 summation order.
  * Returns SA_ERR_INVALID_ARG for other values.  Not thread-safe.
  */
-int sa_set_linear_tuning(int tile, int slices);
+int sa_set_linear_tuning(int tile, int split);
 
 #ifdef __cplusplus
 }

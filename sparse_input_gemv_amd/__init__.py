@@ -895,10 +895,10 @@ def gemm_plan(op: str, T: int, d_in: int, d_out: int, n: int = 0, m: int = 0, cu
             "tile_cols": c.value, "tiles": t.value}
 
 
-def set_linear_tuning(tile: int = -1, slices: int = 0) -> None:
+def set_linear_tuning(tile: int = -1, split: int = -1) -> None:
     """Tile and split of the dense linear layers' products (see the C
-    declaration); -1 and 0 are the automatic choices."""
-    _check(lib().sa_set_linear_tuning(tile, slices), "sa_set_linear_tuning")
+    declaration); -1 is the automatic choice."""
+    _check(lib().sa_set_linear_tuning(tile, split), "sa_set_linear_tuning")
     _lin_ws_bytes.cache_clear()
 
 
@@ -907,12 +907,13 @@ LINEAR_OPS = {"forward": 0, "gated": 1, "dx": 2, "dw": 3, "gated_dx": 4, "gated_
 
 def linear_plan(op: str, T: int, d_in: int, d_out: int):
     """The decomposition a product of the dense linear layers would use: a
-    dict with ``tile_rows``, ``tile_cols``, ``slices`` and ``items``."""
+    dict with ``tile_rows``, ``tile_cols``, ``split`` (workgroups that share
+    all tiles' steps, 0: whole tiles) and ``tiles``."""
     r, c, sl = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
     it = ctypes.c_int64()
     _check(lib().sa_linear_plan(LINEAR_OPS[op], T, d_in, d_out,
                                 *[ctypes.addressof(o) for o in (r, c, sl, it)]), "sa_linear_plan")
-    return {"tile_rows": r.value, "tile_cols": c.value, "slices": sl.value, "items": it.value}
+    return {"tile_rows": r.value, "tile_cols": c.value, "split": sl.value, "tiles": it.value}
 
 
 def gemv_tiling_info(i: int):

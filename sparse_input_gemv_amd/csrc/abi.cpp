@@ -889,22 +889,22 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
   return run_linear(c, true, fn, stream);
 }
 
-int sa_set_linear_tuning(int tile, int slices) {
+int sa_set_linear_tuning(int tile, int split) {
   sa::clear_error();
-  if (sa::linear_set_tuning(tile, slices) != 0) {
-    sa::set_error("sa_set_linear_tuning: tile must be -1..4 and slices 0..64");
+  if (sa::linear_set_tuning(tile, split) != 0) {
+    sa::set_error("sa_set_linear_tuning: tile must be -1..4 and split -1..512");
     return SA_ERR_INVALID_ARG;
   }
   return SA_OK;
 }
 
 int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols,
-                   int* slices, int64_t* items) {
+                   int* split, int64_t* tiles) {
   sa::clear_error();
   int st = sa::check_linear_sizes("sa_linear_plan", SA_F16, T, d_in, d_out, 0);
   if (st != SA_OK) return SA_ERR_INVALID_ARG;
-  if (!rows || !cols || !slices || !items ||
-      sa::linear_plan(op, T, d_in, d_out, rows, cols, slices, items) != 0) {
+  if (!rows || !cols || !split || !tiles ||
+      sa::linear_plan(op, T, d_in, d_out, rows, cols, split, tiles) != 0) {
     sa::set_error("sa_linear_plan: unknown op or a NULL output");
     return SA_ERR_INVALID_ARG;
   }

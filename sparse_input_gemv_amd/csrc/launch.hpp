@@ -182,9 +182,9 @@ struct LinearCall {
 size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out);
 size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
                                        bool dbias);
-int linear_set_tuning(int tile, int slices);
-int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* slices,
-                int64_t* items);
+int linear_set_tuning(int tile, int split);
+int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* split,
+                int64_t* tiles);
 hipError_t launch_linear(const LinearCall& c, hipStream_t s);
 hipError_t launch_linear_backward(const LinearCall& c, hipStream_t s);
 

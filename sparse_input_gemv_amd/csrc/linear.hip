@@ -206,8 +206,9 @@ struct LinP {
   int M, N, K;           // K per segment
   int segs;              // K segments (dx of the gated pair: 2)
   int outs;              // outputs side by side (dW of the gated pair: 2)
-  int slices;            // split of the K steps over workgroups
-  float* part;           // [slices][M][N * (gated ? 2 : 1)] when slices > 1
+  int split;             // 0: whole tiles; else the workgroups (a power of two) that
+                         // share all tiles' steps
+  float* part;           // split: [slot][outs * M][N * (gated ? 2 : 1)]
   // epilogue
   int act;
   const uint16_t* bias;
@@ -339,25 +340,31 @@ __device__ __forceinline__ void add_part(F8& f, const float* p) {
   }
 }
 
-// The tile of workgroup b: the hardware deals workgroups over the 8 XCDs in
-// turn, so each XCD takes a contiguous run of a grouped order (kGroupM row
-// tiles across all column tiles); tiles that run together on one XCD share
-// their operands in its L2.  A bijection.
+// The hardware deals workgroups over the 8 XCDs in turn; this gives each XCD a
+// contiguous run of [0, total).  A bijection.
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t total) {
+  const uint32_t x = b % 8, per = total / 8, rem = total % 8;
+  return x * per + (x < rem ? x : rem) + b / 8;
+}
+// Whole tiles: an XCD's run goes through kGroupM row tiles across all column
+// tiles, so tiles that run together on one XCD share operands in its L2.
 constexpr int kGroupM = 4;
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t total, uint32_t mt, uint32_t nt, int& m,
-                                        int& n, int& slice) {
-  const uint32_t x = b % 8, l = b / 8;
-  const uint32_t per = total / 8, rem = total % 8;
-  uint32_t t = x * per + (x < rem ? x : rem) + l;
-  const uint32_t tiles = mt * nt;
-  slice = uni((int)(t / tiles));
-  t -= (uint32_t)slice * tiles;
+                                        int& n) {
+  const uint32_t t = xcd_run(b, total);
   const uint32_t gsz = kGroupM * nt;
   const uint32_t grp = t / gsz, first = grp * kGroupM;
   const uint32_t gm = (mt - first < kGroupM) ? mt - first : kGroupM;
   const uint32_t in = t - grp * gsz;
   n = uni((int)(in / gm));
   m = uni((int)(first + in - (uint32_t)n * gm));
+}
+// Split tiles: the steps of all tiles in a row (tile t's at t * steps ...)
+// are dealt evenly: share i of G (a power of two) holds positions [i TS / G,
+// (i + 1) TS / G).  share_of(P): the share that holds position P.  TS * G is
+// at most 2^31.
+__host__ __device__ __forceinline__ int share_of(uint32_t P, uint32_t TS, uint32_t G) {
+  return (int)(((P + 1) * G - 1) / TS);
 }
 
 // One operand's tile: R rows (KC) or columns (NC) by 64 k, loaded by four
@@ -436,8 +443,9 @@ struct Operand {
 };
 
 // C tiles of BM x BN (gated: BN / 2 columns of g and of u), 256 threads as
-// WM x WN waves.  A workgroup takes the (tile, slice) items blockIdx.x,
-// blockIdx.x + gridDim.x, ... and runs one K loop over all their steps: the
+// WM x WN waves.  A workgroup takes tiles blockIdx.x, blockIdx.x + gridDim.x,
+// ..., or, where tiles are few, an even share of all tiles' steps, whose
+// partial sums k_lin_reduce adds.  It runs one K loop over all its items: the
 // loads of the next item's first steps are under way while an item's outputs
 // are written.
 //
@@ -490,21 +498,38 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   constexpr int BNO = GATED ? BN / 2 : BN;  // output columns per tile
   const int mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO;
   const int nt = nt1 * p.outs;
-  const int total = mt * nt * p.slices;
+  const int tiles = mt * nt;
   const int ks = (p.K + BK - 1) / BK;  // steps per segment
   const int steps = ks * p.segs;
+  // A cursor goes over the workgroup's items: a tile's number, or (split) a
+  // position among all tiles' steps, up to `end`.
+  const bool split = p.split > 0;
+  const int share = split ? (int)xcd_run(blockIdx.x, gridDim.x) : 0;
+  const int lg = split ? __builtin_ctz(p.split) : 0;
+  const int begin = split ? (int)((uint32_t)share * (uint32_t)(tiles * steps) >> lg) : (int)blockIdx.x;
+  const int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)(tiles * steps) >> lg) : tiles;
   struct Item {
-    int m0, n0, slice, out, s0, s1;
+    int m0, n0, out, s0, s1, next;
   };
-  auto item_of = [&](int id) SA_INLINE {
+  auto item_at = [&](int cur) SA_INLINE {
     Item it;
     int mi, ni;
-    tile_of(id, total, mt, nt, mi, ni, it.slice);
+    if (split) {
+      const int t = uni((int)((uint32_t)cur / (uint32_t)steps));
+      ni = mt == 1 ? t : uni((int)((uint32_t)t / (uint32_t)mt));
+      mi = t - ni * mt;
+      it.s0 = cur - t * steps;
+      it.s1 = uni(it.s0 + end - cur < steps ? it.s0 + end - cur : steps);
+      it.next = cur + it.s1 - it.s0;
+    } else {
+      tile_of(cur, tiles, mt, nt, mi, ni);
+      it.s0 = 0;
+      it.s1 = steps;
+      it.next = cur + (int)gridDim.x;
+    }
     it.out = ni >= nt1;
     it.m0 = mi * BM;
     it.n0 = (ni - (it.out ? nt1 : 0)) * BNO;
-    it.s0 = uni((int)((int64_t)steps * it.slice / p.slices));
-    it.s1 = uni((int)((int64_t)steps * (it.slice + 1) / p.slices));
     return it;
   };
 
@@ -515,8 +540,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   const int qh = GATED ? (w * OQ::I) / 16 : 0;
   op.init(w, p.ldp);
   oq.init(w, qh ? p.ldq[1] : p.ldq[0]);
-  int load_id = blockIdx.x;
-  Item li = item_of(load_id);
+  Item li = item_at(begin);
   int at = li.s0;  // its step
   int stop = 0;    // the step at which the segment or the item ends
   int left = 0;    // k left in the segment (0 or less: past the last item)
@@ -543,9 +567,8 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   auto turn = [&]() SA_INLINE {
     if (__builtin_expect(at == stop, 0)) {
       if (at == li.s1) {
-        load_id += gridDim.x;
-        if (load_id < total) {
-          li = item_of(load_id);
+        if (li.next < end) {
+          li = item_at(li.next);
           at = li.s0;
         } else {
           left = 0;
@@ -668,6 +691,9 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
     for (int b = 0; b < NB; ++b) acc_settle(acc[a][b]);
   };
   auto finish_parts = [&](const Item& it) SA_INLINE {
+    // slot: how many shares before this one hold part of the tile
+    const int t = (it.n0 / BNO + (it.out ? nt1 : 0)) * mt + it.m0 / BM;
+    const int slot = it.s0 == 0 ? 0 : uni(share - share_of(t * steps, tiles * steps, p.split));
     static_for<MB>([&](auto A) {
       constexpr int a = decltype(A)::value;
       take_row(a);
@@ -679,12 +705,12 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
         if constexpr (GATED) {
           const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
           if (m >= p.M || n >= p.N) continue;
-          float* q = p.part + (((int64_t)it.slice * p.M + m) * 2) * p.N + n;
+          float* q = p.part + (((int64_t)slot * p.M + m) * 2) * p.N + n;
           store_part(q, f);
           store_part(q + p.N, u);
         } else {
           if (m >= p.M || n >= p.N) continue;
-          store_part(p.part + ((int64_t)(it.slice * p.outs + it.out) * p.M + m) * p.N + n, f);
+          store_part(p.part + ((int64_t)(slot * p.outs + it.out) * p.M + m) * p.N + n, f);
         }
       }
     });
@@ -781,7 +807,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   };
   auto finish = [&](const Item& it) SA_INLINE {
     acc_wait();
-    if (p.slices > 1) finish_parts(it);
+    if (split) finish_parts(it);
     else finish_rows(it);
     clear();
   };
@@ -811,8 +837,9 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
     static_for<R>([&](auto I) { read_one(decltype(I)::value, 0, 0); });
   }
   int pbuf = NS - 1, buf = 0;
-  for (int id = blockIdx.x; id < total; id += gridDim.x) {
-    const Item it = item_of(id);
+  for (int cur = begin; cur < end;) {
+    const Item it = item_at(cur);
+    cur = it.next;
     for (int t = it.s0; t < it.s1; ++t) {
       const int nbuf = buf + 1 == NS ? 0 : buf + 1;
       half(std::integral_constant<int, 0>{}, pbuf, buf, nbuf);
@@ -824,32 +851,38 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   }
   stage_barrier<0, 0>();  // no load may land in LDS after the workgroup's end
 }
-// Sums the slices' partials and finishes the outputs, 8 columns of a row per
-// thread.  With few rows there are few threads and each waits for its loads
-// in turn, so `groups` threads share an output: group k adds slices k, k +
-// groups, ..., and the groups' sums are added in order.
+// Sums the shares' partials of each tile (2^lbm x 2^lbn outputs) and finishes the outputs, 8
+// columns of a row per thread.  With few rows there are few threads and each
+// waits for its loads in turn, so `groups` threads share an output: group k
+// adds slots k, k + groups, ..., and the groups' sums are added in order.
 template <int DT, bool GATED>
-__global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups) {
+__global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm, int lbn) {
   __shared__ float part[256][GATED ? 17 : 9];  // odd rows: lanes in different banks
-  const int64_t n8 = p.N / 8, rows = (int64_t)p.M * p.outs;
+  const uint32_t n8 = p.N / 8, rows = p.M * p.outs;  // few tiles: 32 bits hold their sizes
   const int per = 256 / groups;
   const int o = (int)threadIdx.x % per, k = (int)threadIdx.x / per;
-  const int64_t id = (int64_t)blockIdx.x * per + o;
+  const uint32_t id = blockIdx.x * per + o;
   const bool in = id < rows * n8;
-  const int n = in ? (int)(id % n8) * 8 : 0;
-  const int64_t mo = in ? id / n8 : 0;
+  const uint32_t mo = in ? id / n8 : 0;
+  const int n = in ? (int)(id - mo * n8) * 8 : 0;
+  const int out = mo >= (uint32_t)p.M;
+  const int row = (int)(mo - (out ? p.M : 0));
   F8 f = {}, u = {};
   if (in) {
+    const int mt = (p.M + (1 << lbm) - 1) >> lbm, nt1 = (p.N + (1 << lbn) - 1) >> lbn;
+    const uint32_t steps = (uint32_t)((p.K + BK - 1) / BK * p.segs), TS = mt * nt1 * p.outs * steps;
+    const uint32_t at = (uint32_t)(((n >> lbn) + out * nt1) * mt + (row >> lbm)) * steps;
+    const int slots = share_of(at + steps - 1, TS, p.split) - share_of(at, TS, p.split) + 1;
     if constexpr (GATED) {
 #pragma unroll 4
-      for (int s = k; s < p.slices; s += groups) {
+      for (int s = k; s < slots; s += groups) {
         const float* q = p.part + (((int64_t)s * p.M + mo) * 2) * p.N + n;
         add_part(f, q);
         add_part(u, q + p.N);
       }
     } else {
 #pragma unroll 4
-      for (int s = k; s < p.slices; s += groups) add_part(f, p.part + (s * rows + mo) * p.N + n);
+      for (int s = k; s < slots; s += groups) add_part(f, p.part + ((int64_t)s * rows + mo) * p.N + n);
     }
   }
   if (groups > 1) {
@@ -870,10 +903,9 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups) {
   }
   if (!in) return;
   if constexpr (GATED) {
-    finish_gated<DT>(p, mo, n, f, u);
+    finish_gated<DT>(p, row, n, f, u);
   } else {
-    const int out = mo >= p.M;
-    finish_linear<DT>(p, out, mo - (out ? p.M : 0), n, f);
+    finish_linear<DT>(p, out, row, n, f);
   }
 }
 
@@ -980,11 +1012,11 @@ constexpr int64_t kCus = 256;  // compute units of an MI355X
 // and LDS stages.
 constexpr int kTiles = 5;
 constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16}, kTileN[kTiles] = {256, 128, 128, 128, 128};
-int g_lin_tile = -1, g_lin_slices = 0;  // overrides (linear_set_tuning)
+int g_lin_tile = -1, g_lin_split = -1;  // overrides (linear_set_tuning)
 
 struct Plan {
-  int tile, slices;
-  int64_t items;
+  int tile, split;  // split: shares, 0 for whole tiles
+  int64_t tiles;
 };
 
 int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
@@ -992,32 +1024,75 @@ int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
   return ((M + kTileM[tile] - 1) / kTileM[tile]) * ((N + bn - 1) / bn) * outs;
 }
 
-Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  Plan pl{0, 1, 0};
-  const int64_t steps = ((K + BK - 1) / BK) * segs;
-  if (lay != kDw && M <= 64) pl.tile = M <= 16 ? 4 : M <= 32 ? 3 : 2;
-  else if (tiles_of(0, gated, M, N, outs) < kCus) pl.tile = 1;
-  if (g_lin_tile >= 0 && (lay != kDw || g_lin_tile < 2)) pl.tile = g_lin_tile;
-  const int64_t tiles = tiles_of(pl.tile, gated, M, N, outs);
-  int64_t s = 1;
-  if (pl.tile > 0 && tiles > 0) s = (2 * kCus) / tiles;
-  if (s > steps / 2) s = steps / 2;
-  if (g_lin_slices > 0) s = g_lin_slices < steps ? g_lin_slices : steps;
-  if (s > 64) s = 64;
-  pl.slices = s < 1 ? 1 : (int)s;
-  pl.items = tiles * pl.slices;
-  return pl;
+// Largest number of shares that hold part of one tile.
+int64_t slots_of(const Plan& pl, int64_t steps) {
+  int64_t most = 0;
+  for (int64_t t = 0; t < pl.tiles; ++t) {
+    const uint32_t at = (uint32_t)(t * steps), TS = (uint32_t)(pl.tiles * steps);
+    const int64_t n = share_of(at + (uint32_t)steps - 1, TS, pl.split) - share_of(at, TS, pl.split) + 1;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
-size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int outs) {
-  return pl.slices > 1 ? (size_t)pl.slices * M * N * outs * 4 : 0;
+// The tile and split with the smallest estimated time.  Per tile: a step's
+// time with one workgroup on a CU (latency) and each workgroup's part of it
+// with two (throughput; gated small tiles run alone), in us, measured over
+// sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
+// 3 us for the reduction's launch and the partials' bytes at 4 TB/s; one
+// row tile streams its weights at 26 GB/s per CU at most.
+Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.40}, {1.45, 0.95, 0.60, 0.55, 0.50}};
+  static const double paired[kTiles] = {0, 0.50, 0.28, 0.25, 0.22};
+  const int64_t steps = ((K + BK - 1) / BK) * segs;
+  Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
+  double least = 1e30;
+  for (int t = 0; t < kTiles; ++t) {
+    if (lay == kDw && t > 1) break;
+    if (g_lin_tile >= 0 && (lay != kDw || g_lin_tile < 2) && t != g_lin_tile) continue;
+    const int64_t tiles = tiles_of(t, gated, M, N, outs);
+    const bool pairs = t > 0 && !gated;
+    double step = alone[gated][t];
+    if (M <= kTileM[t]) {
+      const double stream = (gated ? 32768 : kTileN[t] * 128) / 26e3 + 0.1 * step;
+      step = stream > step ? stream : step;
+    }
+    // whole tiles
+    const int64_t per = pairs ? 2 * kCus : kCus, full = tiles / per, rest = tiles % per;
+    const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
+    double whole = full * (steps * (pairs ? both : step) + 4);
+    if (rest) whole += steps * (rest > kCus ? both : step) + 4;
+    if (g_lin_split <= 0 && whole < least) {
+      least = whole;
+      best = Plan{t, 0, tiles};
+    }
+    // split over one workgroup per CU, at least two steps each
+    int64_t shares = tiles * steps / 2 < kCus ? tiles * steps / 2 : kCus;
+    if (g_lin_split > 0) shares = g_lin_split < tiles * steps ? g_lin_split : tiles * steps;
+    if (g_lin_split == 0 || shares < 1 || tiles * steps >= (1 << 22)) continue;
+    while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
+    if (g_lin_split < 0 && (tiles >= shares || steps < 2)) continue;
+    const double rows = M < kTileM[t] ? M : kTileM[t];
+    const double parts = (shares + tiles) * rows * (gated ? 256 : kTileN[t]) * 8.0 / 4e6;
+    const double time = (double)tiles * steps / shares * step + 7 + parts;
+    if (time < least) {
+      least = time;
+      best = Plan{t, (int)shares, tiles};
+    }
+  }
+  return best;
+}
+
+size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+  if (!pl.split || pl.tiles == 0) return 0;
+  return (size_t)(slots_of(pl, (K + BK - 1) / BK * segs) * M * N * outs * 4);
 }
 
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
-void launch_tile(const LinP& p, int64_t items, hipStream_t s) {
+void launch_tile(const LinP& p, int64_t items, hipStream_t s) {  // items: shares or tiles
   constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes + Operand<LAY != kDx, BN>::kBytes);
   constexpr int64_t most = kCus * (160 * 1024 / lds);  // workgroups that run at once
-  const dim3 grid((unsigned)(items < most ? items : most));
+  const dim3 grid((unsigned)(p.split || items < most ? items : most));
   hipLaunchKernelGGL((k_lin<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
 }
 
@@ -1025,35 +1100,37 @@ template <int DT, int LAY, bool GATED>
 hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
   const Plan pl = lin_plan(LAY, GATED, p.M, p.N, p.K, p.segs, p.outs);
-  if (pl.items > 0x7fffffffLL) return hipErrorNotSupported;
-  p.slices = pl.slices;
+  if (pl.tiles > 0x7fffffffLL) return hipErrorNotSupported;
+  const int64_t groups_of_work = pl.split ? pl.split : pl.tiles;
+  p.split = pl.split;
   p.part = reinterpret_cast<float*>(ws);
   constexpr int SB = GATED ? 256 : 128;
   constexpr int EPI = LAY == kFwd ? kGeneral : kPlain;
   if (pl.tile == 0) {
     // split products finish in k_lin_reduce
-    if (LAY != kFwd || pl.slices > 1 ||
+    if (LAY != kFwd || pl.split ||
         (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res))
-      launch_tile<DT, LAY, GATED, kPlain, 256, 256, 2, 2, 2>(p, pl.items, s);
+      launch_tile<DT, LAY, GATED, kPlain, 256, 256, 2, 2, 2>(p, groups_of_work, s);
     else if (!GATED && !p.bias && !p.pre[0] && p.act == SA_ACT_NONE)
-      launch_tile<DT, LAY, GATED, LAY == kFwd && !GATED ? kResidual : EPI, 256, 256, 2, 2, 2>(p, pl.items, s);
+      launch_tile<DT, LAY, GATED, LAY == kFwd && !GATED ? kResidual : EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
     else
-      launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, pl.items, s);
+      launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
   } else if (pl.tile == 1) {
-    launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, GATED ? 3 : 2>(p, pl.items, s);
+    launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, GATED ? 3 : 2>(p, groups_of_work, s);
   } else if constexpr (LAY != kDw) {
-    if (pl.tile == 2) launch_tile<DT, LAY, GATED, EPI, 64, SB, 1, 4, 3>(p, pl.items, s);
-    else if (pl.tile == 3) launch_tile<DT, LAY, GATED, EPI, 32, SB, 1, 4, GATED ? 4 : 3>(p, pl.items, s);
-    else launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 4>(p, pl.items, s);
+    if (pl.tile == 2) launch_tile<DT, LAY, GATED, EPI, 64, SB, 1, 4, 3>(p, groups_of_work, s);
+    else if (pl.tile == 3) launch_tile<DT, LAY, GATED, EPI, 32, SB, 1, 4, GATED ? 4 : 3>(p, groups_of_work, s);
+    else launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 4>(p, groups_of_work, s);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || pl.slices == 1) return e;
+  if (e != hipSuccess || !pl.split) return e;
   const int64_t octets = (int64_t)p.M * p.outs * (p.N / 8);
   int groups = 1;  // up to 8 threads per output while there is less than a workgroup per CU
-  while (groups < 8 && groups * 2 <= pl.slices && octets * groups < kCus * 256) groups *= 2;
+  while (groups < 8 && groups * pl.tiles <= pl.split && octets * groups < kCus * 256) groups *= 2;
   const int64_t n = (octets * groups + 255) / 256;
   if (n > 0x7fffffffLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups);
+  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups,
+                     __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(GATED ? 128 : kTileN[pl.tile]));
   return hipGetLastError();
 }
 
@@ -1185,7 +1262,7 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
 }  // namespace
 
 size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out) {
-  return part_bytes(lin_plan(kFwd, gated, T, d_out, d_in, 1, 1), T, d_out, gated ? 2 : 1);
+  return part_bytes(lin_plan(kFwd, gated, T, d_out, d_in, 1, 1), T, d_out, d_in, 1, gated ? 2 : 1);
 }
 
 size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
@@ -1194,20 +1271,20 @@ size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int6
   size_t b = 0;
   if (gated || act != SA_ACT_NONE) b += n * round256((size_t)T * d_out * 2);
   if (dbias) b += round256((size_t)strips_of(T) * d_out * 4);
-  const size_t px = part_bytes(lin_plan(kDx, false, T, d_in, d_out, n, 1), T, d_in, 1);
-  const size_t pw = part_bytes(lin_plan(kDw, false, d_in, d_out, T, 1, n), d_in, d_out, n);
+  const size_t px = part_bytes(lin_plan(kDx, false, T, d_in, d_out, n, 1), T, d_in, d_out, n, 1);
+  const size_t pw = part_bytes(lin_plan(kDw, false, d_in, d_out, T, 1, n), d_in, d_out, T, 1, n);
   return b + (px > pw ? px : pw);
 }
 
-int linear_set_tuning(int tile, int slices) {
-  if (tile < -1 || tile >= kTiles || slices < 0 || slices > 64) return 1;
+int linear_set_tuning(int tile, int split) {
+  if (tile < -1 || tile >= kTiles || split < -1 || split > 2 * kCus) return 1;
   g_lin_tile = tile;
-  g_lin_slices = slices;
+  g_lin_split = split;
   return 0;
 }
 
-int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* slices,
-                int64_t* items) {
+int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* split,
+                int64_t* tiles) {
   Plan pl;
   switch (op) {
     case SA_LINEAR_FORWARD: pl = lin_plan(kFwd, false, T, d_out, d_in, 1, 1); break;
@@ -1220,8 +1297,8 @@ int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* 
   }
   *rows = kTileM[pl.tile];
   *cols = op == SA_LINEAR_GATED ? 128 : kTileN[pl.tile];
-  *slices = pl.slices;
-  *items = pl.items;
+  *split = pl.split;
+  *tiles = pl.tiles;
   return 0;
 }
 

@@ -115,6 +115,50 @@ def test_gated_backward_exact(dims, dtype):
         same(dwu, x.double().T @ du)
 
 
+@pytest.fixture
+def tuning():
+    yield sa.set_linear_tuning
+    sa.set_linear_tuning()
+
+
+@pytest.mark.parametrize("split", [0, 8, 64, 512])
+@pytest.mark.parametrize("tile", range(5))
+def test_every_tile_and_split(tuning, tile, split):
+    """All compiled tiles, whole and shared: ragged rows and columns, K steps
+    that end inside a step, shares that cross tiles, more tiles than
+    workgroups, every epilogue."""
+    tuning(tile, split)
+    for t, d_in, d_out, dt in ((1, 200, 72, torch.float16), (77, 584, 392, torch.bfloat16),
+                               (530, 328, 1032, torch.float16), (300, 72, 40968, torch.bfloat16)):
+        x, res = ints((t, d_in), -2, 2, dt, 90), ints((t, d_out), -50, 50, dt, 91)
+        wg, wu = ints((d_in, d_out), -2, 2, dt, 92), ints((d_in, d_out), -1, 1, dt, 93)
+        bias = ints((d_out,), -9, 9, dt, 94)
+        g64, u64 = x.double() @ wg.double(), x.double() @ wu.double()
+        same(sa.dense_linear(x, wg), g64)
+        same(sa.dense_linear(x, wg, residual=res), g64 + res.double())
+        y, pre = sa.dense_linear(x, wg, bias=bias, act="relu", residual=res, with_pre=True)
+        same(pre, g64 + bias.double())
+        same(y, (g64 + bias.double()).clamp(min=0) + res.double())
+        same(sa.dense_linear(x, wg, bias=bias), g64 + bias.double())
+        h, g, u = sa.gated_linear(x, wg, wu, act="relu", with_gu=True)
+        same(g, g64)
+        same(u, u64)
+        same(h, g64.clamp(min=0) * u64)
+        same(sa.gated_linear(x, wg, wu, act="relu"), g64.clamp(min=0) * u64)
+        dh, u = ints((t, d_out), -1, 1, dt, 95), ints((t, d_out), -1, 1, dt, 96)
+        g = ints((t, d_out), -1, 1, dt, 97)
+        dx, dwg, dwu = sa.gated_linear_backward(dh, x, wg, wu, g, u, act="relu")
+        dg = dh.double() * u.double() * (g > 0).double()
+        du = dh.double() * g.double().clamp(min=0)
+        same(dx, dg @ wg.double().T + du @ wu.double().T)
+        same(dwg, x.double().T @ dg)
+        same(dwu, x.double().T @ du)
+        dx, dwt, db = sa.dense_linear_backward(dh, x, wg, with_dbias=True)
+        same(dx, dh.double() @ wg.double().T)
+        same(dwt, x.double().T @ dh.double())
+        same(db, dh.double().sum(0))
+
+
 @pytest.mark.parametrize("shape", [(2000, 4096, 1024), (1024, 1024, 4096), (260, 2056, 11008),
                                    (1, 11008, 4096), (8, 4096, 14336), (48, 14336, 4096),
                                    (2500, 4104, 4168), (4100, 200, 8200)], ids=str)

@@ -184,3 +184,35 @@ def gated_bwd(sa, dtype=0, dh=P, lddh=32, x=2 * P, ldx=64, T=3, wg=3 * P, ldwg=3
 def test_gated_linear_backward_refusals(sa, bad, status):
     assert gated_bwd(sa, **bad) == status
     assert b"gated_linear_backward" in sa.sa_last_error()
+
+
+def plan(sa, op, t, d_in, d_out):
+    import ctypes
+    o = [ctypes.c_int() for _ in range(3)] + [ctypes.c_int64()]
+    assert sa.sa_linear_plan(op, t, d_in, d_out, *[ctypes.addressof(v) for v in o]) == OK
+    return tuple(v.value for v in o)  # rows, cols, split, tiles
+
+
+@needs_lib
+def test_plans(sa):
+    """Large products take whole 256 x 256 tiles, few rows share the weights'
+    steps over one workgroup per CU, and the workspace holds the partials."""
+    assert plan(sa, 0, 8192, 14336, 4096) == (256, 256, 0, 512)
+    assert plan(sa, 1, 8192, 4096, 14336) == (256, 128, 0, 3584)
+    assert plan(sa, 3, 4096, 4096, 11008) == (256, 256, 0, 688)
+    assert plan(sa, 5, 4096, 4096, 11008) == (256, 256, 0, 1376)
+    rows, cols, split, tiles = plan(sa, 0, 1, 4096, 4096)
+    assert (rows, split) == (16, 256) and tiles == 32
+    # 64 steps x 32 tiles over 256 shares: 8 steps each, 8 shares per tile
+    assert sa.dense_linear_workspace_bytes(1, 4096, 4096) == 8 * 4096 * 4
+    rows, cols, split, tiles = plan(sa, 1, 1, 4096, 11008)
+    assert (rows, split, tiles) == (16, 256, 86)
+    # 21.5 steps per share: a tile of 64 steps meets at most 5 shares
+    assert sa.gated_linear_workspace_bytes(1, 4096, 11008) in (4 * 11008 * 8, 5 * 11008 * 8)
+    assert sa.sa_linear_plan(6, 1, 64, 64, P, P, P, P) == INVALID
+    assert sa.sa_linear_plan(0, 1, 60, 64, P, P, P, P) == INVALID
+    assert sa.sa_linear_plan(0, 1, 64, 64, None, P, P, P) == INVALID
+    assert sa.sa_set_linear_tuning(5, 0) == INVALID
+    assert sa.sa_set_linear_tuning(0, 513) == INVALID
+    assert sa.sa_set_linear_tuning(-2, 0) == INVALID
+    assert sa.sa_set_linear_tuning(-1, -1) == OK
