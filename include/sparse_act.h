@@ -518,11 +518,18 @@ int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
  *   *_workspace_bytes function names (16-byte aligned; its contents on entry
  *   do not matter; NULL allowed when that is 0).  Calls that share one must
  *   be ordered on one stream.
+ * - `tickets` (forward calls) is NULL, or SA_LINEAR_TICKET_BYTES of device
+ *   memory, 16-byte aligned, zero before its first use and left zero by every
+ *   call.  With it, calls of at most 64 rows sum their split products in the
+ *   same launch instead of a second one; the bits are the same.  Calls that
+ *   share it must be ordered on one stream, so a captured graph that may run
+ *   beside other calls takes its own, or NULL.
  * - Inf and NaN in a row of x reach that row's outputs only.
  * - Sums run in a fixed order: equal calls give equal bits.
  * - act: SA_ACT_*.  sigma(z) = 1 / (1 + e^-z), Phi the normal distribution
  *   function.  The slope of relu and relu2 at 0 is 0.
  */
+#define SA_LINEAR_TICKET_BYTES ((size_t)256 << 10)
 #define SA_F16 0
 #define SA_BF16 1
 #define SA_ACT_NONE 0
@@ -541,7 +548,7 @@ int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
 int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
                  int64_t d_in, int64_t d_out, const void* bias, int act, const void* residual,
                  int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldpre, void* ws,
-                 size_t ws_bytes, void* stream);
+                 size_t ws_bytes, void* tickets, void* stream);
 size_t dense_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
 /*
@@ -574,7 +581,7 @@ size_t dense_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_
 int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
                  const void* wut, int64_t ldwu, int64_t d_in, int64_t d_out, int act, void* h,
                  int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
-                 size_t ws_bytes, void* stream);
+                 size_t ws_bytes, void* tickets, void* stream);
 size_t gated_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
 /*

@@ -85,13 +85,13 @@ _SIGNATURES = {
     "dense_gemm": (_i32, [_vp, _i64, _i64, _vp, _i64, _vp, _vp]),
     "sa_set_gemv_tuning": (_i32, [_i32, _i32, _i32]),
     "dense_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp,
-                            _i64, _vp, _i64, _vp, _sz, _vp]),
+                            _i64, _vp, _i64, _vp, _sz, _vp, _vp]),
     "dense_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "dense_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32,
                                      _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
     "dense_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "gated_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64,
-                            _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+                            _vp, _i64, _vp, _i64, _vp, _sz, _vp, _vp]),
     "gated_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "gated_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64,
                                      _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
@@ -716,19 +716,32 @@ def _lin_ws_bytes(fn: str, *args) -> int:
     return int(getattr(lib(), fn + "_workspace_bytes")(*args))
 
 
+LINEAR_TICKET_BYTES = 256 << 10  # SA_LINEAR_TICKET_BYTES
+_tickets: dict = {}  # (device index, stream) -> the zero counters of the one-launch sum
+
+
 def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
     """Runs ``fn`` on the current stream of ``like``'s device, with scratch
     of its own from torch's allocator: calls on other streams and captured
-    graphs share none."""
-    need = _lin_ws_bytes(fn, *sizes)
+    graphs share none.  The forward calls' counters belong to the stream; a
+    captured call goes without (its replays may run on any stream)."""
     dev = like.device
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, _ptr(ws), need, torch.cuda.current_stream(dev).cuda_stream)
-    else:
+    if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            st = f(*args, _ptr(ws), need, torch.cuda.current_stream(dev).cuda_stream)
+            return _lin_call(fn, like, sizes, *args)
+    need = _lin_ws_bytes(fn, *sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if fn in ("dense_linear", "gated_linear"):
+        tk = None
+        if need and sizes[0] <= 64 and not torch.cuda.is_current_stream_capturing():
+            tk = _tickets.get((dev.index, stream))
+            if tk is None:
+                tk = torch.zeros(LINEAR_TICKET_BYTES, dtype=torch.uint8, device=dev)
+                _tickets[dev.index, stream] = tk
+        st = getattr(lib(), fn)(*args, _ptr(ws), need, _ptr(tk), stream)
+    else:
+        st = getattr(lib(), fn)(*args, _ptr(ws), need, stream)
     _check(st, fn)
 
 

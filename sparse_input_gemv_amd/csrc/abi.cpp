@@ -645,6 +645,8 @@ int sa_gemv_tiling_info(int i, int* tile_o, int* threads, int* unroll) {
   return SA_OK;
 }
 
+static_assert(SA_LINEAR_TICKET_BYTES == sa::kLinearTicketBytes, "header and library agree");
+
 // ---- dense linear layers --------------------------------------------------------
 
 static int run_linear(const sa::LinearCall& c, bool backward, const char* fn, void* stream) {
@@ -684,7 +686,7 @@ size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_
 int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
                  int64_t d_in, int64_t d_out, const void* bias, int act, const void* residual,
                  int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldpre, void* ws,
-                 size_t ws_bytes, void* stream) {
+                 size_t ws_bytes, void* tickets, void* stream) {
   const char* fn = "dense_linear";
   sa::clear_error();
   int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
@@ -702,6 +704,7 @@ int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* w
   if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "residual", residual);
   if (st == SA_OK)
     st = sa::check_linear_ws(fn, ws, ws_bytes, sa::linear_workspace_bytes(false, T, d_in, d_out));
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "tickets", tickets);
   if (st != SA_OK) return st;
   if (T == 0) return SA_OK;
   sa::LinearCall c;
@@ -722,13 +725,14 @@ int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* w
   c.pre[0] = out16(pre);
   c.ldpre[0] = ldpre;
   c.ws = ws;
+  c.tickets = tickets;
   return run_linear(c, false, fn, stream);
 }
 
 int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
                  const void* wut, int64_t ldwu, int64_t d_in, int64_t d_out, int act, void* h,
                  int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
-                 size_t ws_bytes, void* stream) {
+                 size_t ws_bytes, void* tickets, void* stream) {
   const char* fn = "gated_linear";
   sa::clear_error();
   int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
@@ -750,6 +754,7 @@ int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* w
   }
   if (st == SA_OK)
     st = sa::check_linear_ws(fn, ws, ws_bytes, sa::linear_workspace_bytes(true, T, d_in, d_out));
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "tickets", tickets);
   if (st != SA_OK) return st;
   if (T == 0) return SA_OK;
   sa::LinearCall c;
@@ -772,6 +777,7 @@ int gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* w
   c.pre[1] = out16(u);
   c.ldpre[1] = ldu;
   c.ws = ws;
+  c.tickets = tickets;
   return run_linear(c, false, fn, stream);
 }
 

@@ -178,7 +178,9 @@ struct LinearCall {
   int64_t lddw[2] = {0, 0};
   uint16_t* dbias = nullptr;
   void* ws = nullptr;
+  void* tickets = nullptr;  // forward: zero counters for the one-launch sum, or NULL
 };
+constexpr size_t kLinearTicketBytes = (size_t)512 * 4 * 128;  // 512 tiles, four waves, a line each
 size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out);
 size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
                                        bool dbias);

@@ -62,10 +62,30 @@ __device__ __forceinline__ void acc_wait() { asm volatile("s_nop 15\n\ts_nop 7" 
 __device__ __forceinline__ void acc_settle(f4v& acc) { asm volatile("" : "+a"(acc)); }
 
 // ---- activations and their slopes (fp32) -------------------------------------
-// sigma(z) = 1 / (1 + e^-z).  gelu's normal distribution function goes
-// through erfc, which keeps its relative accuracy in the lower tail.
+// sigma(z) = 1 / (1 + e^-z).  gelu's normal distribution function is, for
+// z <= 0, e^(-z^2/2) erfcx(x) / 2 at x = -z / sqrt 2, with erfcx(x) = e^(x^2)
+// erfc(x) as t times a polynomial of degree 8 in t = 1 / (1 + 0.4 x), fitted
+// to the least largest relative error over x >= 0 (4.5e-7 in fp32); so it
+// keeps its relative accuracy in the lower tail, and shares its exponential
+// with the density.  erfcf took three times as long in the elementwise
+// gradient, which it bound.
 constexpr float kTanhA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
+__device__ __forceinline__ float normal_cdf(float z, float& e) {  // e: e^(-z^2/2)
+  e = __expf(-0.5f * z * z);
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.28284271247461901f * fabsf(z));
+  float q = 0.05026216432452202f;
+  q = q * t - 0.18290163576602936f;
+  q = q * t + 0.16908571124076843f;
+  q = q * t - 0.005607785657048225f;
+  q = q * t + 0.1414315551519394f;
+  q = q * t + 0.16854193806648254f;
+  q = q * t + 0.20784270763397217f;
+  q = q * t + 0.22566959261894226f;
+  q = q * t + 0.22567586600780487f;
+  const float h = 0.5f * t * q * e;
+  return z < 0.f ? h : 1.f - h;
+}
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
@@ -74,7 +94,10 @@ __device__ __forceinline__ float act_value(int act, float v) {
     case SA_ACT_RELU: return v > 0.f ? v : 0.f;
     case SA_ACT_RELU2: return v > 0.f ? v * v : 0.f;
     case SA_ACT_SILU: return v * sigmoid(v);
-    case SA_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case SA_ACT_GELU: {
+      float e;
+      return v * normal_cdf(v, e);
+    }
     case SA_ACT_GELU_TANH: return v * sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
     default: return v;
   }
@@ -87,9 +110,11 @@ __device__ __forceinline__ float act_slope(int act, float v) {
       const float s = sigmoid(v);
       return s * (1.f + v * (1.f - s));
     }
-    case SA_ACT_GELU:
-      return 0.5f * erfcf(-0.70710678118654752f * v) +
-             v * 0.3989422804014327f * __expf(-0.5f * v * v);
+    case SA_ACT_GELU: {
+      float e;
+      const float c = normal_cdf(v, e);
+      return c + v * 0.3989422804014327f * e;
+    }
     case SA_ACT_GELU_TANH: {
       const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
       return s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
@@ -108,9 +133,10 @@ __device__ __forceinline__ void act_both(int act, float v, float& f, float& df) 
       return;
     }
     case SA_ACT_GELU: {
-      const float c = 0.5f * erfcf(-0.70710678118654752f * v);
+      float e;
+      const float c = normal_cdf(v, e);
       f = v * c;
-      df = c + v * 0.3989422804014327f * __expf(-0.5f * v * v);
+      df = c + v * 0.3989422804014327f * e;
       return;
     }
     case SA_ACT_GELU_TANH: {
@@ -193,6 +219,8 @@ __device__ __forceinline__ s8v read_nc(uint32_t a) {
   return s8v{q0[0], q0[1], q0[2], q0[3], q1[0], q1[1], q1[2], q1[3]};
 }
 
+constexpr int kTicketStride = 32;  // 128 bytes: counters in one line would wait for each other
+constexpr int kTicketTiles = 512;
 enum Layout { kFwd = 0, kDx = 1, kDw = 2 };
 // Epilogues, each compiled by itself (the general one needs registers that
 // the plain one's K loop would have to give up): the sums as they are (gated:
@@ -209,6 +237,7 @@ struct LinP {
   int split;             // 0: whole tiles; else the workgroups (a power of two) that
                          // share all tiles' steps
   float* part;           // split: [slot][outs * M][N * (gated ? 2 : 1)]
+  uint32_t* tickets;     // split, or NULL: a zero counter per tile and wave, kTicketStride apart
   // epilogue
   int act;
   const uint16_t* bias;
@@ -268,6 +297,16 @@ __device__ __forceinline__ u32x4 round8(const F8& f) {
   for (int i = 0; i < 4; ++i)
     o[i] = (uint32_t)from_f<DT>(f.v[2 * i]) | (uint32_t)from_f<DT>(f.v[2 * i + 1]) << 16;
   return o;
+}
+
+// Slots are added in kChains chains (slot s to chain s % kChains), the chains
+// then in order, wherever the sum is taken.
+constexpr int kChains = 4;
+__device__ __forceinline__ F8 add_chains(const F8 (&c)[kChains]) {
+  F8 f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f.v[e] = ((c[0].v[e] + c[1].v[e]) + c[2].v[e]) + c[3].v[e];
+  return f;
 }
 
 // A matrix's rows from m0 on as a buffer resource: rows past the last lie
@@ -690,6 +729,67 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc_settle(acc[a][b]);
   };
+  // One-launch joining (a wave owns its columns): partials are stored through
+  // to memory (sc1: coherent between XCDs); when they have arrived, the wave
+  // counts itself in, and the last of a tile's shares adds all of them and
+  // finishes the outputs.  No wave waits for another.
+  constexpr bool kJoin = LAY == kFwd && WM == 1;
+  constexpr int kCoherent = 16;  // buffer accesses' sc1 bit
+  const auto part_rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p.part, 0, 0x7fffffff, 0x00020000);
+  auto part_at = [&](int slot, int m, int n) SA_INLINE {
+    return (uint32_t)((slot * p.M + m) * (GATED ? 2 : 1) * p.N + n) * 4u;
+  };
+  auto put_part = [&](uint32_t at, const F8& f) SA_INLINE {
+    u32x4 lo, hi;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = f.v[e], y = f.v[4 + e];
+      lo[e] = __builtin_bit_cast(uint32_t, x);
+      hi[e] = __builtin_bit_cast(uint32_t, y);
+    }
+    __builtin_amdgcn_raw_buffer_store_b128(lo, part_rsrc, at, 0, kCoherent);
+    __builtin_amdgcn_raw_buffer_store_b128(hi, part_rsrc, at + 16, 0, kCoherent);
+  };
+  auto get_part = [&](uint32_t at, F8& f) SA_INLINE {
+    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(part_rsrc, at, 0, kCoherent);
+    const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(part_rsrc, at + 16, 0, kCoherent);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t x = lo[e], y = hi[e];
+      f.v[e] += __builtin_bit_cast(float, x);
+      f.v[4 + e] += __builtin_bit_cast(float, y);
+    }
+  };
+  auto join = [&](const Item& it, int t) SA_INLINE {
+    const int slots = uni(share_of(t * steps + steps - 1, tiles * steps, p.split) -
+                          share_of(t * steps, tiles * steps, p.split) + 1);
+    uint32_t* const ticket = p.tickets + (t * 4 + w) * kTicketStride;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int before_me = 0;
+    if (lane == 0)
+      before_me = (int)__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (uni(before_me) != slots - 1) return;
+    if (lane == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    constexpr int OC = NO * 2;  // octets of the wave's columns
+    const int rows = p.M - it.m0 < BM ? p.M - it.m0 : BM;
+    for (int o = lane; o < rows * OC; o += 64) {
+      const int m = it.m0 + o / OC, n = it.n0 + wn * NO * 16 + (o % OC) * 8;
+      if (n >= p.N) continue;
+      F8 f[kChains] = {}, u[kChains] = {};
+      for (int s = 0; s < slots; s += kChains) {
+#pragma unroll
+        for (int c = 0; c < kChains; ++c) {
+          if (s + c >= slots) break;
+          const uint32_t q = part_at(s + c, m, n);
+          get_part(q, f[c]);
+          if constexpr (GATED) get_part(q + 4 * p.N, u[c]);
+        }
+      }
+      const F8 fs = add_chains(f);
+      if constexpr (GATED) finish_gated<DT>(p, m, n, fs, add_chains(u));
+      else finish_linear<DT>(p, it.out, m, n, fs);
+    }
+  };
   auto finish_parts = [&](const Item& it) SA_INLINE {
     // slot: how many shares before this one hold part of the tile
     const int t = (it.n0 / BNO + (it.out ? nt1 : 0)) * mt + it.m0 / BM;
@@ -702,6 +802,15 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
       for (int b = 0; b < NO; b += 2) {
         const F8 f = pair8(acc[a][b], acc[a][b + 1]);
         const int n = it.n0 + (wn * NO + b + (g & 1)) * 16 + 8 * (g >> 1);
+        if constexpr (kJoin) {
+          if (p.tickets) {
+            const uint32_t q = m < p.M && n < p.N ? part_at(slot, m, n) : kOutOfRange;
+            put_part(q, f);
+            if constexpr (GATED)
+              put_part(q + 4 * p.N, pair8(acc[a][b + NO], acc[a][b + NO + 1]));
+            continue;
+          }
+        }
         if constexpr (GATED) {
           const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
           if (m >= p.M || n >= p.N) continue;
@@ -714,6 +823,9 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
         }
       }
     });
+    if constexpr (kJoin) {
+      if (p.tickets) join(it, t);
+    }
   };
   auto finish_rows = [&](const Item& it) SA_INLINE {
     constexpr int mode = EPI;
@@ -852,9 +964,8 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   stage_barrier<0, 0>();  // no load may land in LDS after the workgroup's end
 }
 // Sums the shares' partials of each tile (2^lbm x 2^lbn outputs) and finishes the outputs, 8
-// columns of a row per thread.  With few rows there are few threads and each
-// waits for its loads in turn, so `groups` threads share an output: group k
-// adds slots k, k + groups, ..., and the groups' sums are added in order.
+// columns of a row per thread, or (groups = kChains, for few outputs) one of
+// their chains per thread.
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm, int lbn) {
   __shared__ float part[256][GATED ? 17 : 9];  // odd rows: lanes in different banks
@@ -867,45 +978,52 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm,
   const int n = in ? (int)(id - mo * n8) * 8 : 0;
   const int out = mo >= (uint32_t)p.M;
   const int row = (int)(mo - (out ? p.M : 0));
-  F8 f = {}, u = {};
+  F8 f[kChains] = {}, u[kChains] = {};
   if (in) {
     const int mt = (p.M + (1 << lbm) - 1) >> lbm, nt1 = (p.N + (1 << lbn) - 1) >> lbn;
     const uint32_t steps = (uint32_t)((p.K + BK - 1) / BK * p.segs), TS = mt * nt1 * p.outs * steps;
     const uint32_t at = (uint32_t)(((n >> lbn) + out * nt1) * mt + (row >> lbm)) * steps;
     const int slots = share_of(at + steps - 1, TS, p.split) - share_of(at, TS, p.split) + 1;
-    if constexpr (GATED) {
+    auto add = [&](int s, F8& fc, F8& uc) {
+      const float* q = p.part + ((int64_t)s * rows + mo) * (GATED ? 2 : 1) * p.N + n;
+      add_part(fc, q);
+      if constexpr (GATED) add_part(uc, q + p.N);
+    };
+    if (groups > 1) {  // this thread's chain
 #pragma unroll 4
-      for (int s = k; s < slots; s += groups) {
-        const float* q = p.part + (((int64_t)s * p.M + mo) * 2) * p.N + n;
-        add_part(f, q);
-        add_part(u, q + p.N);
-      }
+      for (int s = k; s < slots; s += kChains) add(s, f[0], u[0]);
     } else {
-#pragma unroll 4
-      for (int s = k; s < slots; s += groups) add_part(f, p.part + ((int64_t)s * rows + mo) * p.N + n);
+      for (int s = 0; s < slots; s += kChains) {
+#pragma unroll
+        for (int c = 0; c < kChains; ++c) {
+          if (s + c >= slots) break;
+          add(s + c, f[c], u[c]);
+        }
+      }
     }
   }
   if (groups > 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      part[threadIdx.x][e] = f.v[e];
-      if constexpr (GATED) part[threadIdx.x][8 + e] = u.v[e];
+      part[threadIdx.x][e] = f[0].v[e];
+      if constexpr (GATED) part[threadIdx.x][8 + e] = u[0].v[e];
     }
     __syncthreads();
     if (k > 0) return;
-    for (int j = 1; j < groups; ++j) {
+#pragma unroll
+    for (int c = 1; c < kChains; ++c) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f.v[e] += part[j * per + o][e];
-        if constexpr (GATED) u.v[e] += part[j * per + o][8 + e];
+        f[c].v[e] = part[c * per + o][e];
+        if constexpr (GATED) u[c].v[e] = part[c * per + o][8 + e];
       }
     }
   }
   if (!in) return;
   if constexpr (GATED) {
-    finish_gated<DT>(p, row, n, f, u);
+    finish_gated<DT>(p, row, n, add_chains(f), add_chains(u));
   } else {
-    finish_linear<DT>(p, out, row, n, f);
+    finish_linear<DT>(p, out, row, n, add_chains(f));
   }
 }
 
@@ -1042,7 +1160,7 @@ int64_t slots_of(const Plan& pl, int64_t steps) {
 // 3 us for the reduction's launch and the partials' bytes at 4 TB/s; one
 // row tile streams its weights at 26 GB/s per CU at most.
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.40}, {1.45, 0.95, 0.60, 0.55, 0.50}};
+  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38}, {1.45, 0.95, 0.60, 0.55, 0.50}};
   static const double paired[kTiles] = {0, 0.50, 0.28, 0.25, 0.22};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
   Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
@@ -1050,6 +1168,7 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
   for (int t = 0; t < kTiles; ++t) {
     if (lay == kDw && t > 1) break;
     if (g_lin_tile >= 0 && (lay != kDw || g_lin_tile < 2) && t != g_lin_tile) continue;
+    if (g_lin_tile < 0 && M <= 64 && kTileM[t] < M) continue;  // one row tile holds them all
     const int64_t tiles = tiles_of(t, gated, M, N, outs);
     const bool pairs = t > 0 && !gated;
     double step = alone[gated][t];
@@ -1066,8 +1185,9 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
       least = whole;
       best = Plan{t, 0, tiles};
     }
-    // split over one workgroup per CU, at least two steps each
-    int64_t shares = tiles * steps / 2 < kCus ? tiles * steps / 2 : kCus;
+    // split over one workgroup per CU, at least four steps each (two: 33 rows
+    // of 4096 x 1024 10.9 us against 10.1)
+    int64_t shares = tiles * steps / 4 < kCus ? tiles * steps / 4 : kCus;
     if (g_lin_split > 0) shares = g_lin_split < tiles * steps ? g_lin_split : tiles * steps;
     if (g_lin_split == 0 || shares < 1 || tiles * steps >= (1 << 22)) continue;
     while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
@@ -1104,6 +1224,15 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
   const int64_t groups_of_work = pl.split ? pl.split : pl.tiles;
   p.split = pl.split;
   p.part = reinterpret_cast<float*>(ws);
+  // One launch where a wave owns its columns, offsets fit 31 bits, and the
+  // last wave of a tile adds its partials in at most 4 rounds of loads (one
+  // row of 4096 x 4096: 13.5 -> 12.1 us; 33 rows of 4096 x 1024, 24 rounds:
+  // 13.8 -> 22.8 us, so those take the second launch).
+  const int64_t slots = pl.split ? pl.split / pl.tiles + 2 : 0;
+  const int64_t rounds = ((p.M < kTileM[pl.tile] ? p.M : kTileM[pl.tile]) * 4 + 63) / 64 * ((slots + 2) / 4);
+  if (!(LAY == kFwd && pl.split && pl.tile >= 2 && pl.tiles <= kTicketTiles && rounds <= 4 &&
+        (int64_t)p.M * p.N * (GATED ? 2 : 1) * 4 * slots < 0x7fffffffLL))
+    p.tickets = nullptr;
   constexpr int SB = GATED ? 256 : 128;
   constexpr int EPI = LAY == kFwd ? kGeneral : kPlain;
   if (pl.tile == 0) {
@@ -1123,10 +1252,10 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
     else launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 4>(p, groups_of_work, s);
   }
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !pl.split) return e;
+  if (e != hipSuccess || !pl.split || p.tickets) return e;
   const int64_t octets = (int64_t)p.M * p.outs * (p.N / 8);
-  int groups = 1;  // up to 8 threads per output while there is less than a workgroup per CU
-  while (groups < 8 && groups * pl.tiles <= pl.split && octets * groups < kCus * 256) groups *= 2;
+  // a thread per chain while that is less than a workgroup per CU
+  const int groups = octets * kChains <= kCus * 256 ? kChains : 1;
   const int64_t n = (octets * groups + 255) / 256;
   if (n > 0x7fffffffLL) return hipErrorNotSupported;
   hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups,
@@ -1165,6 +1294,7 @@ hipError_t fwd_dt(const LinearCall& c, hipStream_t s) {
     p.pre[i] = c.pre[i];
     p.ldpre[i] = (int)c.ldpre[i];
   }
+  p.tickets = static_cast<uint32_t*>(c.tickets);
   return c.gated ? launch_lin<DT, kFwd, true>(p, c.ws, s) : launch_lin<DT, kFwd, false>(p, c.ws, s);
 }
 

@@ -505,6 +505,29 @@ def test_graphs_and_streams(t):
                 assert torch.equal(v, e)
 
 
+@pytest.mark.parametrize("t", [1, 16, 64])
+def test_calls_on_streams_at_once(t):
+    """Single-token calls, whose workgroups add their partial sums within the
+    launch, on three streams at once: each stream has its own counters and
+    scratch, and every call gives the bits of a call by itself."""
+    ins = [layer_inputs(t, 2056, 1032, 7 + k, torch.float16) for k in range(3)]
+    f = lambda i: (sa.gated_linear(i[0], i[1], i[2], with_gu=True),  # noqa: E731
+                   sa.dense_linear(i[0], i[1], bias=i[3][:, 0].contiguous(), act="gelu"))
+    want = [f(i) for i in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for _ in range(5):
+            for i, s in zip(ins, streams):
+                with torch.cuda.stream(s):
+                    got.append(f(i))
+        torch.cuda.synchronize()
+        for k, (gu, y) in enumerate(got):
+            for a, b in zip(gu + (y,), want[k % 3][0] + (want[k % 3][1],)):
+                assert torch.equal(a, b)
+
+
 # ---- with the sparse operators --------------------------------------------------------
 
 def test_decode_block_with_the_sparse_down_projection():

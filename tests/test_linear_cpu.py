@@ -80,9 +80,10 @@ BIG = 1 << 40  # a workspace size no check refuses
 
 
 def linear(sa, dtype=0, x=P, ldx=64, T=3, wt=2 * P, ldw=32, d_in=64, d_out=32, bias=None, act=0,
-           res=None, ldr=32, y=3 * P, ldy=32, pre=None, ldpre=32, ws=4 * P, wsb=BIG):
+           res=None, ldr=32, y=3 * P, ldy=32, pre=None, ldpre=32, ws=4 * P, wsb=BIG,
+           tk=None):
     return sa.dense_linear(dtype, x, ldx, T, wt, ldw, d_in, d_out, bias, act, res, ldr, y, ldy, pre,
-                           ldpre, ws, wsb, None)
+                           ldpre, ws, wsb, tk, None)
 
 
 @needs_lib
@@ -98,7 +99,7 @@ def linear(sa, dtype=0, x=P, ldx=64, T=3, wt=2 * P, ldw=32, d_in=64, d_out=32, b
     (dict(ldy=0), INVALID), (dict(res=5 * P, ldr=24), INVALID), (dict(pre=5 * P, ldpre=0), INVALID),
     (dict(ldx=1 << 22), UNSUPPORTED),
     (dict(y=P), INVALID), (dict(y=2 * P), INVALID), (dict(pre=3 * P), INVALID),
-    (dict(res=5 * P, pre=5 * P), INVALID),
+    (dict(res=5 * P, pre=5 * P), INVALID), (dict(tk=P + 4), INVALID),
 ])
 def test_dense_linear_refusals(sa, bad, status):
     assert linear(sa, **bad) == status
@@ -109,7 +110,7 @@ def test_dense_linear_refusals(sa, bad, status):
 def test_empty_calls(sa):
     assert linear(sa, T=0, x=None, y=None) == OK
     assert sa.gated_linear(0, None, 64, 0, P, 32, 2 * P, 32, 64, 32, 3, None, 32, None, 0, None, 0,
-                           None, 0, None) == OK
+                           None, 0, None, None) == OK
 
 
 @needs_lib
@@ -126,9 +127,9 @@ def test_workspace_refusals(sa):
 
 
 def gated(sa, dtype=1, x=P, ldx=64, T=3, wg=2 * P, ldg=32, wu=3 * P, ldu=32, d_in=64, d_out=32,
-          act=3, h=4 * P, ldh=32, g=5 * P, ldgo=32, u=6 * P, lduo=32, ws=7 * P, wsb=BIG):
+          act=3, h=4 * P, ldh=32, g=5 * P, ldgo=32, u=6 * P, lduo=32, ws=7 * P, wsb=BIG, tk=None):
     return sa.gated_linear(dtype, x, ldx, T, wg, ldg, wu, ldu, d_in, d_out, act, h, ldh, g, ldgo, u,
-                           lduo, ws, wsb, None)
+                           lduo, ws, wsb, tk, None)
 
 
 @needs_lib
@@ -139,6 +140,7 @@ def gated(sa, dtype=1, x=P, ldx=64, T=3, wg=2 * P, ldg=32, wu=3 * P, ldu=32, d_i
     (dict(ldgo=16), INVALID), (dict(lduo=28), INVALID), (dict(h=P), INVALID),
     (dict(h=5 * P), INVALID), (dict(g=6 * P), INVALID), (dict(u=3 * P), INVALID),
     (dict(d_in=12), INVALID), (dict(d_out=4), INVALID), (dict(wu=3 * P + 8), INVALID),
+    (dict(tk=P + 8), INVALID),
 ])
 def test_gated_linear_refusals(sa, bad, status):
     assert gated(sa, **bad) == status
