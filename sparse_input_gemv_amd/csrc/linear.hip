@@ -177,6 +177,10 @@ __device__ __forceinline__ void set_lds(uint32_t lds) {
 __device__ __forceinline__ void load_lds16(uint32_t voff, i4v rsrc) {
   asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc) : "memory");
 }
+// Non-temporal: for weights that are read once.
+__device__ __forceinline__ void load_lds16_nt(uint32_t voff, i4v rsrc) {
+  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen nt lds" : : "v"(voff), "s"(rsrc) : "memory");
+}
 
 // Waits until at most VM loads and LG LDS reads are outstanding (63, 15: no
 // wait), then the workgroup barrier.  s_waitcnt encoding: vmcnt bits 3:0 and
@@ -474,10 +478,11 @@ struct Operand {
   __device__ __forceinline__ static void place(int j, uint32_t lds, int w) {
     set_lds(lds + (w * I + j) * 1024);
   }
-  __device__ __forceinline__ void load(int j, i4v rs, int left) const {
+  __device__ __forceinline__ void load(int j, i4v rs, int left, bool once) const {
     uint32_t v = voff[j];
     if constexpr (!NC) v = kc[j & 1] < left ? v : kOutOfRange;
-    load_lds16(v, rs);
+    if (once) load_lds16_nt(v, rs);
+    else load_lds16(v, rs);
   }
 };
 
@@ -543,7 +548,10 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   // A cursor goes over the workgroup's items: a tile's number, or (split) a
   // position among all tiles' steps, up to `end`.
   const bool split = p.split > 0;
-  const int share = split ? (int)xcd_run(blockIdx.x, gridDim.x) : 0;
+  // Row tiles that read the same weights are kept on one XCD; with a single
+  // one nothing is shared, and neighbouring shares on different XCDs stream
+  // faster (one row of 4096 x 4096: 11.4 -> 11.1 us).
+  const int share = !split ? 0 : mt == 1 ? (int)blockIdx.x : (int)xcd_run(blockIdx.x, gridDim.x);
   const int lg = split ? __builtin_ctz(p.split) : 0;
   const int begin = split ? (int)((uint32_t)share * (uint32_t)(tiles * steps) >> lg) : (int)blockIdx.x;
   const int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)(tiles * steps) >> lg) : tiles;
@@ -622,9 +630,12 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
     if (j < OP::I) OP::place(j, lp + buf * OP::kBytes, w);
     else OQ::place(j - OP::I, lq + buf * OQ::kBytes, w);
   };
+  // A single row tile reads its weights once, past the caches (one row of
+  // 4096 x 4096: 13.4 -> 11.4 us, gate and up 4096 x 11008: 40.4 -> 37.1).
+  const bool once = BM <= 64 && LAY != kDw && mt == 1;
   auto load_one = [&](int j) SA_INLINE {
-    if (j < OP::I) op.load(j, rp, left);
-    else oq.load(j - OP::I, rq, left);
+    if (j < OP::I) op.load(j, rp, left, false);
+    else oq.load(j - OP::I, rq, left, once);
   };
 
   // ---- the computing side
