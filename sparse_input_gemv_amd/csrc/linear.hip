@@ -89,63 +89,61 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {  // e: e^(-z^2/
 __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
-__device__ __forceinline__ float act_value(int act, float v) {
-  switch (act) {
-    case SA_ACT_RELU: return v > 0.f ? v : 0.f;
-    case SA_ACT_RELU2: return v > 0.f ? v * v : 0.f;
-    case SA_ACT_SILU: return v * sigmoid(v);
-    case SA_ACT_GELU: {
-      float e;
-      return v * normal_cdf(v, e);
-    }
-    case SA_ACT_GELU_TANH: return v * sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
-    default: return v;
+// The activation is a template argument where it is applied: a branch per
+// value costs more than the value.
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if constexpr (ACT == SA_ACT_RELU) return v > 0.f ? v : 0.f;
+  if constexpr (ACT == SA_ACT_RELU2) return v > 0.f ? v * v : 0.f;
+  if constexpr (ACT == SA_ACT_SILU) return v * sigmoid(v);
+  if constexpr (ACT == SA_ACT_GELU) {
+    float e;
+    return v * normal_cdf(v, e);
+  }
+  if constexpr (ACT == SA_ACT_GELU_TANH)
+    return v * sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
+  return v;
+}
+// Value and slope, sharing their transcendental part.
+template <int ACT>
+__device__ __forceinline__ void act_both(float v, float& f, float& df) {
+  f = v;
+  df = 1.f;
+  if constexpr (ACT == SA_ACT_RELU) {
+    f = v > 0.f ? v : 0.f;
+    df = v > 0.f ? 1.f : 0.f;
+  }
+  if constexpr (ACT == SA_ACT_RELU2) {
+    f = v > 0.f ? v * v : 0.f;
+    df = v > 0.f ? 2.f * v : 0.f;
+  }
+  if constexpr (ACT == SA_ACT_SILU) {
+    const float s = sigmoid(v);
+    f = v * s;
+    df = s * (1.f + v * (1.f - s));
+  }
+  if constexpr (ACT == SA_ACT_GELU) {
+    float e;
+    const float c = normal_cdf(v, e);
+    f = v * c;
+    df = c + v * 0.3989422804014327f * e;
+  }
+  if constexpr (ACT == SA_ACT_GELU_TANH) {
+    const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
+    f = v * s;
+    df = s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
   }
 }
-__device__ __forceinline__ float act_slope(int act, float v) {
+// f(integral_constant<act>) for the call's activation.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {
-    case SA_ACT_RELU: return v > 0.f ? 1.f : 0.f;
-    case SA_ACT_RELU2: return v > 0.f ? 2.f * v : 0.f;
-    case SA_ACT_SILU: {
-      const float s = sigmoid(v);
-      return s * (1.f + v * (1.f - s));
-    }
-    case SA_ACT_GELU: {
-      float e;
-      const float c = normal_cdf(v, e);
-      return c + v * 0.3989422804014327f * e;
-    }
-    case SA_ACT_GELU_TANH: {
-      const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
-      return s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
-    }
-    default: return 1.f;
-  }
-}
-
-// Both, sharing their transcendental part.
-__device__ __forceinline__ void act_both(int act, float v, float& f, float& df) {
-  switch (act) {
-    case SA_ACT_SILU: {
-      const float s = sigmoid(v);
-      f = v * s;
-      df = s * (1.f + v * (1.f - s));
-      return;
-    }
-    case SA_ACT_GELU: {
-      float e;
-      const float c = normal_cdf(v, e);
-      f = v * c;
-      df = c + v * 0.3989422804014327f * e;
-      return;
-    }
-    case SA_ACT_GELU_TANH: {
-      const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
-      f = v * s;
-      df = s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
-      return;
-    }
-    default: f = act_value(act, v); df = act_slope(act, v);
+    case SA_ACT_RELU: f(std::integral_constant<int, SA_ACT_RELU>{}); break;
+    case SA_ACT_RELU2: f(std::integral_constant<int, SA_ACT_RELU2>{}); break;
+    case SA_ACT_SILU: f(std::integral_constant<int, SA_ACT_SILU>{}); break;
+    case SA_ACT_GELU: f(std::integral_constant<int, SA_ACT_GELU>{}); break;
+    case SA_ACT_GELU_TANH: f(std::integral_constant<int, SA_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, SA_ACT_NONE>{});
   }
 }
 
@@ -282,6 +280,14 @@ __device__ __forceinline__ void store8(uint16_t* p, const F8& f) {
   *reinterpret_cast<u16x8*>(p) = o;
 }
 
+// f = act(f), value by value.
+__device__ __forceinline__ void act8(int act, F8& f) {
+  with_act(act, [&](auto A) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = act_value<decltype(A)::value>(f.v[i]);
+  });
+}
+
 // Eight values of the element type.
 template <int DT>
 __device__ __forceinline__ F8 widen8(u32x4 r) {
@@ -331,10 +337,7 @@ __device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, i
     for (int i = 0; i < 8; ++i) f.v[i] += b.v[i];
   }
   if (p.pre[0]) store8<DT>(p.pre[0] + m * p.ldpre[0] + n, f);
-  if (p.act != SA_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f.v[i] = act_value(p.act, f.v[i]);
-  }
+  act8(p.act, f);
   if (p.res) {
     const F8 r = load8<DT>(p.res + m * p.ldr + n);
 #pragma unroll
@@ -348,8 +351,9 @@ __device__ __forceinline__ void finish_gated(const LinP& p, int64_t m, int n, F8
     store8<DT>(p.pre[0] + m * p.ldpre[0] + n, g);
     store8<DT>(p.pre[1] + m * p.ldpre[1] + n, u);
   }
+  act8(p.act, g);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) g.v[i] = act_value(p.act, g.v[i]) * u.v[i];
+  for (int i = 0; i < 8; ++i) g.v[i] *= u.v[i];
   store8<DT>(p.y[0] + m * p.ldy[0] + n, g);
 }
 
@@ -869,8 +873,9 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
             __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(u), ur,
                 (uint32_t)((row + 16 * a) * p.ldpre[1] * 2) + col[b / 2], 0, 0);
           }
+          act8(p.act, f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f.v[e] = act_value(p.act, f.v[e]) * u.v[e];
+          for (int e = 0; e < 8; ++e) f.v[e] *= u.v[e];
           __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
         }
       });
@@ -913,10 +918,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
             __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
-            if (p.act != SA_ACT_NONE) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f.v[e] = act_value(p.act, f.v[e]);
-            }
+            act8(p.act, f);
           }
           if constexpr (mode >= kResidual) {
             const F8 r = widen8<DT>(rv[a & 1][b / 2]);
@@ -1048,12 +1050,49 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm,
 struct DactP {
   const uint16_t *dy, *a, *b;  // a: pre or g; b: u
   int64_t lddy, lda, ldb;
-  uint16_t *d0, *d1;           // [T][N]; d0 NULL: sums only
+  uint16_t *d0, *d1;           // [T][N] (linear without an activation: none, sums only)
   float* sums;                 // [strips][N] or NULL
   int64_t T, N, strip;
   int act;
 };
 constexpr int kDactRows = 4;
+template <int DT, bool GATED, int ACT>
+__device__ __forceinline__ void dact_rows(const DactP& p, int64_t n, int64_t t0, int64_t t1,
+                                          float (&sum)[8]) {
+  for (int64_t t = t0; t < t1; t += kDactRows) {
+    u16x8 dy[kDactRows], a[kDactRows], b[kDactRows];
+#pragma unroll
+    for (int r = 0; r < kDactRows; ++r) {
+      const int64_t tr = t + r < t1 ? t + r : t1 - 1;
+      dy[r] = *reinterpret_cast<const u16x8*>(p.dy + tr * p.lddy + n);
+      if constexpr (GATED || ACT != SA_ACT_NONE)
+        a[r] = *reinterpret_cast<const u16x8*>(p.a + tr * p.lda + n);
+      if constexpr (GATED) b[r] = *reinterpret_cast<const u16x8*>(p.b + tr * p.ldb + n);
+    }
+#pragma unroll
+    for (int r = 0; r < kDactRows; ++r) {
+      if (t + r >= t1) break;
+      u16x8 o0, o1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = to_f<DT>(dy[r][e]);
+        float f = 0.f, df = 1.f;
+        if constexpr (GATED || ACT != SA_ACT_NONE) act_both<ACT>(to_f<DT>(a[r][e]), f, df);
+        if constexpr (GATED) {
+          o0[e] = from_f<DT>(v * to_f<DT>(b[r][e]) * df);
+          o1[e] = from_f<DT>(v * f);
+        } else {
+          const float d = v * df;
+          sum[e] += d;
+          o0[e] = from_f<DT>(d);
+        }
+      }
+      if constexpr (GATED || ACT != SA_ACT_NONE)
+        *reinterpret_cast<u16x8*>(p.d0 + (t + r) * p.N + n) = o0;
+      if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + (t + r) * p.N + n) = o1;
+    }
+  }
+}
 template <int DT, bool GATED>
 __global__ __launch_bounds__(256) void k_lin_dact(DactP p) {
   __shared__ float part[4][64][9];  // 9: the lanes' rows in different banks
@@ -1066,39 +1105,8 @@ __global__ __launch_bounds__(256) void k_lin_dact(DactP p) {
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  if (in) {
-    for (int64_t t = t0; t < t1; t += kDactRows) {
-      u16x8 dy[kDactRows], a[kDactRows], b[kDactRows];
-#pragma unroll
-      for (int r = 0; r < kDactRows; ++r) {
-        const int64_t tr = t + r < t1 ? t + r : t1 - 1;
-        dy[r] = *reinterpret_cast<const u16x8*>(p.dy + tr * p.lddy + n);
-        if (p.a) a[r] = *reinterpret_cast<const u16x8*>(p.a + tr * p.lda + n);
-        if constexpr (GATED) b[r] = *reinterpret_cast<const u16x8*>(p.b + tr * p.ldb + n);
-      }
-#pragma unroll
-      for (int r = 0; r < kDactRows; ++r) {
-        if (t + r >= t1) break;
-        u16x8 o0, o1;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = to_f<DT>(dy[r][e]);
-          if constexpr (GATED) {
-            float f, df;
-            act_both(p.act, to_f<DT>(a[r][e]), f, df);
-            o0[e] = from_f<DT>(v * to_f<DT>(b[r][e]) * df);
-            o1[e] = from_f<DT>(v * f);
-          } else {
-            const float d = p.a ? v * act_slope(p.act, to_f<DT>(a[r][e])) : v;
-            sum[e] += d;
-            o0[e] = from_f<DT>(d);
-          }
-        }
-        if (p.d0) *reinterpret_cast<u16x8*>(p.d0 + (t + r) * p.N + n) = o0;
-        if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + (t + r) * p.N + n) = o1;
-      }
-    }
-  }
+  if (in)
+    with_act(p.act, [&](auto A) { dact_rows<DT, GATED, decltype(A)::value>(p, n, t0, t1, sum); });
   if constexpr (!GATED) {
     if (!p.sums) return;
 #pragma unroll
@@ -1336,7 +1344,7 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
     DactP a{};
     a.dy = c.dy;
     a.lddy = c.lddy;
-    a.a = map ? c.pre[0] : nullptr;
+    a.a = c.pre[0];
     a.lda = c.ldpre[0];
     a.b = c.pre[1];
     a.ldb = c.ldpre[1];
