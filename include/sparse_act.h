@@ -533,7 +533,7 @@ int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
 #define SA_F16 0
 #define SA_BF16 1
 #define SA_ACT_NONE 0
-#define SA_ACT_RELU 1      /* max(z, 0) */
+#define SA_ACT_RELU 1      /* max(z, 0); NaN stays NaN, here and below */
 #define SA_ACT_RELU2 2     /* max(z, 0)^2 */
 #define SA_ACT_SILU 3      /* z sigma(z) */
 #define SA_ACT_GELU 4      /* z Phi(z) */
@@ -764,8 +764,9 @@ int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, in
                    int* split, int64_t* tiles);
 /*
  * Process-wide choices of the dense linear layers, for tuning sweeps and
- * cross-checks: tile -1 = automatic, or 0..4 (256 x 256, 128 x 128, and 64,
- * 32 or 16 rows x 128; weight gradients take 0 and 1 only); split -1 =
+ * cross-checks: tile -1 = automatic, or 0..5 (256 x 256, 128 x 128, 64, 32
+ * or 16 rows x 128, 256 x 192; weight gradients take 0, 1 and 5 only, gated
+ * products not 5, and 5 is never split); split -1 =
  * automatic, 0 = whole tiles, or that many shares (up to 512, rounded down to
  * a power of two).  Workspace
  * sizes follow the choices: query them again.  Every choice computes the

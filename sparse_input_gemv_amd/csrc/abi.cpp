@@ -898,7 +898,7 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
 int sa_set_linear_tuning(int tile, int split) {
   sa::clear_error();
   if (sa::linear_set_tuning(tile, split) != 0) {
-    sa::set_error("sa_set_linear_tuning: tile must be -1..4 and split -1..512");
+    sa::set_error("sa_set_linear_tuning: tile must be -1..5 and split -1..512");
     return SA_ERR_INVALID_ARG;
   }
   return SA_OK;

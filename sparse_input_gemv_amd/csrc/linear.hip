@@ -8,12 +8,28 @@
 //   gated_linear_backward  dg = dh * u * act'(g), du = dh * act(g);
 //                          dx = dg Wg + du Wu, dWg^T = x^T dg, dWu^T = x^T du
 //
-// Every product is one kernel, k_lin<DT, LAY, ...>: C[m][n] = sum_k P[m][k]
-// Q[k][n] for a row operand P and a column operand Q, each stored with k
-// contiguous ("KC") or with m or n contiguous ("NC"):
+// Every product is one kernel, k_lin: C[m][n] = sum_k P[m][k] Q[k][n] for a
+// row operand P and a column operand Q, each stored with k contiguous ("KC")
+// or with m or n contiguous ("NC"):
 //   forward  P = x  [T][d_in]  KC,  Q = WT [d_in][d_out] NC;
-//   dx       P = d  [T][d_out] KC,  Q = WT, read as n = d_in, k = d_out: KC;
-//   dWT      P = x, read as m = d_in, k = T: NC,  Q = d [T][d_out]: NC.
+//   dx       P = d  [T][d_out] KC,  Q = WT, read as n = d_in, k = d_out: KC
+//            (gated: the K loop runs over dg, Wg and then du, Wu);
+//   dWT      P = x, read as m = d_in, k = T: NC,  Q = d [T][d_out]: NC
+//            (gated: both outputs in one launch, side by side).
+// The gated forward tile holds 128 columns of g and the same 128 of u, so the
+// wave that ends with a g has its u, and x is read once for both.
+//
+// What bounds it, and what it measured on one MI355X (bf16, random data):
+//   large: the matrix cores' power.  MFMAs alone run at 2025 TFLOP/s with
+//     random operands on all CUs (2414 with zeros, 2448 on one CU); the
+//     kernel runs 8192 x 14336 x 4096 at 1400 TFLOP/s, dx 4096 x 11008 x 4096
+//     at 1370, dW 4096 x 4096 x 16384 at 1390, gate and up 8192 x 4096 x
+//     14336 with g and u kept at 1350.  The library's product reaches 1414
+//     at 8192^3 with both operands K-contiguous, 1323 in the forward layout
+//     and 1158 in dW's.
+//   few rows: the weights' stream.  1 x 4096 x 11008 gate and up 35 us (180
+//     MB: 5.1 TB/s; a plain read runs at 7.2, a copy at 5.1), 8 x 11008 x
+//     4096 19 us, 1 x 4096 x 4096 12 us (most of it launch and fill).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -93,8 +109,8 @@ __device__ __forceinline__ float sigmoid(float z) {
 // value costs more than the value.
 template <int ACT>
 __device__ __forceinline__ float act_value(float v) {
-  if constexpr (ACT == SA_ACT_RELU) return v > 0.f ? v : 0.f;
-  if constexpr (ACT == SA_ACT_RELU2) return v > 0.f ? v * v : 0.f;
+  if constexpr (ACT == SA_ACT_RELU) return v <= 0.f ? 0.f : v;  // NaN stays NaN
+  if constexpr (ACT == SA_ACT_RELU2) return v <= 0.f ? 0.f : v * v;
   if constexpr (ACT == SA_ACT_SILU) return v * sigmoid(v);
   if constexpr (ACT == SA_ACT_GELU) {
     float e;
@@ -110,12 +126,12 @@ __device__ __forceinline__ void act_both(float v, float& f, float& df) {
   f = v;
   df = 1.f;
   if constexpr (ACT == SA_ACT_RELU) {
-    f = v > 0.f ? v : 0.f;
-    df = v > 0.f ? 1.f : 0.f;
+    f = v <= 0.f ? 0.f : v;
+    df = v <= 0.f ? 0.f : 1.f;
   }
   if constexpr (ACT == SA_ACT_RELU2) {
-    f = v > 0.f ? v * v : 0.f;
-    df = v > 0.f ? 2.f * v : 0.f;
+    f = v <= 0.f ? 0.f : v * v;
+    df = v <= 0.f ? 0.f : 2.f * v;
   }
   if constexpr (ACT == SA_ACT_SILU) {
     const float s = sigmoid(v);
@@ -131,7 +147,8 @@ __device__ __forceinline__ void act_both(float v, float& f, float& df) {
   if constexpr (ACT == SA_ACT_GELU_TANH) {
     const float s = sigmoid(2.f * kTanhA * (v + kTanhB * v * v * v));
     f = v * s;
-    df = s + 2.f * kTanhA * v * s * (1.f - s) * (1.f + 3.f * kTanhB * v * v);
+    // s (1 - s) first: where v^2 is cut off, or v overflows a product, it is 0
+    df = s + s * (1.f - s) * v * (2.f * kTanhA * (1.f + 3.f * kTanhB * fminf(v * v, 1e6f)));
   }
 }
 // f(integral_constant<act>) for the call's activation.
@@ -514,7 +531,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   static_assert(WM * WN == 4 && MB >= 1 && NB >= 2 && NB % (GATED ? 4 : 2) == 0, "four waves");
   using OP = Operand<PNC, BM>;
-  using OQ = Operand<QNC, BN>;
+  using OQ = Operand<QNC, QNC ? (BN + 127) / 128 * 128 : BN>;  // NC: whole halves are loaded
   constexpr int L = OP::I + OQ::I;
   constexpr int kStage = OP::kBytes + OQ::kBytes;
   __shared__ __align__(16) uint8_t S[NS * kStage];
@@ -1147,8 +1164,9 @@ constexpr int64_t kCus = 256;  // compute units of an MI355X
 
 // The compiled tiles: rows and columns (of g and of u each: 128 at most),
 // and LDS stages.
-constexpr int kTiles = 5;
-constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16}, kTileN[kTiles] = {256, 128, 128, 128, 128};
+constexpr int kTiles = 6;
+constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16, 256}, kTileN[kTiles] = {256, 128, 128, 128, 128, 192};
+constexpr int kNarrow = 5;  // 256 x 192: whole tiles of plain products only, for another tile count
 int g_lin_tile = -1, g_lin_split = -1;  // overrides (linear_set_tuning)
 
 struct Plan {
@@ -1179,17 +1197,21 @@ int64_t slots_of(const Plan& pl, int64_t steps) {
 // 3 us for the reduction's launch and the partials' bytes at 4 TB/s; one
 // row tile streams its weights at 26 GB/s per CU at most.
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38}, {1.45, 0.95, 0.60, 0.55, 0.50}};
-  static const double paired[kTiles] = {0, 0.50, 0.28, 0.25, 0.22};
+  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
+                                          {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
+  static const double paired[kTiles] = {0, 0.50, 0.28, 0.25, 0.22, 0};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
   Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
   double least = 1e30;
   for (int t = 0; t < kTiles; ++t) {
-    if (lay == kDw && t > 1) break;
-    if (g_lin_tile >= 0 && (lay != kDw || g_lin_tile < 2) && t != g_lin_tile) continue;
+    if (lay == kDw && t > 1 && t != kNarrow) continue;
+    if (t == kNarrow && gated) continue;
+    const bool forced = g_lin_tile >= 0 && !(lay == kDw && g_lin_tile > 1 && g_lin_tile != kNarrow) &&
+                        !(g_lin_tile == kNarrow && gated);
+    if (forced && t != g_lin_tile) continue;
     if (g_lin_tile < 0 && M <= 64 && kTileM[t] < M) continue;  // one row tile holds them all
     const int64_t tiles = tiles_of(t, gated, M, N, outs);
-    const bool pairs = t > 0 && !gated;
+    const bool pairs = t > 0 && t != kNarrow && !gated;
     double step = alone[gated][t];
     if (M <= kTileM[t]) {
       const double stream = (gated ? 32768 : kTileN[t] * 128) / 26e3 + 0.1 * step;
@@ -1200,7 +1222,7 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
     double whole = full * (steps * (pairs ? both : step) + 4);
     if (rest) whole += steps * (rest > kCus ? both : step) + 4;
-    if (g_lin_split <= 0 && whole < least) {
+    if ((g_lin_split <= 0 || t == kNarrow) && whole < least) {
       least = whole;
       best = Plan{t, 0, tiles};
     }
@@ -1208,7 +1230,7 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     // of 4096 x 1024 10.9 us against 10.1)
     int64_t shares = tiles * steps / 4 < kCus ? tiles * steps / 4 : kCus;
     if (g_lin_split > 0) shares = g_lin_split < tiles * steps ? g_lin_split : tiles * steps;
-    if (g_lin_split == 0 || shares < 1 || tiles * steps >= (1 << 22)) continue;
+    if (g_lin_split == 0 || t == kNarrow || shares < 1 || tiles * steps >= (1 << 22)) continue;
     while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
     if (g_lin_split < 0 && (tiles >= shares || steps < 2)) continue;
     const double rows = M < kTileM[t] ? M : kTileM[t];
@@ -1229,7 +1251,8 @@ size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int64_t K, int segs, int
 
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const LinP& p, int64_t items, hipStream_t s) {  // items: shares or tiles
-  constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes + Operand<LAY != kDx, BN>::kBytes);
+  constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes +
+                            Operand<LAY != kDx, LAY != kDx ? (BN + 127) / 128 * 128 : BN>::kBytes);
   constexpr int64_t most = kCus * (160 * 1024 / lds);  // workgroups that run at once
   const dim3 grid((unsigned)(p.split || items < most ? items : most));
   hipLaunchKernelGGL((k_lin<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
@@ -1263,6 +1286,8 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
       launch_tile<DT, LAY, GATED, LAY == kFwd && !GATED ? kResidual : EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
     else
       launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
+  } else if (pl.tile == kNarrow) {
+    if constexpr (!GATED) launch_tile<DT, LAY, GATED, EPI, 256, 192, 2, 2, 2>(p, groups_of_work, s);
   } else if (pl.tile == 1) {
     launch_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, GATED ? 3 : 2>(p, groups_of_work, s);
   } else if constexpr (LAY != kDw) {

@@ -122,7 +122,7 @@ def tuning():
 
 
 @pytest.mark.parametrize("split", [0, 8, 64, 512])
-@pytest.mark.parametrize("tile", range(5))
+@pytest.mark.parametrize("tile", range(6))
 def test_every_tile_and_split(tuning, tile, split):
     """All compiled tiles, whole and shared: ragged rows and columns, K steps
     that end inside a step, shares that cross tiles, more tiles than
@@ -380,8 +380,32 @@ def test_inf_and_nan_stay_in_their_row(t):
     h = sa.gated_linear(x, wt, wt, act="relu")
     assert torch.isnan(y[1]).all() and torch.isinf(y[4]).all()
     assert torch.isnan(h[4] / h[4]).all()
+    for act in sa.ACTIVATIONS:
+        assert torch.isnan(sa.dense_linear(x, wt, act=act)[1]).all()
+        assert torch.isnan(sa.gated_linear(x, wt, wt, act=act)[1]).all()
     keep = [r for r in range(t) if r not in (1, 4)]
     assert torch.equal(y[keep], want[keep]) and torch.isfinite(h[keep]).all()
+
+
+@pytest.mark.parametrize("act", SMOOTH)
+def test_far_arguments(act):
+    """Saturated arguments, up to bf16's largest: the value is z or 0 and the
+    slope 1 or 0, without Inf or NaN on the way."""
+    dt = torch.bfloat16
+    z = torch.tensor([[-3e38, -1e20, -1e13, -1e4, -200, 200, 1e4, 1e13, 1e18, 3e38]], dtype=dt, device=DEV)
+    z = torch.cat([z, z[:, :6]], 1)  # 16 values
+    eye = torch.eye(16, dtype=dt, device=DEV)
+    one = torch.ones(1, 16, dtype=dt, device=DEV)
+    up = z > 0
+    for j in range(16):  # one value at a time: 0 * z of the others stays finite, z * 1 exact
+        x = torch.zeros(1, 16, dtype=dt, device=DEV)
+        x[0, j] = z[0, j]
+        y = sa.dense_linear(x, eye, act=act)
+        assert y[0, j] == (z[0, j] if up[0, j] else 0)
+    dx, _, db = sa.dense_linear_backward(one, one, eye, act=act, pre=z, with_dbias=True)
+    assert torch.equal(dx, up.to(dt)) and torch.equal(db, up[0].to(dt))
+    g = sa.gated_linear_backward(one, one, eye, eye, z, torch.zeros_like(one), act=act)[0]
+    assert torch.equal(g, torch.where(up, z, 0 * z).to(dt))
 
 
 def test_no_rows():

@@ -214,7 +214,7 @@ def test_plans(sa):
     assert sa.sa_linear_plan(6, 1, 64, 64, P, P, P, P) == INVALID
     assert sa.sa_linear_plan(0, 1, 60, 64, P, P, P, P) == INVALID
     assert sa.sa_linear_plan(0, 1, 64, 64, None, P, P, P) == INVALID
-    assert sa.sa_set_linear_tuning(5, 0) == INVALID
+    assert sa.sa_set_linear_tuning(6, 0) == INVALID
     assert sa.sa_set_linear_tuning(0, 513) == INVALID
     assert sa.sa_set_linear_tuning(-2, 0) == INVALID
     assert sa.sa_set_linear_tuning(-1, -1) == OK
