@@ -525,16 +525,20 @@ struct Operand {
 // arrived.  Loads past the last item read zeros, so counts never change.
 // gfx950 at 256 x 256: 64 KB per stage, two stages, one wave per SIMD with
 // 256 sums in accumulation registers.
+template <int LAY, int BM, int BN, int NS>
+constexpr int lin_lds() {
+  return NS * (Operand<LAY == kDw, BM>::kBytes +
+               Operand<LAY != kDx, LAY != kDx ? (BN + 127) / 128 * 128 : BN>::kBytes);
+}
+// Workgroup `block` of `blocks`, with lin_lds bytes at S.
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
+__device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, uint8_t* S) {
   constexpr bool PNC = LAY == kDw, QNC = LAY != kDx;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   static_assert(WM * WN == 4 && MB >= 1 && NB >= 2 && NB % (GATED ? 4 : 2) == 0, "four waves");
   using OP = Operand<PNC, BM>;
   using OQ = Operand<QNC, QNC ? (BN + 127) / 128 * 128 : BN>;  // NC: whole halves are loaded
   constexpr int L = OP::I + OQ::I;
-  constexpr int kStage = OP::kBytes + OQ::kBytes;
-  __shared__ __align__(16) uint8_t S[NS * kStage];
   const uint32_t lp = lds_addr(S), lq = lp + NS * OP::kBytes;
 
   constexpr int N = MB * NB, R = MB + NB;
@@ -572,9 +576,9 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   // Row tiles that read the same weights are kept on one XCD; with a single
   // one nothing is shared, and neighbouring shares on different XCDs stream
   // faster (one row of 4096 x 4096: 11.4 -> 11.1 us).
-  const int share = !split ? 0 : mt == 1 ? (int)blockIdx.x : (int)xcd_run(blockIdx.x, gridDim.x);
+  const int share = !split ? 0 : mt == 1 ? block : (int)xcd_run(block, blocks);
   const int lg = split ? __builtin_ctz(p.split) : 0;
-  const int begin = split ? (int)((uint32_t)share * (uint32_t)(tiles * steps) >> lg) : (int)blockIdx.x;
+  const int begin = split ? (int)((uint32_t)share * (uint32_t)(tiles * steps) >> lg) : block;
   const int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)(tiles * steps) >> lg) : tiles;
   struct Item {
     int m0, n0, out, s0, s1, next;
@@ -593,7 +597,7 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
       tile_of(cur, tiles, mt, nt, mi, ni);
       it.s0 = 0;
       it.s1 = steps;
-      it.next = cur + (int)gridDim.x;
+      it.next = cur + blocks;
     }
     it.out = ni >= nt1;
     it.m0 = mi * BM;
@@ -993,6 +997,29 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
   }
   stage_barrier<0, 0>();  // no load may land in LDS after the workgroup's end
 }
+
+template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
+  __shared__ __align__(16) uint8_t S[lin_lds<LAY, BM, BN, NS>()];
+  lin_run<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S);
+}
+
+// Small gradients: dx (the first `first` workgroups) and dW in one launch, a
+// workgroup of each on a CU.  One after the other, each leaves the chip
+// waiting for its own latency (the whole backward call of 509 rows 1024 ->
+// 4096: 34.8 -> 28.1 us, gated with 300 rows 39.5 -> 33.8).
+template <int DT, int XM>
+__global__ __launch_bounds__(256, 1) void k_lin_pair(LinP x, LinP w, int first) {
+  constexpr int NX = XM == 64 ? 3 : 2, WX = XM == 64 ? 1 : 2;
+  constexpr int lx = lin_lds<kDx, XM, 128, NX>(), lw = lin_lds<kDw, 128, 128, 2>();
+  __shared__ __align__(16) uint8_t S[lx > lw ? lx : lw];
+  if ((int)blockIdx.x < first)
+    lin_run<DT, kDx, false, kPlain, XM, 128, WX, 4 / WX, NX>(x, blockIdx.x, first, S);
+  else
+    lin_run<DT, kDw, false, kPlain, 128, 128, 2, 2, 2>(w, (int)blockIdx.x - first,
+                                                       (int)gridDim.x - first, S);
+}
+
 // Sums the shares' partials of each tile (2^lbm x 2^lbn outputs) and finishes the outputs, 8
 // columns of a row per thread, or (groups = kChains, for few outputs) one of
 // their chains per thread.
@@ -1251,11 +1278,21 @@ size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int64_t K, int segs, int
 
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const LinP& p, int64_t items, hipStream_t s) {  // items: shares or tiles
-  constexpr int lds = NS * (Operand<LAY == kDw, BM>::kBytes +
-                            Operand<LAY != kDx, LAY != kDx ? (BN + 127) / 128 * 128 : BN>::kBytes);
-  constexpr int64_t most = kCus * (160 * 1024 / lds);  // workgroups that run at once
+  constexpr int64_t most = kCus * (160 * 1024 / lin_lds<LAY, BM, BN, NS>());  // workgroups that run at once
   const dim3 grid((unsigned)(p.split || items < most ? items : most));
   hipLaunchKernelGGL((k_lin<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+}
+
+template <int DT, bool GATED>
+hipError_t launch_reduce(const LinP& p, const Plan& pl, hipStream_t s) {
+  const int64_t octets = (int64_t)p.M * p.outs * (p.N / 8);
+  // a thread per chain while that is less than a workgroup per CU
+  const int groups = octets * kChains <= kCus * 256 ? kChains : 1;
+  const int64_t n = (octets * groups + 255) / 256;
+  if (n > 0x7fffffffLL) return hipErrorNotSupported;
+  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups,
+                     __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(GATED ? 128 : kTileN[pl.tile]));
+  return hipGetLastError();
 }
 
 template <int DT, int LAY, bool GATED>
@@ -1295,16 +1332,31 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
     else if (pl.tile == 3) launch_tile<DT, LAY, GATED, EPI, 32, SB, 1, 4, GATED ? 4 : 3>(p, groups_of_work, s);
     else launch_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, 4>(p, groups_of_work, s);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !pl.split || p.tickets) return e;
-  const int64_t octets = (int64_t)p.M * p.outs * (p.N / 8);
-  // a thread per chain while that is less than a workgroup per CU
-  const int groups = octets * kChains <= kCus * 256 ? kChains : 1;
-  const int64_t n = (octets * groups + 255) / 256;
-  if (n > 0x7fffffffLL) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups,
-                     __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(GATED ? 128 : kTileN[pl.tile]));
-  return hipGetLastError();
+  return launch_reduce<DT, GATED>(p, pl, s);
+}
+
+// dx and dW of one backward call; whichever is split has ws to itself when it runs.
+template <int DT>
+hipError_t launch_gradients(LinP x, LinP w, void* ws, hipStream_t s) {
+  const Plan px = lin_plan(kDx, false, x.M, x.N, x.K, x.segs, x.outs);
+  const Plan pw = lin_plan(kDw, false, w.M, w.N, w.K, w.segs, w.outs);
+  const bool pair = px.tiles > 0 && (px.tile == 1 || px.tile == 2) && pw.tile == 1 && !pw.split &&
+                    (px.split || px.tiles <= kCus) && pw.tiles <= 2 * kCus;
+  if (!pair) {
+    hipError_t e = launch_lin<DT, kDx, false>(x, ws, s);
+    return e != hipSuccess ? e : launch_lin<DT, kDw, false>(w, ws, s);
+  }
+  x.split = px.split;
+  x.part = reinterpret_cast<float*>(ws);
+  w.split = 0;
+  const int first = px.split ? px.split : (int)px.tiles;
+  const dim3 grid((unsigned)(first + pw.tiles));
+  if (px.tile == 2) hipLaunchKernelGGL((k_lin_pair<DT, 64>), grid, dim3(256), 0, s, x, w, first);
+  else hipLaunchKernelGGL((k_lin_pair<DT, 128>), grid, dim3(256), 0, s, x, w, first);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || !px.split ? e : launch_reduce<DT, false>(x, px, s);
 }
 
 // Rows per strip of the elementwise kernel (a workgroup's): 16 for small T
@@ -1394,42 +1446,35 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (c.dx) {
-    LinP p{};
-    p.p[0] = d[0];
-    p.p[1] = d[1];
-    p.ldp = (int)ldd;
-    for (int i = 0; i < 2; ++i) {
-      p.q[i] = c.w[i];
-      p.ldq[i] = (int)c.ldw[i];
-    }
-    p.M = (int)c.T;
-    p.N = (int)c.d_in;
-    p.K = (int)c.d_out;
-    p.segs = c.gated ? 2 : 1;
-    p.outs = 1;
-    p.y[0] = c.dx;
-    p.ldy[0] = (int)c.lddx;
-    e = launch_lin<DT, kDx, false>(p, ws, s);
-    if (e != hipSuccess) return e;
+  LinP x{}, w{};
+  x.p[0] = d[0];
+  x.p[1] = d[1];
+  x.ldp = (int)ldd;
+  w.p[0] = c.x;
+  w.ldp = (int)c.ldx;
+  for (int i = 0; i < 2; ++i) {
+    x.q[i] = c.w[i];
+    x.ldq[i] = (int)c.ldw[i];
+    w.q[i] = d[i];
+    w.ldq[i] = (int)ldd;
+    w.y[i] = c.dw[i];
+    w.ldy[i] = (int)c.lddw[i];
   }
-  if (c.dw[0]) {
-    LinP p{};
-    p.p[0] = c.x;
-    p.ldp = (int)c.ldx;
-    for (int i = 0; i < 2; ++i) {
-      p.q[i] = d[i];
-      p.ldq[i] = (int)ldd;
-      p.y[i] = c.dw[i];
-      p.ldy[i] = (int)c.lddw[i];
-    }
-    p.M = (int)c.d_in;
-    p.N = (int)c.d_out;
-    p.K = (int)c.T;
-    p.segs = 1;
-    p.outs = c.gated ? 2 : 1;
-    e = launch_lin<DT, kDw, false>(p, ws, s);
-  }
+  x.y[0] = c.dx;
+  x.ldy[0] = (int)c.lddx;
+  x.M = (int)c.T;
+  x.N = (int)c.d_in;
+  x.K = (int)c.d_out;
+  x.segs = c.gated ? 2 : 1;
+  x.outs = 1;
+  w.M = (int)c.d_in;
+  w.N = (int)c.d_out;
+  w.K = (int)c.T;
+  w.segs = 1;
+  w.outs = c.gated ? 2 : 1;
+  if (c.dx && c.dw[0]) return launch_gradients<DT>(x, w, ws, s);
+  if (c.dx) return launch_lin<DT, kDx, false>(x, ws, s);
+  if (c.dw[0]) return launch_lin<DT, kDw, false>(w, ws, s);
   return e;
 }
 
