@@ -29,7 +29,7 @@
 //     and 1158 in dW's.
 //   few rows: the weights' stream.  1 x 4096 x 11008 gate and up 35 us (180
 //     MB: 5.1 TB/s; a plain read runs at 7.2, a copy at 5.1), 8 x 11008 x
-//     4096 19 us, 1 x 4096 x 4096 12 us (most of it launch and fill).
+//     4096 19 us, 1 x 4096 x 4096 10 us (most of it launch and fill).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
