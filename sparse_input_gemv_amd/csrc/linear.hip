@@ -1222,11 +1222,11 @@ int64_t slots_of(const Plan& pl, int64_t steps) {
 // with two (throughput; gated small tiles run alone), in us, measured over
 // sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
 // 3 us for the reduction's launch and the partials' bytes at 4 TB/s; one
-// row tile streams its weights at 26 GB/s per CU at most.
+// row tile (gated: up to four) streams its weights at 26 GB/s per CU at most.
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
                                           {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
-  static const double paired[kTiles] = {0, 0.50, 0.28, 0.25, 0.22, 0};
+  static const double paired[kTiles] = {0, 0.50, 0.36, 0.25, 0.22, 0};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
   Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
   double least = 1e30;
@@ -1236,11 +1236,12 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     const bool forced = g_lin_tile >= 0 && !(lay == kDw && g_lin_tile > 1 && g_lin_tile != kNarrow) &&
                         !(g_lin_tile == kNarrow && gated);
     if (forced && t != g_lin_tile) continue;
-    if (g_lin_tile < 0 && M <= 64 && kTileM[t] < M) continue;  // one row tile holds them all
+    // up to 64 rows in one row tile, more in tiles of 64 at least
+    if (g_lin_tile < 0 && kTileM[t] < (M < 64 ? M : 64)) continue;
     const int64_t tiles = tiles_of(t, gated, M, N, outs);
     const bool pairs = t > 0 && t != kNarrow && !gated;
     double step = alone[gated][t];
-    if (M <= kTileM[t]) {
+    if (t > 0 && M <= (gated ? 4 : 1) * kTileM[t]) {
       const double stream = (gated ? 32768 : kTileN[t] * 128) / 26e3 + 0.1 * step;
       step = stream > step ? stream : step;
     }
@@ -1253,9 +1254,13 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
       least = whole;
       best = Plan{t, 0, tiles};
     }
-    // split over one workgroup per CU, at least four steps each (two: 33 rows
-    // of 4096 x 1024 10.9 us against 10.1)
-    int64_t shares = tiles * steps / 4 < kCus ? tiles * steps / 4 : kCus;
+    // split over one workgroup per CU, of four steps each at least (33 rows of
+    // 4096 x 1024 10.1 us, two steps 10.9), down to two for 128 shares (8
+    // rows of 880 x 3704, dx: 9.0, four 10.5) and one for 64
+    const int64_t TS = tiles * steps;
+    int64_t shares = TS / 4 < kCus ? TS / 4 : kCus;
+    if (shares < 128) shares = TS / 2 < 128 ? TS / 2 : 128;
+    if (shares < 64) shares = TS < 64 ? TS : 64;
     if (g_lin_split > 0) shares = g_lin_split < tiles * steps ? g_lin_split : tiles * steps;
     if (g_lin_split == 0 || t == kNarrow || shares < 1 || tiles * steps >= (1 << 22)) continue;
     while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
