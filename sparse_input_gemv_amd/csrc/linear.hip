@@ -1221,8 +1221,10 @@ int64_t slots_of(const Plan& pl, int64_t steps) {
 // time with one workgroup on a CU (latency) and each workgroup's part of it
 // with two (throughput; gated small tiles run alone), in us, measured over
 // sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
-// 3 us for the reduction's launch and the partials' bytes at 4 TB/s; one
-// row tile (gated: up to four) streams its weights at 26 GB/s per CU at most.
+// 3 us for the reduction's launch (7 with 256 x 256 tiles) and the partials'
+// bytes at 4 TB/s; one row tile streams its weights at 26 GB/s per CU at most
+// (gated: up to four share them at 40).  Over 88 random shapes the choice
+// took 2 to 3 percent longer than the best of a sweep, on average.
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
                                           {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
@@ -1242,7 +1244,7 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     const bool pairs = t > 0 && t != kNarrow && !gated;
     double step = alone[gated][t];
     if (t > 0 && M <= (gated ? 4 : 1) * kTileM[t]) {
-      const double stream = (gated ? 32768 : kTileN[t] * 128) / 26e3 + 0.1 * step;
+      const double stream = (gated ? 32768 : kTileN[t] * 128) / (M <= kTileM[t] ? 26e3 : 40e3) + 0.1 * step;
       step = stream > step ? stream : step;
     }
     // whole tiles
@@ -1267,7 +1269,7 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     if (g_lin_split < 0 && (tiles >= shares || steps < 2)) continue;
     const double rows = M < kTileM[t] ? M : kTileM[t];
     const double parts = (shares + tiles) * rows * (gated ? 256 : kTileN[t]) * 8.0 / 4e6;
-    const double time = (double)tiles * steps / shares * step + 7 + parts;
+    const double time = (double)tiles * steps / shares * step + (t == 0 ? 11 : 7) + parts;
     if (time < least) {
       least = time;
       best = Plan{t, (int)shares, tiles};
