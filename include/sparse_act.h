@@ -517,7 +517,8 @@ int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
  * - `ws` is a device workspace of at least the bytes the call's
  *   *_workspace_bytes function names (16-byte aligned; its contents on entry
  *   do not matter; NULL allowed when that is 0).  Calls that share one must
- *   be ordered on one stream.
+ *   be ordered on one stream.  The backward calls' sizes are fp16's, which
+ *   holds a second copy of d; bf16 needs less.
  * - `tickets` (forward calls) is NULL, or SA_LINEAR_TICKET_BYTES of device
  *   memory, 16-byte aligned, zero before its first use and left zero by every
  *   call.  With it, calls of at most 64 rows sum their split products in the
@@ -557,6 +558,11 @@ size_t dense_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
  *   dx = d W;  dwt = x^T d (the transposed layout);  dbias = sum over rows
  *   of d.  The residual's gradient is dy itself.
  * d is rounded to `dtype` before the two products (dbias sums it unrounded).
+ * SA_F16: rows of d (for dx) and columns of d (for dwt) whose largest entry m
+ * lies outside [2^-8, 2^15) are scaled by a power of two while d is fp16, so
+ * d may pass 65504 or fp16's subnormals where dx and dwt do not.  An entry is
+ * off by half a step, 2^-11 of itself, or 2^-17 m where it is small.  (Inf or
+ * NaN in an entry makes its row of dx and its column of dwt Inf or NaN.)
  *   dy, pre [T][d_out] (pre NULL allowed when act is none); dx [T][d_in],
  *   dwt [d_in][d_out], dbias [d_out]: each NULL when not wanted.
  */
@@ -586,7 +592,8 @@ size_t gated_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
 /*
  * gated_linear_backward -- the gradients of gated_linear from dh:
- *   dg = dh * u * act'(g), du = dh * act(g), rounded to `dtype`;
+ *   dg = dh * u * act'(g), du = dh * act(g), rounded to `dtype` as in
+ *   dense_linear_backward (for dx, m is the larger of dg's and du's row);
  *   dx = dg Wg + du Wu;  dwgt = x^T dg;  dwut = x^T du.
  *   dh, g, u [T][d_out]; dx [T][d_in] or NULL; dwgt, dwut [d_in][d_out],
  *   both or neither NULL.

@@ -675,12 +675,13 @@ size_t gated_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
 size_t dense_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int act,
                                              int with_dbias) {
   if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, act) != SA_OK) return 0;
-  return sa::linear_backward_workspace_bytes(false, T, d_in, d_out, act, with_dbias != 0);
+  // fp16's need: it holds bf16's
+  return sa::linear_backward_workspace_bytes(SA_F16, false, T, d_in, d_out, act, with_dbias != 0);
 }
 
 size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out) {
   if (sa::check_linear_sizes("", SA_F16, T, d_in, d_out, 0) != SA_OK) return 0;
-  return sa::linear_backward_workspace_bytes(true, T, d_in, d_out, 0, false);
+  return sa::linear_backward_workspace_bytes(SA_F16, true, T, d_in, d_out, 0, false);
 }
 
 int dense_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
@@ -807,7 +808,7 @@ int dense_linear_backward(int dtype, const void* dy, int64_t lddy, const void* x
   if (st == SA_OK) st = sa::check_linear_distinct(fn, "dx", dx, "dwt", dwt);
   if (st == SA_OK)
     st = sa::check_linear_ws(fn, ws, ws_bytes,
-                             sa::linear_backward_workspace_bytes(false, T, d_in, d_out, act,
+                             sa::linear_backward_workspace_bytes(dtype, false, T, d_in, d_out, act,
                                                                  dbias != nullptr));
   if (st != SA_OK) return st;
   sa::LinearCall c;
@@ -864,7 +865,7 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
   }
   if (st == SA_OK)
     st = sa::check_linear_ws(fn, ws, ws_bytes,
-                             sa::linear_backward_workspace_bytes(true, T, d_in, d_out, act, false));
+                             sa::linear_backward_workspace_bytes(dtype, true, T, d_in, d_out, act, false));
   if (st != SA_OK) return st;
   sa::LinearCall c;
   c.dtype = dtype;

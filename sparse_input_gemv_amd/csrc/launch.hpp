@@ -182,8 +182,8 @@ struct LinearCall {
 };
 constexpr size_t kLinearTicketBytes = (size_t)512 * 4 * 128;  // 512 tiles, four waves, a line each
 size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out);
-size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
-                                       bool dbias);
+size_t linear_backward_workspace_bytes(int dtype, bool gated, int64_t T, int64_t d_in, int64_t d_out,
+                                       int act, bool dbias);
 int linear_set_tuning(int tile, int split);
 int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* split,
                 int64_t* tiles);

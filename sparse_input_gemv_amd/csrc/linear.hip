@@ -243,8 +243,9 @@ constexpr int kTicketTiles = 512;
 enum Layout { kFwd = 0, kDx = 1, kDw = 2 };
 // Epilogues, each compiled by itself (the general one needs registers that
 // the plain one's K loop would have to give up): the sums as they are (gated:
-// h alone), plus the residual, or everything.
-enum Epilogue { kPlain = 0, kResidual = 1, kGeneral = 2 };
+// h alone), plus the residual, or everything; for fp16 gradients, the sums
+// times their row's (dx) or column's (dW) power of two.
+enum Epilogue { kPlain = 0, kResidual = 1, kGeneral = 2, kScaled = 3 };
 
 struct LinP {
   const uint16_t* p[2];  // row operand (per K segment)
@@ -266,6 +267,11 @@ struct LinP {
   int ldy[2];
   uint16_t* pre[2];      // pre-activation, or g and u
   int ldpre[2];
+  // scaled gradients (fp16), or NULL: powers of two that undo d's scales
+  const float* rs;       // dx: [M]
+  const float* cs;       // dW: [outs][N]
+  const uint32_t* scaled;  // dx: not 0: the row operand is alt, not p
+  const uint16_t* alt[2];
 };
 
 // f(0), ..., f(N - 1) with compile-time arguments.
@@ -346,8 +352,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* m, i
 }
 
 // Eight outputs of row m from column n on (n a multiple of 8 below N).
-template <int DT>
+template <int DT, bool SCALED>
 __device__ __forceinline__ void finish_linear(const LinP& p, int o, int64_t m, int n, F8 f) {
+  if constexpr (SCALED) {
+    const float r = p.rs ? p.rs[m] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] *= p.cs ? p.cs[(int64_t)o * p.N + n + i] : r;
+  }
   if (p.bias) {
     const F8 b = load8<DT>(p.bias + n);
 #pragma unroll
@@ -612,6 +623,13 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
   const int qh = GATED ? (w * OQ::I) / 16 : 0;
   op.init(w, p.ldp);
   oq.init(w, qh ? p.ldq[1] : p.ldq[0]);
+  const uint16_t *p0 = p.p[0], *p1 = p.p[1];
+  if constexpr (EPI == kScaled && LAY == kDx) {
+    if (p.scaled && uni((int)*p.scaled)) {
+      p0 = p.alt[0];
+      p1 = p.alt[1];
+    }
+  }
   Item li = item_at(begin);
   int at = li.s0;  // its step
   int stop = 0;    // the step at which the segment or the item ends
@@ -624,7 +642,7 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
     stop = uni(!seg && ks < li.s1 ? ks : li.s1);
     if (LAY == kDx && p.segs == 2) oq.init(w, seg ? p.ldq[1] : p.ldq[0]);
     const bool second = GATED ? qh : LAY == kDx ? seg : LAY == kDw ? li.out : 0;
-    op.start(LAY == kDx && seg ? p.p[1] : p.p[0], li.m0, p.M, k0, w);
+    op.start(LAY == kDx && seg ? p1 : p0, li.m0, p.M, k0, w);
     // gated: half 0 is g's columns, half 1 u's, both from n0 on
     oq.start(second ? p.q[1] : p.q[0], GATED ? li.n0 - 128 * qh : li.n0, p.N, k0, w);
   };
@@ -823,7 +841,7 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
       }
       const F8 fs = add_chains(f);
       if constexpr (GATED) finish_gated<DT>(p, m, n, fs, add_chains(u));
-      else finish_linear<DT>(p, it.out, m, n, fs);
+      else finish_linear<DT, EPI == kScaled>(p, it.out, m, n, fs);
     }
   };
   auto finish_parts = [&](const Item& it) SA_INLINE {
@@ -901,7 +919,8 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
         }
       });
     } else {
-      const bool hr = mode >= kResidual && p.res, hp = mode == kGeneral && p.pre[0], hb = mode == kGeneral && p.bias;
+      constexpr bool residual = mode == kResidual || mode == kGeneral;
+      const bool hr = residual && p.res, hp = mode == kGeneral && p.pre[0], hb = mode == kGeneral && p.bias;
       const auto rr = rows_rsrc(hr ? p.res : p.y[0], hr ? p.ldr : 0, it.m0, hr ? rows : 1, hr ? p.N : 0);
       const auto pr = rows_rsrc(hp ? p.pre[0] : p.y[0], hp ? p.ldpre[0] : 0, it.m0, hp ? rows : 1, hp ? p.N : 0);
       const auto br = __builtin_amdgcn_make_buffer_rsrc((void*)uni(hb ? p.bias : p.y[0]), 0,
@@ -915,7 +934,35 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
 #pragma unroll
         for (int b = 0; b < NO / 2; ++b) bv[b] = __builtin_amdgcn_raw_buffer_load_b128(br, col[b], 0, 0);
       }
-      if constexpr (mode >= kResidual) {
+      // a row's or a column's scale: a lane's rows or columns of the tile
+      float rsv[MB];
+      F8 csv[NO / 2];
+      if constexpr (mode == kScaled && LAY == kDx) {
+        const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)uni(p.rs), 0, uni(p.rs ? p.M * 4 : 0), 0x00020000);
+#pragma unroll
+        for (int a = 0; a < MB; ++a) {
+          const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(r, (uint32_t)(it.m0 + row + 16 * a) * 4, 0, 0);
+          rsv[a] = p.rs ? __builtin_bit_cast(float, v) : 1.f;
+        }
+      }
+      if constexpr (mode == kScaled && LAY == kDw) {
+        const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)uni(p.cs + (it.out ? p.N : 0)), 0,
+                                                         uni(p.cs ? p.N * 4 : 0), 0x00020000);
+#pragma unroll
+        for (int b = 0; b < NO / 2; ++b) {
+          const uint32_t n = it.n0 + (wn * NO + 2 * b + (g & 1)) * 16 + 8 * (g >> 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, n * 4 + 16 * h, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = v[e];
+              csv[b].v[4 * h + e] = p.cs ? __builtin_bit_cast(float, x) : 1.f;
+            }
+          }
+        }
+      }
+      if constexpr (residual) {
 #pragma unroll
         for (int b = 0; b < NO / 2; ++b)
           rv[0][b] = __builtin_amdgcn_raw_buffer_load_b128(rr, ro + col[b], 0, 0);
@@ -923,7 +970,7 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
       static_for<MB>([&](auto A) {
         constexpr int a = decltype(A)::value;
         take_row(a);
-        if constexpr (mode >= kResidual) {
+        if constexpr (residual) {
           if constexpr (a + 1 < MB) {
 #pragma unroll
             for (int b = 0; b < NO / 2; ++b)
@@ -941,7 +988,11 @@ __device__ __forceinline__ void lin_run(const LinP& p, int block, int blocks, ui
             __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
             act8(p.act, f);
           }
-          if constexpr (mode >= kResidual) {
+          if constexpr (mode == kScaled) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] *= LAY == kDx ? rsv[a] : csv[b / 2].v[e];
+          }
+          if constexpr (residual) {
             const F8 r = widen8<DT>(rv[a & 1][b / 2]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f.v[e] += r.v[e];
@@ -1011,12 +1062,13 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
 template <int DT, int XM>
 __global__ __launch_bounds__(256, 1) void k_lin_pair(LinP x, LinP w, int first) {
   constexpr int NX = XM == 64 ? 3 : 2, WX = XM == 64 ? 1 : 2;
+  constexpr int EPI = DT == SA_F16 ? kScaled : kPlain;
   constexpr int lx = lin_lds<kDx, XM, 128, NX>(), lw = lin_lds<kDw, 128, 128, 2>();
   __shared__ __align__(16) uint8_t S[lx > lw ? lx : lw];
   if ((int)blockIdx.x < first)
-    lin_run<DT, kDx, false, kPlain, XM, 128, WX, 4 / WX, NX>(x, blockIdx.x, first, S);
+    lin_run<DT, kDx, false, EPI, XM, 128, WX, 4 / WX, NX>(x, blockIdx.x, first, S);
   else
-    lin_run<DT, kDw, false, kPlain, 128, 128, 2, 2, 2>(w, (int)blockIdx.x - first,
+    lin_run<DT, kDw, false, EPI, 128, 128, 2, 2, 2>(w, (int)blockIdx.x - first,
                                                        (int)gridDim.x - first, S);
 }
 
@@ -1080,7 +1132,7 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm,
   if constexpr (GATED) {
     finish_gated<DT>(p, row, n, add_chains(f), add_chains(u));
   } else {
-    finish_linear<DT>(p, out, row, n, add_chains(f));
+    finish_linear<DT, DT == SA_F16>(p, out, row, n, add_chains(f));
   }
 }
 
@@ -1091,6 +1143,19 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm,
 // values and writes 1 (2) per entry.  A wave takes 512 columns (8 per lane:
 // 16-byte accesses) of a quarter of a strip, kDactRows rows at a time so that
 // their loads are in flight together; the four waves' sums meet in LDS.
+//
+// fp16 holds 2^-24 to 65504, d up to 2^49 and far smaller ones, where dx and
+// dW may well be ordinary numbers.  So its rows (for dx) and columns (for dW)
+// whose largest |d| m lies outside [2^-8, 2^15) are scaled to [2^14, 2^15) by
+// a power of two, which the products' epilogues undo in fp32.  A d is rounded
+// to half a step or, where it is small, to 2^-17 m (half a subnormal step) at
+// worst.  Three launches, as a scale has to be known before a value is
+// rounded: kFind writes the unscaled d and the largest |d| of every row and
+// column of its block; k_lin_scales finds the scales; kApply returns at once
+// if all are 1, as in most training steps, or else evaluates d again and
+// writes it by rows' scales (another buffer, which dx then reads) and by
+// columns' (over the unscaled d).
+enum Scaling { kNone = 0, kFind = 1, kApply = 2 };
 struct DactP {
   const uint16_t *dy, *a, *b;  // a: pre or g; b: u
   int64_t lddy, lda, ldb;
@@ -1098,74 +1163,224 @@ struct DactP {
   float* sums;                 // [strips][N] or NULL
   int64_t T, N, strip;
   int act;
+  // scaling (fp16); with dx (dW) not wanted the rows' (columns') are NULL
+  uint16_t *e0, *e1;           // [T][N]: d by rows' scales
+  float *rmax, *cmax;          // [T][column blocks], [strips][outs][N]: largest |d|
+  float *rs, *cs;              // [T], [outs][N]: the scales' reciprocals
+  uint32_t* scaled;            // not 0: some scale is not 1
+};
+// The reciprocal of the scale for values up to m.  Rows and columns with Inf
+// or NaN have no use for one: all they reach is Inf or NaN.
+__device__ __forceinline__ float unscale_of(float m) {
+  const int e = (int)(__builtin_bit_cast(uint32_t, m) >> 23) - 127;
+  if (m == 0.f || e > 127 || (e >= -8 && e < 15)) return 1.f;
+  const int by = 14 - e < 64 ? 14 - e : 64;  // 2^-78 reaches no fp16 output; -35 at least
+  return __builtin_bit_cast(float, (uint32_t)(127 - by) << 23);
+}
+__device__ __forceinline__ float reciprocal_pow2(float u) {
+  return __builtin_bit_cast(float, (254u << 23) - __builtin_bit_cast(uint32_t, u));
+}
+// The largest of the wave's values, none of them negative, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+  auto shifted = [&](auto C) {
+    const int x = __builtin_bit_cast(int, v);
+    v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, decltype(C)::value, 0xf, 0xf, true)));
+  };
+  shifted(std::integral_constant<int, 0x111>{});  // row_shr:1
+  shifted(std::integral_constant<int, 0x112>{});
+  shifted(std::integral_constant<int, 0x114>{});
+  shifted(std::integral_constant<int, 0x118>{});
+  const int x = __builtin_bit_cast(int, v);
+  const int r0 = __builtin_amdgcn_readlane(x, 15), r1 = __builtin_amdgcn_readlane(x, 31);
+  const int r2 = __builtin_amdgcn_readlane(x, 47), r3 = __builtin_amdgcn_readlane(x, 63);
+  return fmaxf(fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1)),
+               fmaxf(__builtin_bit_cast(float, r2), __builtin_bit_cast(float, r3)));
+}
+struct DactLane {
+  float sum[8];   // column sums
+  float m0[8], m1[8];  // kFind: largest |d0|, |d1| of a column; kApply: the columns' scales
 };
 constexpr int kDactRows = 4;
-template <int DT, bool GATED, int ACT>
-__device__ __forceinline__ void dact_rows(const DactP& p, int64_t n, int64_t t0, int64_t t1,
-                                          float (&sum)[8]) {
+// `in`: the lane's columns exist; if not it reads column 0 and writes nothing.
+template <int DT, bool GATED, int ACT, int SCALING>
+__device__ __forceinline__ void dact_rows(const DactP& p, int64_t n, bool in, int64_t t0, int64_t t1,
+                                          DactLane& l) {
+  constexpr bool map = GATED || ACT != SA_ACT_NONE;
   for (int64_t t = t0; t < t1; t += kDactRows) {
     u16x8 dy[kDactRows], a[kDactRows], b[kDactRows];
 #pragma unroll
     for (int r = 0; r < kDactRows; ++r) {
       const int64_t tr = t + r < t1 ? t + r : t1 - 1;
       dy[r] = *reinterpret_cast<const u16x8*>(p.dy + tr * p.lddy + n);
-      if constexpr (GATED || ACT != SA_ACT_NONE)
-        a[r] = *reinterpret_cast<const u16x8*>(p.a + tr * p.lda + n);
+      if constexpr (map) a[r] = *reinterpret_cast<const u16x8*>(p.a + tr * p.lda + n);
       if constexpr (GATED) b[r] = *reinterpret_cast<const u16x8*>(p.b + tr * p.ldb + n);
     }
 #pragma unroll
     for (int r = 0; r < kDactRows; ++r) {
       if (t + r >= t1) break;
-      u16x8 o0, o1;
+      u16x8 o0, o1, q0, q1;
+      float most = 0.f, by = 1.f;
+      if constexpr (SCALING == kApply) by = p.rs ? reciprocal_pow2(p.rs[t + r]) : 1.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float v = to_f<DT>(dy[r][e]);
         float f = 0.f, df = 1.f;
-        if constexpr (GATED || ACT != SA_ACT_NONE) act_both<ACT>(to_f<DT>(a[r][e]), f, df);
+        if constexpr (map) act_both<ACT>(to_f<DT>(a[r][e]), f, df);
+        float x, y = 0.f;
         if constexpr (GATED) {
-          o0[e] = from_f<DT>(v * to_f<DT>(b[r][e]) * df);
-          o1[e] = from_f<DT>(v * f);
+          x = v * to_f<DT>(b[r][e]) * df;
+          y = v * f;
         } else {
-          const float d = v * df;
-          sum[e] += d;
-          o0[e] = from_f<DT>(d);
+          x = v * df;
+          l.sum[e] += x;
+        }
+        if constexpr (SCALING == kFind) {
+          l.m0[e] = fmaxf(l.m0[e], fabsf(x));
+          most = fmaxf(most, fabsf(x));
+          if constexpr (GATED) {
+            l.m1[e] = fmaxf(l.m1[e], fabsf(y));
+            most = fmaxf(most, fabsf(y));
+          }
+        }
+        if constexpr (SCALING == kApply) {
+          q0[e] = from_f<DT>(x * by);
+          x *= l.m0[e];
+          if constexpr (GATED) {
+            q1[e] = from_f<DT>(y * by);
+            y *= l.m1[e];
+          }
+        }
+        o0[e] = from_f<DT>(x);
+        if constexpr (GATED) o1[e] = from_f<DT>(y);
+      }
+      const int64_t at = (t + r) * p.N + n;
+      if (in && (SCALING != kApply || p.cs)) {
+        if constexpr (map) *reinterpret_cast<u16x8*>(p.d0 + at) = o0;
+        if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + at) = o1;
+      }
+      if constexpr (SCALING == kFind) {
+        most = wave_max(in ? most : 0.f);
+        if (lane_id() == 0) p.rmax[(t + r) * gridDim.x + blockIdx.x] = most;
+      }
+      if constexpr (SCALING == kApply) {
+        if (in && p.rs) {
+          *reinterpret_cast<u16x8*>(p.e0 + at) = q0;
+          if constexpr (GATED) *reinterpret_cast<u16x8*>(p.e1 + at) = q1;
         }
       }
-      if constexpr (GATED || ACT != SA_ACT_NONE)
-        *reinterpret_cast<u16x8*>(p.d0 + (t + r) * p.N + n) = o0;
-      if constexpr (GATED) *reinterpret_cast<u16x8*>(p.d1 + (t + r) * p.N + n) = o1;
     }
   }
 }
-template <int DT, bool GATED>
+template <int DT, bool GATED, int SCALING>
 __global__ __launch_bounds__(256) void k_lin_dact(DactP p) {
+  static_assert(SCALING == kNone || DT == SA_F16, "bf16 has fp32's range");
   __shared__ float part[4][64][9];  // 9: the lanes' rows in different banks
+  if constexpr (SCALING == kApply) {
+    if (!*p.scaled) return;
+  }
+  if constexpr (SCALING == kFind) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scaled = 0;
+  }
   const int lane = lane_id(), w = (int)threadIdx.x / kWave;
-  const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 8;
+  int64_t n = ((int64_t)blockIdx.x * 64 + lane) * 8;
   const bool in = n < p.N;
+  n = in ? n : 0;
   const int64_t quarter = (p.strip + 3) / 4;
   const int64_t s0 = blockIdx.y * p.strip, send = s0 + p.strip < p.T ? s0 + p.strip : p.T;
   const int64_t t0 = s0 + w * quarter, t1 = t0 + quarter < send ? t0 + quarter : send;
-  float sum[8];
+  DactLane l;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  if (in)
-    with_act(p.act, [&](auto A) { dact_rows<DT, GATED, decltype(A)::value>(p, n, t0, t1, sum); });
-  if constexpr (!GATED) {
-    if (!p.sums) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) part[w][lane][e] = sum[e];
+  for (int e = 0; e < 8; ++e) {
+    l.sum[e] = 0.f;
+    l.m0[e] = SCALING == kApply && p.cs ? reciprocal_pow2(p.cs[n + e]) : 0.f;
+    l.m1[e] = SCALING == kApply && GATED && p.cs ? reciprocal_pow2(p.cs[p.N + n + e]) : 0.f;
+  }
+  with_act(p.act, [&](auto A) {
+    constexpr int ACT = decltype(A)::value;
+    // the host scales only what an activation or a gate has changed
+    if constexpr (SCALING == kNone || GATED || ACT != SA_ACT_NONE)
+      dact_rows<DT, GATED, ACT, SCALING>(p, n, in, t0, t1, l);
+  });
+  // 512 columns by 256 threads, the waves' values in order
+  auto columns = [&](const float (&v)[8], float* out, auto&& join) SA_INLINE {
     __syncthreads();
-    // 512 columns by 256 threads, the waves' sums in order
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[w][lane][e] = v[e];
+    __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = h * 256 + (int)threadIdx.x;
       const int64_t col = (int64_t)blockIdx.x * 512 + c;
       if (col < p.N)
-        p.sums[blockIdx.y * p.N + col] = (part[0][c / 8][c % 8] + part[1][c / 8][c % 8]) +
-                                         (part[2][c / 8][c % 8] + part[3][c / 8][c % 8]);
+        out[col] = join(join(part[0][c / 8][c % 8], part[1][c / 8][c % 8]),
+                        join(part[2][c / 8][c % 8], part[3][c / 8][c % 8]));
+    }
+  };
+  if constexpr (SCALING != kApply && !GATED) {
+    if (p.sums) columns(l.sum, p.sums + blockIdx.y * p.N, [](float a, float b) { return a + b; });
+  }
+  if constexpr (SCALING == kFind) {
+    constexpr int outs = GATED ? 2 : 1;
+    auto larger = [](float a, float b) { return fmaxf(a, b); };
+    columns(l.m0, p.cmax + (int64_t)blockIdx.y * outs * p.N, larger);
+    if constexpr (GATED) columns(l.m1, p.cmax + ((int64_t)blockIdx.y * outs + 1) * p.N, larger);
+  }
+}
+// The scales of the rows and columns of d, and dbias.  The first `cblocks`
+// workgroups take 64 of the C columns each (wave w strips w, w + 4, ...; sums
+// in k_lin_colsum's order), the others a row per wave, of `blocks` maxima.  A
+// workgroup stores the flag once, within its XCD: stores of every row and
+// column through to memory queued at its address (small d, 509 x 4096: 20 us).
+template <bool SUMS>
+__global__ __launch_bounds__(256) void k_lin_scales(DactP p, int64_t strips, int64_t C, int cblocks,
+                                                    int blocks, uint16_t* dbias) {
+  __shared__ float part[4][64], most[4][64];
+  const int lane = lane_id(), w = (int)threadIdx.x / kWave;
+  bool scaled = false;
+  if ((int)blockIdx.x < cblocks) {
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f, m = 0.f;
+    if (n < C) {
+      for (int64_t i = w; i < strips; i += 32) {
+        float v[8], q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t k = i + 4 * j < strips ? i + 4 * j : i;
+          v[j] = p.cmax[k * C + n];
+          q[j] = SUMS ? p.sums[k * C + n] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          m = fmaxf(m, v[j]);
+          if (SUMS && i + 4 * j < strips) s += q[j];
+        }
+      }
+    }
+    part[w][lane] = s;
+    most[w][lane] = m;
+    __syncthreads();
+    if (w == 0 && n < C) {
+      if (SUMS)
+        dbias[n] = from_f<SA_F16>((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]));
+      if (p.cs) {
+        const float u = unscale_of(fmaxf(fmaxf(most[0][lane], most[1][lane]), fmaxf(most[2][lane], most[3][lane])));
+        p.cs[n] = u;
+        scaled = u != 1.f;
+      }
+    }
+  } else {
+    const int64_t step = 4 * (int64_t)((int)gridDim.x - cblocks);
+    for (int64_t t = 4 * (int64_t)((int)blockIdx.x - cblocks) + w; t < p.T; t += step) {
+      float m = 0.f;
+      for (int b = lane; b < blocks; b += 64) m = fmaxf(m, p.rmax[t * blocks + b]);
+      const float u = unscale_of(wave_max(m));
+      if (lane == 0) p.rs[t] = u;
+      scaled |= u != 1.f;
     }
   }
+  // read by later launches only: a store that may stay in this XCD's L2
+  if (__syncthreads_or(scaled) && threadIdx.x == 0)
+    __hip_atomic_store(p.scaled, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 // dbias[n]: the strips' sums.  64 columns per workgroup; wave w adds strips
 // w, w + 4, ..., then the waves' four sums are added in order.
@@ -1320,14 +1535,16 @@ hipError_t launch_lin(LinP p, void* ws, hipStream_t s) {
         (int64_t)p.M * p.N * (GATED ? 2 : 1) * 4 * slots < 0x7fffffffLL))
     p.tickets = nullptr;
   constexpr int SB = GATED ? 256 : 128;
-  constexpr int EPI = LAY == kFwd ? kGeneral : kPlain;
+  constexpr int EPI = LAY == kFwd ? kGeneral : DT == SA_F16 ? kScaled : kPlain;
   if (pl.tile == 0) {
     // split products finish in k_lin_reduce
-    if (LAY != kFwd || pl.split ||
+    if constexpr (LAY != kFwd)
+      launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
+    else if (pl.split ||
         (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res))
       launch_tile<DT, LAY, GATED, kPlain, 256, 256, 2, 2, 2>(p, groups_of_work, s);
     else if (!GATED && !p.bias && !p.pre[0] && p.act == SA_ACT_NONE)
-      launch_tile<DT, LAY, GATED, LAY == kFwd && !GATED ? kResidual : EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
+      launch_tile<DT, LAY, GATED, GATED ? EPI : kResidual, 256, 256, 2, 2, 2>(p, groups_of_work, s);
     else
       launch_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, groups_of_work, s);
   } else if (pl.tile == kNarrow) {
@@ -1401,58 +1618,106 @@ hipError_t fwd_dt(const LinearCall& c, hipStream_t s) {
   return c.gated ? launch_lin<DT, kFwd, true>(p, c.ws, s) : launch_lin<DT, kFwd, false>(p, c.ws, s);
 }
 
+// The backward calls' scratch, in order; the products' partial sums follow.
+struct BwdScratch {
+  bool map = false, scaled = false;  // d differs from dy; it is fp16
+  size_t d[2] = {}, e[2] = {}, sums = 0, rmax = 0, cmax = 0, rs = 0, cs = 0, flag = 0, end = 0;
+};
+BwdScratch bwd_scratch(int dtype, bool gated, int64_t T, int64_t d_out, int act, bool dbias) {
+  BwdScratch b;
+  const int n = gated ? 2 : 1;
+  const int64_t strips = strips_of(T), blocks = (d_out + 511) / 512;
+  b.map = gated || act != SA_ACT_NONE;
+  b.scaled = b.map && dtype == SA_F16;
+  auto take = [&](int64_t bytes) {
+    const size_t at = b.end;
+    b.end += round256((size_t)bytes);
+    return at;
+  };
+  for (int i = 0; i < n && b.map; ++i) b.d[i] = take(T * d_out * 2);
+  if (dbias) b.sums = take(strips * d_out * 4);
+  if (!b.scaled) return b;
+  for (int i = 0; i < n; ++i) b.e[i] = take(T * d_out * 2);
+  b.rmax = take(T * blocks * 4);
+  b.cmax = take(strips * n * d_out * 4);
+  b.rs = take(T * 4);
+  b.cs = take(n * d_out * 4);
+  b.flag = take(4);
+  return b;
+}
+
 template <int DT>
 hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
   char* ws = static_cast<char*>(c.ws);
-  const size_t dbytes = round256((size_t)c.T * c.d_out * 2);
-  const bool map = c.gated || c.act != SA_ACT_NONE;  // d differs from dy
+  const BwdScratch b = bwd_scratch(DT, c.gated, c.T, c.d_out, c.act, c.dbias != nullptr);
+  const int outs = c.gated ? 2 : 1;
   const uint16_t* d[2] = {c.dy, nullptr};
   int64_t ldd = c.lddy;
-  if (map) {
-    d[0] = reinterpret_cast<uint16_t*>(ws);
-    ws += dbytes;
-    if (c.gated) {
-      d[1] = reinterpret_cast<uint16_t*>(ws);
-      ws += dbytes;
-    }
+  if (b.map) {
+    d[0] = reinterpret_cast<uint16_t*>(ws + b.d[0]);
+    if (c.gated) d[1] = reinterpret_cast<uint16_t*>(ws + b.d[1]);
     ldd = c.d_out;
   }
+  const bool scaled = b.scaled && c.T > 0 && (c.dx || c.dw[0]);
   const int64_t strips = strips_of(c.T);
-  float* sums = nullptr;
-  if (c.dbias) {
-    sums = reinterpret_cast<float*>(ws);
-    ws += round256((size_t)strips * c.d_out * 4);
-  }
+  DactP a{};
   hipError_t e = hipSuccess;
-  if (c.T > 0 && (map || c.dbias)) {
-    DactP a{};
+  a.sums = c.dbias ? reinterpret_cast<float*>(ws + b.sums) : nullptr;
+  if (c.T > 0 && (b.map || c.dbias)) {
     a.dy = c.dy;
     a.lddy = c.lddy;
     a.a = c.pre[0];
     a.lda = c.ldpre[0];
     a.b = c.pre[1];
     a.ldb = c.ldpre[1];
-    a.d0 = map ? const_cast<uint16_t*>(d[0]) : nullptr;
+    a.d0 = b.map ? const_cast<uint16_t*>(d[0]) : nullptr;
     a.d1 = const_cast<uint16_t*>(d[1]);
-    a.sums = sums;
     a.T = c.T;
     a.N = c.d_out;
     a.strip = strip_rows(c.T);
     a.act = c.act;
     const dim3 gr((unsigned)((c.d_out + 511) / 512), (unsigned)strips);
-    if (c.gated)
-      hipLaunchKernelGGL((k_lin_dact<DT, true>), gr, dim3(256), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_lin_dact<DT, false>), gr, dim3(256), 0, s, a);
+    if constexpr (DT == SA_F16) {
+      if (scaled) {
+        a.rmax = reinterpret_cast<float*>(ws + b.rmax);
+        a.cmax = reinterpret_cast<float*>(ws + b.cmax);
+        a.scaled = reinterpret_cast<uint32_t*>(ws + b.flag);
+        if (c.dx) {
+          a.rs = reinterpret_cast<float*>(ws + b.rs);
+          a.e0 = reinterpret_cast<uint16_t*>(ws + b.e[0]);
+          a.e1 = c.gated ? reinterpret_cast<uint16_t*>(ws + b.e[1]) : nullptr;
+        }
+        if (c.dw[0]) a.cs = reinterpret_cast<float*>(ws + b.cs);
+        if (c.gated) hipLaunchKernelGGL((k_lin_dact<DT, true, kFind>), gr, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_lin_dact<DT, false, kFind>), gr, dim3(256), 0, s, a);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t C = outs * c.d_out;
+        const int cblocks = a.cs || c.dbias ? (int)((C + 63) / 64) : 0;
+        const int64_t rows = c.dx ? (c.T + 3) / 4 : 0;
+        const dim3 gs((unsigned)(cblocks + (rows < 1024 ? rows : 1024)));
+        if (c.dbias) hipLaunchKernelGGL((k_lin_scales<true>), gs, dim3(256), 0, s, a, strips, C, cblocks, (int)gr.x, c.dbias);
+        else hipLaunchKernelGGL((k_lin_scales<false>), gs, dim3(256), 0, s, a, strips, C, cblocks, (int)gr.x, c.dbias);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (c.gated) hipLaunchKernelGGL((k_lin_dact<DT, true, kApply>), gr, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_lin_dact<DT, false, kApply>), gr, dim3(256), 0, s, a);
+      }
+    }
+    if (!scaled) {
+      if (c.gated) hipLaunchKernelGGL((k_lin_dact<DT, true, kNone>), gr, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((k_lin_dact<DT, false, kNone>), gr, dim3(256), 0, s, a);
+    }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (c.dbias) {
+  if (c.dbias && !scaled) {
     hipLaunchKernelGGL((k_lin_colsum<DT>), dim3((unsigned)((c.d_out + 63) / 64)), dim3(256), 0, s,
-                       sums, strips, c.d_out, c.dbias);
+                       a.sums, strips, c.d_out, c.dbias);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  ws += b.end;
   LinP x{}, w{};
   x.p[0] = d[0];
   x.p[1] = d[1];
@@ -1478,7 +1743,14 @@ hipError_t bwd_dt(const LinearCall& c, hipStream_t s) {
   w.N = (int)c.d_out;
   w.K = (int)c.T;
   w.segs = 1;
-  w.outs = c.gated ? 2 : 1;
+  w.outs = outs;
+  if (scaled) {
+    x.rs = a.rs;
+    x.scaled = a.scaled;
+    x.alt[0] = a.e0;
+    x.alt[1] = a.e1;
+    w.cs = a.cs;
+  }
   if (c.dx && c.dw[0]) return launch_gradients<DT>(x, w, ws, s);
   if (c.dx) return launch_lin<DT, kDx, false>(x, ws, s);
   if (c.dw[0]) return launch_lin<DT, kDw, false>(w, ws, s);
@@ -1491,12 +1763,10 @@ size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out
   return part_bytes(lin_plan(kFwd, gated, T, d_out, d_in, 1, 1), T, d_out, d_in, 1, gated ? 2 : 1);
 }
 
-size_t linear_backward_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out, int act,
-                                       bool dbias) {
+size_t linear_backward_workspace_bytes(int dtype, bool gated, int64_t T, int64_t d_in, int64_t d_out,
+                                       int act, bool dbias) {
   const int n = gated ? 2 : 1;
-  size_t b = 0;
-  if (gated || act != SA_ACT_NONE) b += n * round256((size_t)T * d_out * 2);
-  if (dbias) b += round256((size_t)strips_of(T) * d_out * 4);
+  const size_t b = bwd_scratch(dtype, gated, T, d_out, act, dbias).end;
   const size_t px = part_bytes(lin_plan(kDx, false, T, d_in, d_out, n, 1), T, d_in, d_out, n, 1);
   const size_t pw = part_bytes(lin_plan(kDw, false, d_in, d_out, T, 1, n), d_in, d_out, T, 1, n);
   return b + (px > pw ? px : pw);
