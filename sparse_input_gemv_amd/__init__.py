@@ -717,14 +717,27 @@ def _lin_ws_bytes(fn: str, *args) -> int:
 
 
 LINEAR_TICKET_BYTES = 256 << 10  # SA_LINEAR_TICKET_BYTES
-_tickets: dict = {}  # (device index, stream) -> the zero counters of the one-launch sum
+# (device index, torch's stream id) -> the zero counters of the one-launch sum.
+# Kept as long as the process, so only for streams that live as long: torch's
+# default and pooled streams, which its ids name for good.
+_tickets: dict = {}
+
+
+def _lasting(stream_id: int, handle: int) -> bool:
+    """Whether torch's id names one stream for the process's life: 0 (the
+    default stream) or a pool's odd id.  An external stream's id is its handle,
+    which is no identity: the per-thread default stream has the same one in
+    every thread, and a destroyed stream's is given to a new one while its
+    last kernels may still run."""
+    return handle == 0 if stream_id == 0 else stream_id % 2 == 1 and stream_id != handle
 
 
 def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
     """Runs ``fn`` on the current stream of ``like``'s device, with scratch
     of its own from torch's allocator: calls on other streams and captured
     graphs share none.  The forward calls' counters belong to the stream; a
-    captured call goes without (its replays may run on any stream)."""
+    captured call goes without (its replays may run on any stream), and so
+    does one on a stream that torch did not make."""
     dev = like.device
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -736,10 +749,11 @@ def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
     if fn in ("dense_linear", "gated_linear"):
         tk = None
         if need and sizes[0] <= 64 and not torch.cuda.is_current_stream_capturing():
-            tk = _tickets.get((dev.index, stream))
-            if tk is None:
+            sid = torch._C._cuda_getCurrentStream(dev.index)[0]
+            tk = _tickets.get((dev.index, sid))
+            if tk is None and _lasting(sid, stream):
                 tk = torch.zeros(LINEAR_TICKET_BYTES, dtype=torch.uint8, device=dev)
-                _tickets[dev.index, stream] = tk
+                _tickets[dev.index, sid] = tk
         st = getattr(lib(), fn)(*args, _ptr(ws), need, _ptr(tk), stream)
     else:
         st = getattr(lib(), fn)(*args, _ptr(ws), need, stream)
