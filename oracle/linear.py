@@ -21,7 +21,12 @@ _erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def _sigma(z):
-    return 0.5 * (1.0 + np.tanh(0.5 * z))
+    e = np.exp(-np.abs(z))  # keeps its relative accuracy in the lower tail
+    return np.where(z < 0, e, 1.0) / (1.0 + e)
+
+
+def _tanh_arg(z):
+    return 2.0 * math.sqrt(2.0 / math.pi) * (z + 0.044715 * z**3)
 
 
 def _f64(a):
@@ -41,7 +46,7 @@ def act(name: str, z) -> np.ndarray:
     if name == "gelu":
         return 0.5 * z * _erfc(-z / math.sqrt(2.0))
     if name == "gelu_tanh":
-        return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z**3)))
+        return z * _sigma(_tanh_arg(z))
     raise ValueError(name)
 
 
@@ -56,13 +61,13 @@ def slope(name: str, z) -> np.ndarray:
         return 2.0 * np.maximum(z, 0.0)
     if name == "silu":
         s = _sigma(z)
-        return s + z * s * (1.0 - s)
+        return s + z * s * _sigma(-z)
     if name == "gelu":
         return 0.5 * _erfc(-z / math.sqrt(2.0)) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
     if name == "gelu_tanh":
-        c = math.sqrt(2.0 / math.pi)
-        t = np.tanh(c * (z + 0.044715 * z**3))
-        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * c * (1.0 + 0.134145 * z * z)
+        a = _tanh_arg(z)
+        s = _sigma(a)
+        return s + z * s * _sigma(-a) * 2.0 * math.sqrt(2.0 / math.pi) * (1.0 + 0.134145 * z * z)
     raise ValueError(name)
 
 
