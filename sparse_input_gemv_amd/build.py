@@ -9,6 +9,7 @@ root, the shared library next to this file.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import hashlib
 import os
 import subprocess
 import sys
@@ -28,6 +29,18 @@ DEVICE = ["-x", "hip", "--offload-arch=gfx950",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
+def source_hash(src: str) -> str:
+    """Of a source and every header it may include: an object's .src file
+    holds the one it was built from."""
+    inc = os.path.join(ROOT, "include")
+    headers = [os.path.join(d, f) for d in (CSRC, inc) for f in sorted(os.listdir(d)) if f.endswith((".hpp", ".h"))]
+    h = hashlib.sha256()
+    for path in [os.path.join(CSRC, src)] + headers:
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
+
+
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     path = os.path.join(CSRC, src)
@@ -35,9 +48,12 @@ def _compile(src: str) -> str:
         cmd = [HIPCC] + DEVICE + COMMON + ["-c", path, "-o", obj]
     else:
         cmd = [HIPCC] + COMMON + ["-c", path, "-o", obj]
+    built_from = source_hash(src)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    with open(obj + ".src", "w") as f:
+        f.write(built_from)
     return obj
 
 
