@@ -521,8 +521,12 @@ int dense_gemm(const uint16_t* x, int64_t T, int64_t d_in, const uint16_t* wt,
  *   holds a second copy of d; bf16 needs less.
  * - `tickets` (forward calls) is NULL, or SA_LINEAR_TICKET_BYTES of device
  *   memory, 16-byte aligned, zero before its first use and left zero by every
- *   call.  With it, calls of at most 64 rows sum their split products in the
- *   same launch instead of a second one; the bits are the same.  Calls that
+ *   call.  With it, calls whose split products take little adding sum them in
+ *   the same launch instead of a second one; the bits are the same.  With the
+ *   tile rows, split and tiles of sa_linear_plan, these are the calls of at
+ *   most 64 tile rows and 512 tiles with ceil(min(T, tile rows) / 16) *
+ *   (floor(split / tiles / 4) + 1) <= 4: 17 or 64 rows into 14336 columns,
+ *   but not 33 rows of 4096 x 1024.  Other calls do not use it.  Calls that
  *   share it must be ordered on one stream, so a captured graph that may run
  *   beside other calls takes its own, or NULL.
  * - Inf and NaN in a row of x reach that row's outputs only.

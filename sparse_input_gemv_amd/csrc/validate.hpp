@@ -51,7 +51,7 @@ int check_nm_shared_spmm(const void* xval, const void* mask, int64_t T, int64_t 
                          int m, int tt, const void* wt, int64_t d_out, const void* y);
 
 // Dense linear layers.  A matrix argument: its pointer, row stride and row
-// length; `rows` only for messages.
+// length.
 constexpr int64_t kMaxLinDim = (int64_t)1 << 21;   // d_in, d_out, strides
 constexpr int64_t kMaxLinRows = (int64_t)1 << 22;  // T
 int check_linear_sizes(const char* fn, int dtype, int64_t T, int64_t d_in, int64_t d_out, int act);
