@@ -20,6 +20,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 
 import torch
 
@@ -704,6 +705,14 @@ def _lin_vec(t: torch.Tensor, name: str, like: torch.Tensor, n: int) -> None:
         raise ValueError(f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
 
 
+def _lin_detached(fn: str, *inputs) -> None:
+    """Warns where autograd would expect a graph: outputs carry none."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        warnings.warn(f"{fn} is outside autograd: its outputs carry no graph, and no gradient reaches "
+                      f"inputs that require one. Call {fn}_backward for the gradients, or call it "
+                      f"under torch.no_grad().", stacklevel=3)
+
+
 def _lin_out(t, name: str, like: torch.Tensor, rows: int, cols: int):
     """``(tensor, row stride)`` of an output, allocated when not given."""
     if t is None:
@@ -768,7 +777,9 @@ def dense_linear(x: torch.Tensor, wt: torch.Tensor, bias: torch.Tensor | None = 
     ``[T][d_in]``) and ``wt[d_in][d_out]``; ``act`` is a key of
     ``ACTIVATIONS``.  Rows may be strided.  ``y`` may be ``residual``.
     Returns ``y``, or ``(y, pre)`` with the pre-activation when ``with_pre``
-    or ``pre`` is given (``dense_linear_backward`` reads it)."""
+    or ``pre`` is given (``dense_linear_backward`` reads it).  Outside
+    autograd: the gradients are ``dense_linear_backward``'s, and inputs that
+    require grad bring a warning unless grad mode is off."""
     squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
     x = _lin_x(x, "x")
     T, d_in = x.shape
@@ -779,6 +790,7 @@ def dense_linear(x: torch.Tensor, wt: torch.Tensor, bias: torch.Tensor | None = 
         _lin_vec(bias, "bias", x, d_out)
     ldr = 0 if residual is None else _lin_mat(residual, "residual", x, T, d_out)
     y, ldy = _lin_out(y, "y", x, T, d_out)
+    _lin_detached("dense_linear", x, wt, bias, residual)
     ldp = 0
     if with_pre or pre is not None:
         pre, ldp = _lin_out(pre, "pre", x, T, d_out)
@@ -829,7 +841,8 @@ def gated_linear(x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor, act: str
     """``h = act(x Wg^T) * (x Wu^T)``, both projections in one pass; fp16 or
     bf16.  ``wgt`` and ``wut`` may be column blocks of one side-by-side
     weight.  Returns ``h``, or ``(h, g, u)`` with the rounded projections when
-    ``with_gu`` (or both ``g`` and ``u``) is given."""
+    ``with_gu`` (or both ``g`` and ``u``) is given.  Outside autograd, as
+    ``dense_linear``: the gradients are ``gated_linear_backward``'s."""
     squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
     x = _lin_x(x, "x")
     T, d_in = x.shape
@@ -838,6 +851,7 @@ def gated_linear(x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor, act: str
     ldg_w = _lin_mat(wgt, "wgt", x, d_in, d_out)
     ldu_w = _lin_mat(wut, "wut", x, d_in, d_out)
     h, ldh = _lin_out(h, "h", x, T, d_out)
+    _lin_detached("gated_linear", x, wgt, wut)
     ldg = ldu = 0
     if with_gu or g is not None or u is not None:
         g, ldg = _lin_out(g, "g", x, T, d_out)
