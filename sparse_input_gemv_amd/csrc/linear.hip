@@ -19,14 +19,16 @@
 // The gated forward tile holds 128 columns of g and the same 128 of u, so the
 // wave that ends with a g has its u, and x is read once for both.
 //
-// What bounds it, and what it measured on one MI355X (bf16, random data):
+// What bounds it, and what it measured on MI355X (bf16, random data; ranges
+// are over GPUs):
 //   large: the matrix cores' power.  MFMAs alone run at 2025 TFLOP/s with
 //     random operands on all CUs (2414 with zeros, 2448 on one CU); the
-//     kernel runs 8192 x 14336 x 4096 at 1400 TFLOP/s, dx 4096 x 11008 x 4096
-//     at 1370, dW 4096 x 4096 x 16384 at 1390, gate and up 8192 x 4096 x
-//     14336 with g and u kept at 1350.  The library's product reaches 1414
-//     at 8192^3 with both operands K-contiguous, 1323 in the forward layout
-//     and 1158 in dW's.
+//     kernel runs 8192 x 14336 x 4096 at 1295-1420 TFLOP/s, dx 4096 x 11008 x
+//     4096 at 1340-1360, dW 4096 x 4096 x 11008 at 1240-1270 (2.7 rounds of
+//     tiles; 4096 x 4096 x 16384, which fills its rounds, 1310-1390), gate and
+//     up 8192 x 4096 x 14336 with g and u kept at 1270-1350.  The library's
+//     product reaches 1410-1540 at 8192^3 with both operands K-contiguous,
+//     1320 in the forward layout and 1150 in dW's.
 //   few rows: the weights' stream.  1 x 4096 x 11008 gate and up 35 us (180
 //     MB: 5.1 TB/s; a plain read runs at 7.2, a copy at 5.1), 8 x 11008 x
 //     4096 19 us, 1 x 4096 x 4096 10 us (most of it launch and fill).
@@ -1058,7 +1060,8 @@ __global__ __launch_bounds__(256, 1) void k_lin(LinP p) {
 // Small gradients: dx (the first `first` workgroups) and dW in one launch, a
 // workgroup of each on a CU.  One after the other, each leaves the chip
 // waiting for its own latency (the whole backward call of 509 rows 1024 ->
-// 4096: 34.8 -> 28.1 us, gated with 300 rows 39.5 -> 33.8).
+// 4096: 34.8 -> 28.1 us, gated with 300 rows 39.5 -> 33.8, both before fp16's
+// scales).
 template <int DT, int XM>
 __global__ __launch_bounds__(256, 1) void k_lin_pair(LinP x, LinP w, int first) {
   constexpr int NX = XM == 64 ? 3 : 2, WX = XM == 64 ? 1 : 2;
@@ -1152,9 +1155,11 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinP p, int groups, int lbm,
 // worst.  Three launches, as a scale has to be known before a value is
 // rounded: kFind writes the unscaled d and the largest |d| of every row and
 // column of its block; k_lin_scales finds the scales; kApply returns at once
-// if all are 1, as in most training steps, or else evaluates d again and
+// if all are 1 (a loss scale keeps d there), or else evaluates d again and
 // writes it by rows' scales (another buffer, which dx then reads) and by
-// columns' (over the unscaled d).
+// columns' (over the unscaled d).  4096 x 11008, linear (gated): kNone 58 us
+// (80), kFind 62 (84), k_lin_scales 5, kApply 5 where it returns at once, else
+// 71 (124); 509 x 4096 (gated 300): kFind 7, scales 2-4, kApply 1.6, else 7 (9).
 enum Scaling { kNone = 0, kFind = 1, kApply = 2 };
 struct DactP {
   const uint16_t *dy, *a, *b;  // a: pre or g; b: u
@@ -1438,8 +1443,11 @@ int64_t slots_of(const Plan& pl, int64_t steps) {
 // sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
 // 3 us for the reduction's launch (7 with 256 x 256 tiles) and the partials'
 // bytes at 4 TB/s; one row tile streams its weights at 26 GB/s per CU at most
-// (gated: up to four share them at 40).  Over 88 random shapes the choice
-// took 2 to 3 percent longer than the best of a sweep, on average.
+// (gated: up to four share them at 40).  Over 180 random shapes (plain, gated,
+// dx) the choice took 4 percent longer than the best of a sweep on average,
+// but 7 to 13 at 33 to 64 rows and 14 for gated products of 17 to 32, where a
+// second row tile of half the height can pay for reading the weights again
+// (46 rows, gated 760 x 6584: 19.4 us against 12.7, the largest miss).
 Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
   static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
                                           {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
@@ -1453,7 +1461,8 @@ Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, in
     const bool forced = g_lin_tile >= 0 && !(lay == kDw && g_lin_tile > 1 && g_lin_tile != kNarrow) &&
                         !(g_lin_tile == kNarrow && gated);
     if (forced && t != g_lin_tile) continue;
-    // up to 64 rows in one row tile, more in tiles of 64 at least
+    // up to 64 rows in one row tile, more in tiles of 64 at least (see the
+    // misses above)
     if (g_lin_tile < 0 && kTileM[t] < (M < 64 ? M : 64)) continue;
     const int64_t tiles = tiles_of(t, gated, M, N, outs);
     const bool pairs = t > 0 && t != kNarrow && !gated;
