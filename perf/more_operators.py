@@ -212,10 +212,10 @@ def _slope(v, act):
 
 
 def _codes64(x):
-    """8-bit codes and scales of x's rows.  The scale is fp32; a quotient may
-    lie next to half a step, so it is taken in fp64."""
-    most = x.float().abs().amax(1)
-    s = most / 127
+    """8-bit codes and scales of x's rows.  The scale is the fp32 quotient; a
+    product by the reciprocal of 127 may differ from it, and a value's quotient
+    may lie next to half a step, so both are taken in fp64."""
+    s = (x.float().abs().amax(1).double() / 127).float()
     by = torch.where(s > 0, s, 1.0).double()
     return torch.round(x.double() / by[:, None]).clamp(-127, 127).to(torch.int8), s
 
