@@ -610,6 +610,68 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
                           void* stream);
 size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
+/* ---- linear layers grouped by expert ------------------------------------------ */
+
+/*
+ * The dense layers above with a weight per expert: rows offsets[e] ..
+ * offsets[e + 1] - 1 of x (sorted by expert, as a router leaves them) go
+ * through expert e's matrix.  What holds for the dense layers (types, sums,
+ * sizes, strides, alignment, overlap, `ws`, order of sums) holds here too, and:
+ * - 1 <= experts <= SA_MAX_EXPERTS.  Expert e's matrix starts e * sw (or
+ *   sdw) elements behind expert 0's: a multiple of 8, not negative, at most
+ *   2^42; 0 lets all experts read one weight, and gate and up may lie side by
+ *   side.  Experts' outputs must be apart: one matrix after another, or
+ *   column blocks of common rows.  With one expert the stride is not read.
+ *   Biases and their gradients are [experts][d_out], rows back to back.
+ * - offsets [experts + 1] int32 on the device, read when the call runs: the
+ *   host neither waits for them nor checks them.  They ascend from 0 or more
+ *   to T at most; an expert may have no rows.  Whatever they hold, nothing out
+ *   of range is read or written: an offset counts as min(max(it, 0), T), and
+ *   at least as the largest before it.
+ * - Rows before offsets[0] and from offsets[experts] on belong to no expert:
+ *   they are not read into any result, and outputs keep what they held there.
+ * - An expert without rows has zero weight and bias gradients.
+ */
+#define SA_MAX_EXPERTS 512
+
+/* grouped_linear -- pre = x We^T + be, y = act(pre) + residual, by rows' experts. */
+int grouped_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
+                   int64_t sw, int64_t experts, const int32_t* offsets, int64_t d_in, int64_t d_out,
+                   const void* bias, int act, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                   void* pre, int64_t ldpre, void* ws, size_t ws_bytes, void* stream);
+size_t grouped_linear_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out);
+
+/* grouped_linear_backward -- dx, dwt [experts][d_in][d_out] and dbias of
+ * grouped_linear from dy, as dense_linear_backward (for fp16's scales a
+ * column's m is its largest entry among the expert's rows). */
+int grouped_linear_backward(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t T,
+                            const void* wt, int64_t ldw, int64_t sw, int64_t experts,
+                            const int32_t* offsets, int64_t d_in, int64_t d_out, int act,
+                            const void* pre, int64_t ldpre, void* dx, int64_t lddx, void* dwt,
+                            int64_t lddwt, int64_t sdwt, void* dbias, void* ws, size_t ws_bytes,
+                            void* stream);
+size_t grouped_linear_backward_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out,
+                                               int act, int with_dbias);
+
+/* grouped_gated_linear -- g = x Wge^T, u = x Wue^T, h = act(g) * u, by rows' experts. */
+int grouped_gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
+                         int64_t swg, const void* wut, int64_t ldwu, int64_t swu, int64_t experts,
+                         const int32_t* offsets, int64_t d_in, int64_t d_out, int act, void* h,
+                         int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
+                         size_t ws_bytes, void* stream);
+size_t grouped_gated_linear_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out);
+
+/* grouped_gated_linear_backward -- dx, dwgt and dwut of grouped_gated_linear
+ * from dh, as gated_linear_backward. */
+int grouped_gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x, int64_t ldx,
+                                  int64_t T, const void* wgt, int64_t ldwg, int64_t swg, const void* wut,
+                                  int64_t ldwu, int64_t swu, int64_t experts, const int32_t* offsets,
+                                  int64_t d_in, int64_t d_out, int act, const void* g, int64_t ldg,
+                                  const void* u, int64_t ldu, void* dx, int64_t lddx, void* dwgt,
+                                  int64_t lddwg, int64_t sdwg, void* dwut, int64_t lddwu, int64_t sdwu,
+                                  void* ws, size_t ws_bytes, void* stream);
+size_t grouped_gated_linear_backward_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out);
+
 /* ---- roofline calibration ----------------------------------------------- */
 
 /* Words of `sink` that sa_read_stream writes (one per wave of its grid). */
@@ -774,12 +836,23 @@ enum {
 int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols,
                    int* split, int64_t* tiles);
 /*
+ * The tile rows and split that a product of the layers grouped by expert would
+ * use (op: SA_LINEAR_FORWARD, _GATED, _DX or _GATED_DX), planned for rows
+ * spread evenly over the experts.  split = workgroups that share all tiles'
+ * steps evenly, 0 where workgroups take whole tiles.  It computes nothing on
+ * the GPU.  Returns SA_ERR_INVALID_ARG for another op, sizes the calls refuse
+ * or a NULL output.
+ */
+int sa_grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int* rows, int* split);
+/*
  * Process-wide choices of the dense linear layers, for tuning sweeps and
  * cross-checks: tile -1 = automatic, or 0..5 (256 x 256, 128 x 128, 64, 32
  * or 16 rows x 128, 256 x 192; weight gradients take 0, 1 and 5 only, gated
  * products not 5, and 5 is never split); split -1 =
  * automatic, 0 = whole tiles, or that many shares (up to 512, rounded down to
- * a power of two).  Workspace
+ * a power of two).  The layers grouped by expert follow them too (their
+ * weight gradients take tile 0 or 1 and no split, no product a split of tile
+ * 0; tile 5 counts as -1).  Workspace
  * sizes follow the choices: query them again.  Every choice computes the
  * same result up to fp32 summation order.
  * Returns SA_ERR_INVALID_ARG for other values.  Not thread-safe.

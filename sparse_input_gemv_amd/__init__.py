@@ -34,7 +34,8 @@ __all__ = [
     "masked_gemv",
     "dense_gemv", "masked_swiglu_down", "weight_col_norms", "nm_act_spmm", "nm_shared_spmm",
     "dense_gemm", "dense_linear", "dense_linear_backward", "gated_linear", "gated_linear_backward",
-    "ACTIVATIONS", "set_linear_tuning", "linear_plan", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
+    "grouped_linear", "grouped_linear_backward", "grouped_gated_linear", "grouped_gated_linear_backward",
+    "ACTIVATIONS", "set_linear_tuning", "linear_plan", "grouped_plan", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
     "workspace_zero_bytes", "scratch", "MAX_BATCH",
 ]
 
@@ -98,6 +99,21 @@ _SIGNATURES = {
                                      _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                      _i64, _vp, _sz, _vp]),
     "gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "grouped_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i32,
+                              _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "grouped_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "grouped_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
+                                       _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
+                                       _vp, _sz, _vp]),
+    "grouped_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32, _i32]),
+    "grouped_gated_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp,
+                                    _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "grouped_gated_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "grouped_gated_linear_backward": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64,
+                                             _i64, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp,
+                                             _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "grouped_gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "sa_grouped_plan": (_i32, [_i32, _i64, _i64, _i64, _i64, _vp, _vp]),
     "sa_set_linear_tuning": (_i32, [_i32, _i32]),
     "sa_linear_plan": (_i32, [_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "sa_set_gemm_tuning": (_i32, [_i32, _i32, _i32]),
@@ -893,6 +909,178 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, wgt: torch.Tensor, 
     return None if dx is None else _ret(dx, squeeze), dwgt, dwut
 
 
+# ---- linear layers grouped by expert --------------------------------------------
+
+MAX_EXPERTS = 512  # SA_MAX_EXPERTS
+
+
+def _grp_offsets(offsets: torch.Tensor, like: torch.Tensor) -> int:
+    """The number of experts."""
+    if not isinstance(offsets, torch.Tensor) or offsets.device != like.device or offsets.dtype != torch.int32:
+        raise ValueError(f"offsets must be an int32 tensor on {like.device}")
+    if offsets.dim() != 1 or offsets.numel() < 2 or offsets.stride(0) != 1:
+        raise ValueError(f"offsets must be a contiguous vector of experts + 1, got {tuple(offsets.shape)}")
+    return offsets.numel() - 1
+
+
+def _grp_mat(t: torch.Tensor, name: str, like: torch.Tensor, experts: int, rows: int, cols: int):
+    """Checks an ``[experts][rows][cols]`` operand and returns its row and
+    expert strides."""
+    if not isinstance(t, torch.Tensor) or t.device != like.device:
+        raise ValueError(f"{name} must be a torch tensor on {like.device}")
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.shape != (experts, rows, cols):
+        raise ValueError(f"{name} must be [{experts}][{rows}][{cols}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return st[1], st[0]
+
+
+def _grp_out(t, name: str, like: torch.Tensor, experts: int, rows: int, cols: int):
+    if t is None:
+        return torch.empty((experts, rows, cols), dtype=like.dtype, device=like.device), cols, rows * cols
+    return (t, *_grp_mat(t, name, like, experts, rows, cols))
+
+
+def _grp_x(x: torch.Tensor) -> torch.Tensor:
+    if isinstance(x, torch.Tensor) and x.dim() == 1:
+        raise ValueError("x must be [rows][d_in]: rows belong to experts")
+    return _lin_x(x, "x")
+
+
+def _grp_d_out(wt, name: str) -> int:
+    if not isinstance(wt, torch.Tensor) or wt.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [experts][d_in][d_out]")
+    return wt.shape[2]
+
+
+def _grp_bias(bias, like: torch.Tensor, experts: int, d_out: int) -> None:
+    if bias is not None and (not isinstance(bias, torch.Tensor) or bias.device != like.device
+                             or bias.dtype != like.dtype or bias.shape != (experts, d_out)
+                             or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous {like.dtype} tensor [{experts}][{d_out}] on {like.device}")
+
+
+def grouped_linear(x: torch.Tensor, wt: torch.Tensor, offsets: torch.Tensor,
+                   bias: torch.Tensor | None = None, act: str = "none",
+                   residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                   with_pre: bool = False, pre: torch.Tensor | None = None):
+    """``dense_linear`` with a weight per expert: rows ``offsets[e]`` to
+    ``offsets[e + 1] - 1`` of ``x`` (``[T][d_in]``, sorted by expert) go through
+    ``wt[e]`` (``[experts][d_in][d_out]``) and ``bias[e]``.  ``offsets`` is an
+    int32 tensor on the GPU, which the host does not wait for.  Rows outside
+    every expert's are left as they are: as ``torch.empty`` made them where
+    ``y`` or ``pre`` is not given."""
+    x = _grp_x(x)
+    T, d_in = x.shape
+    d_out = _grp_d_out(wt, "wt")
+    experts = _grp_offsets(offsets, x)
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldw, sw = _grp_mat(wt, "wt", x, experts, d_in, d_out)
+    _grp_bias(bias, x, experts, d_out)
+    ldr = 0 if residual is None else _lin_mat(residual, "residual", x, T, d_out)
+    y, ldy = _lin_out(y, "y", x, T, d_out)
+    _lin_detached("grouped_linear", x, wt, bias, residual)
+    ldp = 0
+    if with_pre or pre is not None:
+        pre, ldp = _lin_out(pre, "pre", x, T, d_out)
+    _lin_call("grouped_linear", x, (T, experts, d_in, d_out), _LIN_DTYPES[x.dtype], x.data_ptr(), ldx, T,
+              wt.data_ptr(), ldw, sw, experts, offsets.data_ptr(), d_in, d_out, _ptr(bias), _act(act),
+              _ptr(residual), ldr, y.data_ptr(), ldy, _ptr(pre), ldp)
+    return y if pre is None else (y, pre)
+
+
+def grouped_linear_backward(dy: torch.Tensor, x: torch.Tensor, wt: torch.Tensor, offsets: torch.Tensor,
+                            act: str = "none", pre: torch.Tensor | None = None, with_dbias: bool = False,
+                            with_dx: bool = True, with_dwt: bool = True, dx: torch.Tensor | None = None,
+                            dwt: torch.Tensor | None = None):
+    """Gradients of ``grouped_linear`` from ``dy``: ``(dx, dwt, dbias)``, None
+    where not asked for; ``dwt`` and ``dbias`` are zero for an expert without
+    rows.  Rows of ``dx`` outside every expert's are left as they are."""
+    x = _grp_x(x)
+    T, d_in = x.shape
+    d_out = _grp_d_out(wt, "wt")
+    experts = _grp_offsets(offsets, x)
+    a = _act(act)
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldw, sw = _grp_mat(wt, "wt", x, experts, d_in, d_out)
+    lddy = _lin_mat(dy, "dy", x, T, d_out)
+    ldp = 0
+    if a != 0:
+        if pre is None:
+            raise ValueError(f"pre is needed for act {act!r}")
+        ldp = _lin_mat(pre, "pre", x, T, d_out)
+    else:
+        pre = None
+    lddx = lddw = sdw = 0
+    if with_dx or dx is not None:
+        dx, lddx = _lin_out(dx, "dx", x, T, d_in)
+    if with_dwt or dwt is not None:
+        dwt, lddw, sdw = _grp_out(dwt, "dwt", x, experts, d_in, d_out)
+    dbias = torch.empty((experts, d_out), dtype=x.dtype, device=x.device) if with_dbias else None
+    _lin_call("grouped_linear_backward", x, (T, experts, d_in, d_out, a, int(with_dbias)),
+              _LIN_DTYPES[x.dtype], dy.data_ptr(), lddy, x.data_ptr(), ldx, T, wt.data_ptr(), ldw, sw,
+              experts, offsets.data_ptr(), d_in, d_out, a, _ptr(pre), ldp, _ptr(dx), lddx, _ptr(dwt),
+              lddw, sdw, _ptr(dbias))
+    return dx, dwt, dbias
+
+
+def grouped_gated_linear(x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor, offsets: torch.Tensor,
+                         act: str = "silu", h: torch.Tensor | None = None, with_gu: bool = False,
+                         g: torch.Tensor | None = None, u: torch.Tensor | None = None):
+    """``gated_linear`` with weights per expert, by rows as ``grouped_linear``:
+    ``h``, or ``(h, g, u)`` when ``with_gu`` (or ``g`` and ``u``) is given."""
+    x = _grp_x(x)
+    T, d_in = x.shape
+    d_out = _grp_d_out(wgt, "wgt")
+    experts = _grp_offsets(offsets, x)
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldg_w, sg = _grp_mat(wgt, "wgt", x, experts, d_in, d_out)
+    ldu_w, su = _grp_mat(wut, "wut", x, experts, d_in, d_out)
+    h, ldh = _lin_out(h, "h", x, T, d_out)
+    _lin_detached("grouped_gated_linear", x, wgt, wut)
+    ldg = ldu = 0
+    if with_gu or g is not None or u is not None:
+        g, ldg = _lin_out(g, "g", x, T, d_out)
+        u, ldu = _lin_out(u, "u", x, T, d_out)
+    _lin_call("grouped_gated_linear", x, (T, experts, d_in, d_out), _LIN_DTYPES[x.dtype], x.data_ptr(),
+              ldx, T, wgt.data_ptr(), ldg_w, sg, wut.data_ptr(), ldu_w, su, experts, offsets.data_ptr(),
+              d_in, d_out, _act(act), h.data_ptr(), ldh, _ptr(g), ldg, _ptr(u), ldu)
+    return h if g is None else (h, g, u)
+
+
+def grouped_gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, wgt: torch.Tensor, wut: torch.Tensor,
+                                  offsets: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
+                                  act: str = "silu", with_dx: bool = True, with_dw: bool = True,
+                                  dx: torch.Tensor | None = None, dwgt: torch.Tensor | None = None,
+                                  dwut: torch.Tensor | None = None):
+    """Gradients of ``grouped_gated_linear`` from ``dh`` and the forward call's
+    ``g`` and ``u``: ``(dx, dwgt, dwut)``, None where not asked for."""
+    x = _grp_x(x)
+    T, d_in = x.shape
+    d_out = _grp_d_out(wgt, "wgt")
+    experts = _grp_offsets(offsets, x)
+    ldx = _lin_mat(x, "x", x, T, d_in)
+    ldg_w, sg = _grp_mat(wgt, "wgt", x, experts, d_in, d_out)
+    ldu_w, su = _grp_mat(wut, "wut", x, experts, d_in, d_out)
+    lddh = _lin_mat(dh, "dh", x, T, d_out)
+    ldg = _lin_mat(g, "g", x, T, d_out)
+    ldu = _lin_mat(u, "u", x, T, d_out)
+    lddx = lddg = lddu = sdg = sdu = 0
+    if with_dx or dx is not None:
+        dx, lddx = _lin_out(dx, "dx", x, T, d_in)
+    if with_dw or dwgt is not None or dwut is not None:
+        dwgt, lddg, sdg = _grp_out(dwgt, "dwgt", x, experts, d_in, d_out)
+        dwut, lddu, sdu = _grp_out(dwut, "dwut", x, experts, d_in, d_out)
+    _lin_call("grouped_gated_linear_backward", x, (T, experts, d_in, d_out), _LIN_DTYPES[x.dtype],
+              dh.data_ptr(), lddh, x.data_ptr(), ldx, T, wgt.data_ptr(), ldg_w, sg, wut.data_ptr(),
+              ldu_w, su, experts, offsets.data_ptr(), d_in, d_out, _act(act), g.data_ptr(), ldg,
+              u.data_ptr(), ldu, _ptr(dx), lddx, _ptr(dwgt), lddg, sdg, _ptr(dwut), lddu, sdu)
+    return dx, dwgt, dwut
+
+
 # ---- tuning -------------------------------------------------------------------
 
 def set_gemv_tuning(tiling: int = -1, target_wgs: int = 0, handoff: int = 0) -> None:
@@ -938,8 +1126,8 @@ def gemm_plan(op: str, T: int, d_in: int, d_out: int, n: int = 0, m: int = 0, cu
 
 
 def set_linear_tuning(tile: int = -1, split: int = -1) -> None:
-    """Tile and split of the dense linear layers' products (see the C
-    declaration); -1 is the automatic choice."""
+    """Tile and split of the linear layers' products, dense and grouped by
+    expert (see the C declaration); -1 is the automatic choice."""
     _check(lib().sa_set_linear_tuning(tile, split), "sa_set_linear_tuning")
     _lin_ws_bytes.cache_clear()
 
@@ -956,6 +1144,16 @@ def linear_plan(op: str, T: int, d_in: int, d_out: int):
     _check(lib().sa_linear_plan(LINEAR_OPS[op], T, d_in, d_out,
                                 *[ctypes.addressof(o) for o in (r, c, sl, it)]), "sa_linear_plan")
     return {"tile_rows": r.value, "tile_cols": c.value, "split": sl.value, "tiles": it.value}
+
+
+def grouped_plan(op: str, T: int, experts: int, d_in: int, d_out: int):
+    """The decomposition a product of the layers grouped by expert would use:
+    a dict with ``tile_rows`` and ``split``.  ``op`` is "forward", "gated", "dx"
+    or "gated_dx"."""
+    r, sp = ctypes.c_int(), ctypes.c_int()
+    _check(lib().sa_grouped_plan(LINEAR_OPS[op], T, experts, d_in, d_out, ctypes.addressof(r),
+                                 ctypes.addressof(sp)), "sa_grouped_plan")
+    return {"tile_rows": r.value, "split": sp.value}
 
 
 def gemv_tiling_info(i: int):

@@ -21,8 +21,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparse_act.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["sparsify.hip", "gemv.hip", "calibrate.hip", "gemm.hip", "stream.hip", "linear.hip", "abi.cpp",
-           "validate.cpp"]
+SOURCES = ["sparsify.hip", "gemv.hip", "calibrate.hip", "gemm.hip", "stream.hip", "linear.hip",
+           "grouped.hip", "grouped_backward.hip", "abi.cpp", "validate.cpp"]
+LINEAR_USERS = ["grouped.hip", "grouped_backward.hip", "int8.hip"]  # include linear.hip's tile engine
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "include")]
 DEVICE = ["-x", "hip", "--offload-arch=gfx950",
@@ -34,6 +35,7 @@ def source_hash(src: str) -> str:
     holds the one it was built from."""
     inc = os.path.join(ROOT, "include")
     headers = [os.path.join(d, f) for d in (CSRC, inc) for f in sorted(os.listdir(d)) if f.endswith((".hpp", ".h"))]
+    headers += [os.path.join(CSRC, "linear.hip")] if src in LINEAR_USERS else []
     h = hashlib.sha256()
     for path in [os.path.join(CSRC, src)] + headers:
         with open(path, "rb") as f:

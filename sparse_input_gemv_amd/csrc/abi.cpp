@@ -896,6 +896,300 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
   return run_linear(c, true, fn, stream);
 }
 
+// ---- linear layers grouped by expert ---------------------------------------------
+
+static_assert(SA_MAX_EXPERTS == sa::kMaxGroupedExperts, "header and library agree");
+
+static int run_grouped(const sa::GroupedCall& c, bool backward, const char* fn, void* stream) {
+  hipError_t e = backward ? sa::launch_grouped_backward(c, as_stream(stream))
+                          : sa::launch_grouped(c, as_stream(stream));
+  if (e == hipErrorNotSupported) {
+    sa::set_error("%s: shape not supported by the compiled kernels", fn);
+    return SA_ERR_UNSUPPORTED;
+  }
+  return hip_status(e, fn);
+}
+
+static bool grouped_sizes_ok(int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int act) {
+  return sa::check_linear_sizes("", SA_F16, T, d_in, d_out, act) == SA_OK && experts >= 1 &&
+         experts <= SA_MAX_EXPERTS;
+}
+
+size_t grouped_linear_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out) {
+  return grouped_sizes_ok(T, experts, d_in, d_out, 0) ? sa::grouped_workspace_bytes(false, T, experts, d_in, d_out) : 0;
+}
+
+size_t grouped_gated_linear_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out) {
+  return grouped_sizes_ok(T, experts, d_in, d_out, 0) ? sa::grouped_workspace_bytes(true, T, experts, d_in, d_out) : 0;
+}
+
+size_t grouped_linear_backward_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out,
+                                               int act, int with_dbias) {
+  if (!grouped_sizes_ok(T, experts, d_in, d_out, act)) return 0;
+  // fp16's need: it holds bf16's
+  return sa::grouped_backward_workspace_bytes(SA_F16, false, T, experts, d_in, d_out, act, with_dbias != 0);
+}
+
+size_t grouped_gated_linear_backward_workspace_bytes(int64_t T, int64_t experts, int64_t d_in, int64_t d_out) {
+  if (!grouped_sizes_ok(T, experts, d_in, d_out, 0)) return 0;
+  return sa::grouped_backward_workspace_bytes(SA_F16, true, T, experts, d_in, d_out, 0, false);
+}
+
+int grouped_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wt, int64_t ldw,
+                   int64_t sw, int64_t experts, const int32_t* offsets, int64_t d_in, int64_t d_out,
+                   const void* bias, int act, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                   void* pre, int64_t ldpre, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "grouped_linear";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_grouped(fn, experts, offsets);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wt", wt, ldw, d_out, false);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wt", wt, experts, sw, d_in, d_out, ldw, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "residual", residual, ldr, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "y", y, ldy, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "pre", pre, ldpre, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "bias", bias);
+  const void* outs[2] = {y, pre};
+  const char* names[2] = {"y", "pre"};
+  for (int i = 0; i < 2; ++i) {
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "x", x);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "wt", wt);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "bias", bias);
+  }
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "y", y);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "pre", pre, "residual", residual);
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes, sa::grouped_workspace_bytes(false, T, experts, d_in, d_out));
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  sa::GroupedCall c;
+  c.dtype = dtype;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.experts = experts;
+  c.offsets = offsets;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wt);
+  c.ldw[0] = ldw;
+  c.sw[0] = experts > 1 ? sw : 0;
+  c.bias = in16(bias);
+  c.res = in16(residual);
+  c.ldr = ldr;
+  c.y = out16(y);
+  c.ldy = ldy;
+  c.pre[0] = out16(pre);
+  c.ldpre[0] = ldpre;
+  c.ws = ws;
+  return run_grouped(c, false, fn, stream);
+}
+
+int grouped_gated_linear(int dtype, const void* x, int64_t ldx, int64_t T, const void* wgt, int64_t ldwg,
+                         int64_t swg, const void* wut, int64_t ldwu, int64_t swu, int64_t experts,
+                         const int32_t* offsets, int64_t d_in, int64_t d_out, int act, void* h,
+                         int64_t ldh, void* g, int64_t ldg, void* u, int64_t ldu, void* ws,
+                         size_t ws_bytes, void* stream) {
+  const char* fn = "grouped_gated_linear";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_grouped(fn, experts, offsets);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wgt", wgt, ldwg, d_out, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wut", wut, ldwu, d_out, false);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wgt", wgt, experts, swg, d_in, d_out, ldwg, false);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wut", wut, experts, swu, d_in, d_out, ldwu, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "h", h, ldh, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_both(fn, "g", g, "u", u);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "g", g, ldg, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "u", u, ldu, d_out, true);
+  const void* outs[3] = {h, g, u};
+  const char* names[3] = {"h", "g", "u"};
+  for (int i = 0; i < 3; ++i) {
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "x", x);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "wgt", wgt);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], "wut", wut);
+    for (int j = 0; j < i; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], names[j], outs[j]);
+  }
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes, sa::grouped_workspace_bytes(true, T, experts, d_in, d_out));
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  sa::GroupedCall c;
+  c.dtype = dtype;
+  c.gated = true;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.experts = experts;
+  c.offsets = offsets;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wgt);
+  c.ldw[0] = ldwg;
+  c.sw[0] = experts > 1 ? swg : 0;
+  c.w[1] = in16(wut);
+  c.ldw[1] = ldwu;
+  c.sw[1] = experts > 1 ? swu : 0;
+  c.y = out16(h);
+  c.ldy = ldh;
+  c.pre[0] = out16(g);
+  c.ldpre[0] = ldg;
+  c.pre[1] = out16(u);
+  c.ldpre[1] = ldu;
+  c.ws = ws;
+  return run_grouped(c, false, fn, stream);
+}
+
+int grouped_linear_backward(int dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t T,
+                            const void* wt, int64_t ldw, int64_t sw, int64_t experts,
+                            const int32_t* offsets, int64_t d_in, int64_t d_out, int act,
+                            const void* pre, int64_t ldpre, void* dx, int64_t lddx, void* dwt,
+                            int64_t lddwt, int64_t sdwt, void* dbias, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const char* fn = "grouped_linear_backward";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_grouped(fn, experts, offsets);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dy", dy, lddy, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, dwt == nullptr || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wt", wt, ldw, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wt", wt, experts, sw, d_in, d_out, ldw, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "pre", pre, ldpre, d_out, act == SA_ACT_NONE || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dx", dx, lddx, d_in, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwt", dwt, lddwt, d_out, true);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "dwt", dwt, experts, sdwt, d_in, d_out, lddwt, true);
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "dbias", dbias);
+  const void* ins[4] = {dy, x, wt, pre};
+  const char* names[4] = {"dy", "x", "wt", "pre"};
+  for (int i = 0; i < 4; ++i) {
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dx", dx, names[i], ins[i]);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dwt", dwt, names[i], ins[i]);
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "dbias", dbias, names[i], ins[i]);
+  }
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "dx", dx, "dwt", dwt);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "dbias", dbias, "dx", dx);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "dbias", dbias, "dwt", dwt);
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes,
+                             sa::grouped_backward_workspace_bytes(dtype, false, T, experts, d_in, d_out, act,
+                                                                  dbias != nullptr));
+  if (st != SA_OK) return st;
+  sa::GroupedCall c;
+  c.dtype = dtype;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.experts = experts;
+  c.offsets = offsets;
+  c.dy = in16(dy);
+  c.lddy = lddy;
+  c.x = in16(x);
+  c.ldx = ldx;
+  c.w[0] = in16(wt);
+  c.ldw[0] = ldw;
+  c.sw[0] = experts > 1 ? sw : 0;
+  c.pre[0] = out16(pre);
+  c.ldpre[0] = ldpre;
+  c.dx = out16(dx);
+  c.lddx = lddx;
+  c.dw[0] = out16(dwt);
+  c.lddw[0] = lddwt;
+  c.sdw[0] = experts > 1 ? sdwt : 0;
+  c.dbias = out16(dbias);
+  c.ws = ws;
+  return run_grouped(c, true, fn, stream);
+}
+
+int grouped_gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x, int64_t ldx,
+                                  int64_t T, const void* wgt, int64_t ldwg, int64_t swg, const void* wut,
+                                  int64_t ldwu, int64_t swu, int64_t experts, const int32_t* offsets,
+                                  int64_t d_in, int64_t d_out, int act, const void* g, int64_t ldg,
+                                  const void* u, int64_t ldu, void* dx, int64_t lddx, void* dwgt,
+                                  int64_t lddwg, int64_t sdwg, void* dwut, int64_t lddwu, int64_t sdwu,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "grouped_gated_linear_backward";
+  sa::clear_error();
+  int st = sa::check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK) st = sa::check_grouped(fn, experts, offsets);
+  if (st == SA_OK) st = sa::check_linear_both(fn, "dwgt", dwgt, "dwut", dwut);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dh", dh, lddh, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, dwgt == nullptr || T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wgt", wgt, ldwg, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wut", wut, ldwu, d_out, dx == nullptr);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wgt", wgt, experts, swg, d_in, d_out, ldwg, false);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "wut", wut, experts, swu, d_in, d_out, ldwu, false);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "g", g, ldg, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "u", u, ldu, d_out, T == 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dx", dx, lddx, d_in, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwgt", dwgt, lddwg, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "dwut", dwut, lddwu, d_out, true);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "dwgt", dwgt, experts, sdwg, d_in, d_out, lddwg, true);
+  if (st == SA_OK) st = sa::check_grouped_stride(fn, "dwut", dwut, experts, sdwu, d_in, d_out, lddwu, true);
+  const void* ins[6] = {dh, x, wgt, wut, g, u};
+  const char* in_names[6] = {"dh", "x", "wgt", "wut", "g", "u"};
+  const void* outs[3] = {dx, dwgt, dwut};
+  const char* names[3] = {"dx", "dwgt", "dwut"};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 6; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], in_names[j], ins[j]);
+    for (int j = 0; j < i; ++j)
+      if (st == SA_OK) st = sa::check_linear_distinct(fn, names[i], outs[i], names[j], outs[j]);
+  }
+  if (st == SA_OK)
+    st = sa::check_linear_ws(fn, ws, ws_bytes,
+                             sa::grouped_backward_workspace_bytes(dtype, true, T, experts, d_in, d_out, act, false));
+  if (st != SA_OK) return st;
+  sa::GroupedCall c;
+  c.dtype = dtype;
+  c.gated = true;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.experts = experts;
+  c.offsets = offsets;
+  c.dy = in16(dh);
+  c.lddy = lddh;
+  c.x = in16(x);
+  c.ldx = ldx;
+  const void* w[2] = {wgt, wut};
+  const int64_t ldw[2] = {ldwg, ldwu}, sw[2] = {swg, swu};
+  void* dw[2] = {dwgt, dwut};
+  const int64_t lddw[2] = {lddwg, lddwu}, sdw[2] = {sdwg, sdwu};
+  const void* pre[2] = {g, u};
+  const int64_t ldpre[2] = {ldg, ldu};
+  for (int i = 0; i < 2; ++i) {
+    c.w[i] = in16(w[i]);
+    c.ldw[i] = ldw[i];
+    c.sw[i] = experts > 1 ? sw[i] : 0;
+    c.dw[i] = out16(dw[i]);
+    c.lddw[i] = lddw[i];
+    c.sdw[i] = experts > 1 ? sdw[i] : 0;
+    c.pre[i] = out16(pre[i]);
+    c.ldpre[i] = ldpre[i];
+  }
+  c.dx = out16(dx);
+  c.lddx = lddx;
+  c.ws = ws;
+  return run_grouped(c, true, fn, stream);
+}
+
+int sa_grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int* rows, int* split) {
+  sa::clear_error();
+  if (!grouped_sizes_ok(T, experts, d_in, d_out, 0) || !rows || !split ||
+      sa::grouped_plan(op, T, experts, d_in, d_out, rows, split) != 0) {
+    sa::set_error("sa_grouped_plan: unknown op, sizes out of range or a NULL output");
+    return SA_ERR_INVALID_ARG;
+  }
+  return SA_OK;
+}
+
 int sa_set_linear_tuning(int tile, int split) {
   sa::clear_error();
   if (sa::linear_set_tuning(tile, split) != 0) {

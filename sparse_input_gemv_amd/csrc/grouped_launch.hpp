@@ -1,0 +1,169 @@
+// Launches of the products grouped by expert, which grouped.hip (forward) and
+// grouped_backward.hip share.  The kernel is the dense layers' (lin_run) on
+// items that carry their expert: every workgroup first turns the offsets,
+// which the host never sees, into a table of row tiles in its LDS.
+//
+// Few rows per expert: the steps of all tiles are dealt evenly over the
+// workgroups, as in the dense layers, but the tiles' number is known on the
+// device only.  So partial sums belong to shares, not tiles: a share can hold
+// part of two tiles at most, its first and its last, and those it holds whole
+// it finishes.  The share that begins a tile it does not end writes the tile
+// down for k_grp_reduce.
+#pragma once
+
+#define SA_LINEAR_ENGINE_ONLY
+#include "linear.hip"
+
+namespace sa {
+namespace {
+
+template <int LAY, int BM>
+constexpr int table_lg() {  // dW: the table's rows alone are used
+  return LAY == kDw ? 6 : __builtin_ctz(BM);
+}
+template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(256, 1) void k_grp(GroupP p) {
+  __shared__ __align__(16) uint8_t S[lin_lds<LAY, BM, BN, NS>()];
+  __shared__ GroupTab tab;
+  group_table(p.offsets, p.E, p.T, table_lg<LAY, BM>(), tab);
+  lin_run<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S, &tab);
+}
+
+// Sums the partials of the tile that share blockIdx.x begins and does not end
+// (if any) and finishes rows 16 blockIdx.y .. + 15, 8 columns per thread.
+template <int DT, bool GATED>
+__global__ __launch_bounds__(256) void k_grp_reduce(GroupP p, int lbm) {
+  const CutTile c = p.cut[blockIdx.x];
+  const int row = (int)blockIdx.y * 16 + (int)threadIdx.x / 16, col = (int)threadIdx.x % 16 * 8;
+  const int n = c.n0 + col;
+  if (c.shares == 0 || row >= c.rows || n >= p.N) return;
+  constexpr int BN = GATED ? 256 : 128;
+  const float* const at = p.part + row * BN + col;
+  const int64_t tile = (int64_t)BN << lbm;
+  F8 f[kChains] = {}, u[kChains] = {};
+  for (int s = 0; s < c.shares; s += kChains) {
+#pragma unroll
+    for (int k = 0; k < kChains; ++k) {
+      if (s + k >= c.shares) break;
+      const float* q = at + (((int64_t)blockIdx.x + s + k) * 2 + (s + k == 0)) * tile;
+      add_part(f[k], q);
+      if constexpr (GATED) add_part(u[k], q + BN / 2);
+    }
+  }
+  LinP l = p;
+  if (l.bias) l.bias += c.e * (int64_t)p.N;
+  if constexpr (GATED) finish_gated<DT>(l, c.m0 + row, n, add_chains(f), add_chains(u));
+  else finish_linear<DT, DT == SA_F16>(l, 0, c.m0 + row, n, add_chains(f));
+}
+
+// The compiled tiles: 256 x 256, and 128, 64, 32 or 16 rows x 128 (gated: 128
+// of g and of u).
+constexpr int kGrpTiles = 5;
+constexpr int kGrpM[kGrpTiles] = {256, 128, 64, 32, 16}, kGrpN[kGrpTiles] = {256, 128, 128, 128, 128};
+
+struct GrpPlan {
+  int tile, split;  // split: shares, 0 for whole tiles
+  int64_t tiles;    // at most
+};
+
+inline int64_t grp_row_tiles(int tile, int64_t T, int64_t E) {  // at most
+  return T / kGrpM[tile] + (E < T ? E : T);
+}
+
+// The tile and split with the smallest estimated time, for rows spread evenly
+// over the experts (the host knows no more).  An expert's rows fill tiles of
+// BM rows but for half of the last one.  Times per step as in the dense plan.
+inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, int64_t K, int segs) {
+  static const double alone[2][kGrpTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38}, {1.45, 0.95, 0.60, 0.55, 0.50}};
+  static const double paired[kGrpTiles] = {0, 0.50, 0.36, 0.25, 0.22};
+  const int64_t steps = ((K + BK - 1) / BK) * segs;
+  const double used = (double)(E < T ? E : T), mean = used > 0 ? T / used : 0;
+  int tuned_tile, tuned_split;
+  linear_tuning(&tuned_tile, &tuned_split);
+  if (tuned_tile >= kGrpTiles) tuned_tile = -1;
+  GrpPlan best{kGrpTiles - 1, 0, 0};
+  double least = 1e30;
+  for (int t = 0; t < kGrpTiles; ++t) {
+    if (tuned_tile >= 0 && t != tuned_tile) continue;
+    const int64_t nt = (N + (gated ? 128 : kGrpN[t]) - 1) / (gated ? 128 : kGrpN[t]);
+    const int64_t most = grp_row_tiles(t, T, E) * nt;
+    const double per = mean <= kGrpM[t] / 2 ? 1 : mean / kGrpM[t] + 0.5;  // row tiles of an expert
+    const double tiles = used * per * nt;
+    const bool pairs = t > 0 && !gated;
+    double step = alone[gated][t];
+    if (t > 0 && per < 4) {
+      const double stream = (gated ? 32768 : 16384) / (per <= 1.5 ? 26e3 : 40e3) + 0.1 * step;
+      step = stream > step ? stream : step;
+    }
+    const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
+    const int64_t cus = pairs ? 2 * kCus : kCus;
+    const double rounds = tiles <= cus ? 1 : (int64_t)(tiles / cus) + 1;
+    const double whole = rounds * (steps * (tiles > kCus ? both : step) + 4);
+    if ((tuned_split <= 0) && whole < least) {
+      least = whole;
+      best = GrpPlan{t, 0, most};
+    }
+    // even shares, one workgroup per CU; positions times shares fit 31 bits
+    int64_t shares = tuned_split > 0 ? tuned_split : kCus;
+    while (shares & (shares - 1)) shares &= shares - 1;
+    if (t == 0 || tuned_split == 0 || most * steps * shares >= 0x7fffffffLL) continue;
+    const double parts = shares * 2.0 * (mean < kGrpM[t] ? mean : kGrpM[t]) * (gated ? 256 : 128) * 8 / 4e6;
+    const double time = tiles * steps / shares * step + 8 + parts;
+    if (time < least) {
+      least = time;
+      best = GrpPlan{t, (int)shares, most};
+    }
+  }
+  if (best.tiles == 0) best.tiles = grp_row_tiles(best.tile, T, E) * ((N + 127) / 128);
+  return best;
+}
+
+inline size_t grp_part_bytes(const GrpPlan& pl, bool gated) {
+  if (!pl.split) return 0;
+  return round256(pl.split * sizeof(CutTile)) + (size_t)pl.split * 2 * kGrpM[pl.tile] * (gated ? 256 : 128) * 4;
+}
+
+template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
+void grp_tile(const GroupP& p, int64_t items, hipStream_t s) {  // items: shares or tiles
+  constexpr int64_t most = kCus * (160 * 1024 / (lin_lds<LAY, BM, BN, NS>() + (int)sizeof(GroupTab)));
+  const dim3 grid((unsigned)(p.split || items < most ? items : most));
+  hipLaunchKernelGGL((k_grp<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+}
+
+// Forward and dx.
+template <int DT, int LAY, bool GATED>
+hipError_t launch_grp(GroupP p, void* ws, hipStream_t s) {
+  static_assert(LAY != kDw, "rows are grouped");
+  if (p.T == 0 || p.N == 0) return hipSuccess;
+  const GrpPlan pl = grp_plan(LAY, GATED, p.T, p.E, p.N, p.K, p.segs);
+  if (pl.tiles > 0x7fffffffLL) return hipErrorNotSupported;
+  p.split = pl.split;
+  p.cut = reinterpret_cast<CutTile*>(ws);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + round256(pl.split * sizeof(CutTile)));
+  const int64_t items = pl.split ? pl.split : pl.tiles;
+  constexpr int SB = GATED ? 256 : 128;
+  constexpr int EPI = LAY == kFwd ? kGeneral : DT == SA_F16 ? kScaled : kPlain;
+  if (pl.tile == 0) {
+    if (LAY == kFwd && (GATED ? !p.pre[0] : !p.bias && !p.pre[0] && p.act == SA_ACT_NONE && !p.res))
+      grp_tile<DT, LAY, GATED, LAY == kFwd ? kPlain : EPI, 256, 256, 2, 2, 2>(p, items, s);
+    else
+      grp_tile<DT, LAY, GATED, EPI, 256, 256, 2, 2, 2>(p, items, s);
+  } else if (pl.tile == 1) {
+    grp_tile<DT, LAY, GATED, EPI, 128, SB, 2, 2, GATED ? 3 : 2>(p, items, s);
+  } else if (pl.tile == 2) {
+    grp_tile<DT, LAY, GATED, EPI, 64, SB, 1, 4, 3>(p, items, s);
+  } else if (pl.tile == 3) {
+    grp_tile<DT, LAY, GATED, EPI, 32, SB, 1, 4, GATED ? 4 : 3>(p, items, s);
+  } else {
+    grp_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, GATED ? 4 : 3>(p, items, s);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !pl.split) return e;
+  const int rows = kGrpM[pl.tile] < p.T ? kGrpM[pl.tile] : p.T;
+  hipLaunchKernelGGL((k_grp_reduce<DT, GATED>), dim3(pl.split, (rows + 15) / 16), dim3(256), 0, s, p,
+                     __builtin_ctz(kGrpM[pl.tile]));
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace sa

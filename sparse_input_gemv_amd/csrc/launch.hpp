@@ -185,9 +185,26 @@ size_t linear_workspace_bytes(bool gated, int64_t T, int64_t d_in, int64_t d_out
 size_t linear_backward_workspace_bytes(int dtype, bool gated, int64_t T, int64_t d_in, int64_t d_out,
                                        int act, bool dbias);
 int linear_set_tuning(int tile, int split);
+void linear_tuning(int* tile, int* split);  // as set, -1: automatic
 int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* cols, int* split,
                 int64_t* tiles);
 hipError_t launch_linear(const LinearCall& c, hipStream_t s);
 hipError_t launch_linear_backward(const LinearCall& c, hipStream_t s);
+
+// ---- linear layers grouped by expert (grouped.hip, grouped_backward.hip) -------
+// Matrices per expert lie sw (weights) or sdw (their gradients) elements
+// apart; bias and dbias are [experts][d_out].
+struct GroupedCall : LinearCall {
+  const int32_t* offsets = nullptr;  // [experts + 1], on the device
+  int64_t experts = 0;
+  int64_t sw[2] = {0, 0}, sdw[2] = {0, 0};
+};
+constexpr int64_t kMaxGroupedExperts = 512;
+size_t grouped_workspace_bytes(bool gated, int64_t T, int64_t experts, int64_t d_in, int64_t d_out);
+size_t grouped_backward_workspace_bytes(int dtype, bool gated, int64_t T, int64_t experts, int64_t d_in,
+                                        int64_t d_out, int act, bool dbias);
+int grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int* rows, int* split);
+hipError_t launch_grouped(const GroupedCall& c, hipStream_t s);
+hipError_t launch_grouped_backward(const GroupedCall& c, hipStream_t s);
 
 }  // namespace sa

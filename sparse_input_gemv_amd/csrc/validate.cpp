@@ -363,6 +363,29 @@ int check_linear_both(const char* fn, const char* a, const void* pa, const char*
   return SA_OK;
 }
 
+int check_grouped(const char* fn, int64_t experts, const void* offsets) {
+  REQUIRE(experts >= 1, SA_ERR_INVALID_ARG, "%s: experts must be >= 1 (got %lld)", fn, (long long)experts);
+  REQUIRE(experts <= SA_MAX_EXPERTS, SA_ERR_UNSUPPORTED, "%s: experts must be at most %d", fn, SA_MAX_EXPERTS);
+  REQUIRE(offsets != nullptr, SA_ERR_INVALID_ARG, "%s: offsets is NULL", fn);
+  REQUIRE(aligned(offsets, 4), SA_ERR_INVALID_ARG, "%s: offsets must be 4-byte aligned", fn);
+  return SA_OK;
+}
+
+int check_grouped_stride(const char* fn, const char* name, const void* p, int64_t experts, int64_t stride,
+                         int64_t rows, int64_t cols, int64_t ld, bool output) {
+  if (p == nullptr || experts == 1) return SA_OK;
+  REQUIRE(stride >= 0 && stride % 8 == 0, SA_ERR_INVALID_ARG,
+          "%s: the expert stride of %s must be a multiple of 8, not negative (got %lld)", fn, name,
+          (long long)stride);
+  REQUIRE(stride <= kMaxLinDim * kMaxLinDim, SA_ERR_UNSUPPORTED,
+          "%s: the expert stride of %s must be at most 2^42", fn, name);
+  if (!output) return SA_OK;
+  // one after another, or every expert's columns within each row
+  REQUIRE(stride >= (rows - 1) * ld + cols || (stride >= cols && ld >= (experts - 1) * stride + cols),
+          SA_ERR_INVALID_ARG, "%s: experts' matrices of %s overlap", fn, name);
+  return SA_OK;
+}
+
 int check_linear_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return SA_OK;
   REQUIRE(ws != nullptr && ws_bytes >= need, SA_ERR_WORKSPACE,

@@ -62,6 +62,11 @@ int check_linear_distinct(const char* fn, const char* out, const void* o, const 
                           const void* i);
 int check_linear_both(const char* fn, const char* a, const void* pa, const char* b,
                       const void* pb);
+// By expert: their number, the offsets, and the distance between experts'
+// rows x cols matrices (of an output: apart).
+int check_grouped(const char* fn, int64_t experts, const void* offsets);
+int check_grouped_stride(const char* fn, const char* name, const void* p, int64_t experts, int64_t stride,
+                         int64_t rows, int64_t cols, int64_t ld, bool output);
 int check_linear_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need);
 int check_dense_gemm(const void* x, int64_t T, int64_t d_in, const void* wt, int64_t d_out,
                      const void* y);
