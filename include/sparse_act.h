@@ -610,6 +610,53 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
                           void* stream);
 size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out);
 
+/* ---- linear layers in 8-bit integers ------------------------------------------- */
+
+/*
+ * Activations with a scale per token (row), weights with one per output
+ * channel, products in 8-bit integers with exact 32-bit sums.  Common to the
+ * calls below:
+ * - `dtype` (SA_F16 or SA_BF16) is the type of the 16-bit matrices and of bias.
+ *   Their strides, alignment and overlap are the dense layers'.
+ * - Codes are int8, in -127 .. 127 where the quantisers wrote them; a matrix of
+ *   them has a row stride in elements, a multiple of 16, at least the row
+ *   length, at most 2^21, and is 16-byte aligned, as are scales (fp32).
+ * - Codes of a row (or channel) with largest magnitude m: the scale s is the
+ *   fp32 quotient m / 127, a code the exact quotient x / s rounded to the
+ *   nearest integer, halves to even.  m = 0 gives s = 0 and codes 0; Inf or
+ *   NaN in the row gives s = NaN and codes 0.
+ * - d_in is a positive multiple of 16, at most 2^17; d_out a positive multiple of
+ *   8, at most 2^21; 0 <= T <= 2^22.
+ * - Integer sums are exact: equal calls give equal bits, whatever the split.
+ */
+
+/* act_quantize_int8 -- codes xq [T][d_in] and scales sx [T] of the rows of x. */
+int act_quantize_int8(int dtype, const void* x, int64_t ldx, int64_t T, int64_t d_in, int8_t* xq,
+                      int64_t ldq, float* sx, void* stream);
+
+/* weight_quantize_int8 -- codes wq [d_out][d_in] (W, not its transpose: d_in
+ * contiguous) and scales sw [d_out] of the columns of wt [d_in][d_out].  Done
+ * once per weight; `ws` as for the dense layers. */
+int weight_quantize_int8(int dtype, const void* wt, int64_t ldw, int64_t d_in, int64_t d_out, int8_t* wq,
+                         int64_t ldq, float* sw, void* ws, size_t ws_bytes, void* stream);
+size_t weight_quantize_int8_workspace_bytes(int64_t d_in, int64_t d_out);
+
+/*
+ * int8_linear -- y[t][o] = act(sx[t] sw[o] sum_k xq[t][k] wq[o][k] + bias[o]) +
+ * residual[t][o]; the scaled sum, the activation and the rest in fp32, y
+ * rounded once.
+ *   sx given: x holds int8 codes [T][d_in] and sx [T] their scales;
+ *   sx NULL: x holds `dtype` values, quantised as act_quantize_int8 does within
+ *   the call (`with_sx` of the workspace size is 0 then, else 1).
+ *   wq [d_out][d_in], sw [d_out]; bias [d_out] or NULL; residual, y [T][d_out]
+ *   (residual NULL allowed, and it may be y).
+ */
+int int8_linear(int dtype, const void* x, int64_t ldx, const float* sx, int64_t T, const int8_t* wq,
+                int64_t ldw, const float* sw, int64_t d_in, int64_t d_out, const void* bias, int act,
+                const void* residual, int64_t ldr, void* y, int64_t ldy, void* ws, size_t ws_bytes,
+                void* stream);
+size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int with_sx);
+
 /* ---- linear layers grouped by expert ------------------------------------------ */
 
 /*

@@ -34,6 +34,7 @@ __all__ = [
     "masked_gemv",
     "dense_gemv", "masked_swiglu_down", "weight_col_norms", "nm_act_spmm", "nm_shared_spmm",
     "dense_gemm", "dense_linear", "dense_linear_backward", "gated_linear", "gated_linear_backward",
+    "act_quantize_int8", "weight_quantize_int8", "int8_linear",
     "grouped_linear", "grouped_linear_backward", "grouped_gated_linear", "grouped_gated_linear_backward",
     "ACTIVATIONS", "set_linear_tuning", "linear_plan", "grouped_plan", "set_gemv_tuning", "set_gemm_tuning", "gemm_plan", "gemv_tiling_info", "workspace_bytes",
     "workspace_zero_bytes", "scratch", "MAX_BATCH",
@@ -99,6 +100,12 @@ _SIGNATURES = {
                                      _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                      _i64, _vp, _sz, _vp]),
     "gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "act_quantize_int8": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "weight_quantize_int8": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "weight_quantize_int8_workspace_bytes": (_sz, [_i64, _i64]),
+    "int8_linear": (_i32, [_i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _vp, _i64,
+                           _vp, _i64, _vp, _sz, _vp]),
+    "int8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "grouped_linear": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i32,
                               _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
     "grouped_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
@@ -757,7 +764,7 @@ def _lasting(stream_id: int, handle: int) -> bool:
     return handle == 0 if stream_id == 0 else stream_id % 2 == 1 and stream_id != handle
 
 
-def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
+def _lin_call(fn: str, like: torch.Tensor, sizes: tuple | None, *args) -> None:
     """Runs ``fn`` on the current stream of ``like``'s device, with scratch
     of its own from torch's allocator: calls on other streams and captured
     graphs share none.  The forward calls' counters belong to the stream; a
@@ -767,6 +774,8 @@ def _lin_call(fn: str, like: torch.Tensor, sizes: tuple, *args) -> None:
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _lin_call(fn, like, sizes, *args)
+    if sizes is None:  # a call without scratch
+        return _check(getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index)), fn)
     need = _lin_ws_bytes(fn, *sizes)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     # the handle alone: a torch.cuda.Stream object costs 1.6 us of a 10 us call
@@ -907,6 +916,113 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, wgt: torch.Tensor, 
               _act(act), g.data_ptr(), ldg, u.data_ptr(), ldu, _ptr(dx), lddx, _ptr(dwgt), lddg,
               _ptr(dwut), lddu)
     return None if dx is None else _ret(dx, squeeze), dwgt, dwut
+
+
+# ---- linear layers in 8-bit integers ---------------------------------------------
+
+def _codes(t, name: str, device, rows: int, cols: int) -> int:
+    """Checks a ``[rows][cols]`` matrix of int8 codes and returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int8:
+        raise ValueError(f"{name} must be an int8 tensor on {device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _scales(t, name: str, device, n: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a float32 tensor on {device}")
+    if t.shape != (n,) or (t.stride(0) != 1 and n > 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
+
+
+def _codes_out(q, s, names, device, rows: int, cols: int):
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    if s is None:
+        s = torch.empty(rows, dtype=torch.float32, device=device)
+    _scales(s, names[1], device, rows)
+    return q, _codes(q, names[0], device, rows, cols), s
+
+
+def act_quantize_int8(x: torch.Tensor, xq: torch.Tensor | None = None, sx: torch.Tensor | None = None):
+    """8-bit codes of fp16 or bf16 rows and a scale per row: ``(xq, sx)`` with
+    ``sx = max|x| / 127`` (fp32) and ``xq`` the exact quotient ``x / sx`` rounded
+    to the nearest integer, halves to even.  A row of zeros has scale 0; one
+    with Inf or NaN has scale NaN and codes 0.  A vector is one row: ``xq`` is
+    a vector then, ``sx`` holds one scale."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    x = _lin_x(x, "x")
+    T, d = x.shape
+    ldx = _lin_mat(x, "x", x, T, d)
+    if squeeze and xq is not None and xq.dim() == 1:
+        xq = xq[None]
+    xq, ldq, sx = _codes_out(xq, sx, ("xq", "sx"), x.device, T, d)
+    _lin_call("act_quantize_int8", x, None, _LIN_DTYPES[x.dtype], x.data_ptr(), ldx, T, d, xq.data_ptr(),
+              ldq, sx.data_ptr())
+    return _ret(xq, squeeze), sx
+
+
+def weight_quantize_int8(wt: torch.Tensor, wq: torch.Tensor | None = None, sw: torch.Tensor | None = None):
+    """8-bit codes and a scale per output channel of ``wt[d_in][d_out]``, for
+    ``int8_linear``: ``(wq, sw)`` with ``wq[d_out][d_in]`` (the weight itself, not
+    its transpose).  Rounded as ``act_quantize_int8`` rounds rows."""
+    wt = _lin_x(wt, "wt")
+    d_in, d_out = wt.shape
+    ldw = _lin_mat(wt, "wt", wt, d_in, d_out)
+    wq, ldq, sw = _codes_out(wq, sw, ("wq", "sw"), wt.device, d_out, d_in)
+    _lin_call("weight_quantize_int8", wt, (d_in, d_out), _LIN_DTYPES[wt.dtype], wt.data_ptr(), ldw, d_in,
+              d_out, wq.data_ptr(), ldq, sw.data_ptr())
+    return wq, sw
+
+
+def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, sx: torch.Tensor | None = None,
+                bias: torch.Tensor | None = None, act: str = "none", residual: torch.Tensor | None = None,
+                y: torch.Tensor | None = None, dtype: torch.dtype | None = None):
+    """``y = act(sx sw (xq Wq^T) + bias) + residual`` with exact integer sums, for
+    the codes ``wq[d_out][d_in]`` and scales ``sw`` of ``weight_quantize_int8``.
+    ``x`` is fp16 or bf16 and quantised within the call, or int8 codes with
+    their scales ``sx``; ``y``, ``bias`` and ``residual`` have ``x``'s type, or for
+    codes ``dtype`` (fp16 where neither it nor ``y`` is given).  ``y`` may be
+    ``residual``."""
+    squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
+    if sx is None:
+        x = _lin_x(x, "x")
+        if dtype is not None and dtype != x.dtype:
+            raise ValueError(f"dtype must be {x.dtype}, as x is")
+        dtype = x.dtype
+    else:
+        if not isinstance(x, torch.Tensor) or x.device.type != "cuda" or x.dim() not in (1, 2):
+            raise ValueError("x must be a vector or [rows][d] on a GPU")
+        x = x[None] if x.dim() == 1 else x
+        dtype = dtype or (y.dtype if y is not None else torch.float16)
+        if dtype not in _LIN_DTYPES:
+            raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
+    T, d_in = x.shape
+    if sx is None:
+        ldx = _lin_mat(x, "x", x, T, d_in)
+    else:
+        ldx = _codes(x, "x", x.device, T, d_in)
+        _scales(sx, "sx", x.device, T)
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
+        raise ValueError("wq must be a tensor [d_out][d_in]")
+    d_out = wq.shape[0]
+    ldw = _codes(wq, "wq", x.device, d_out, d_in)
+    _scales(sw, "sw", x.device, d_out)
+    like = torch.empty(0, dtype=dtype, device=x.device) if x.dtype != dtype else x
+    if bias is not None:
+        _lin_vec(bias, "bias", like, d_out)
+    ldr = 0 if residual is None else _lin_mat(residual, "residual", like, T, d_out)
+    y, ldy = _lin_out(y, "y", like, T, d_out)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, bias, residual)):
+        warnings.warn("int8_linear is outside autograd and has no gradient: its output carries no graph. "
+                      "Call it under torch.no_grad().", stacklevel=2)
+    _lin_call("int8_linear", x, (T, d_in, d_out, int(sx is not None)), _LIN_DTYPES[dtype], x.data_ptr(),
+              ldx, _ptr(sx), T, wq.data_ptr(), ldw, sw.data_ptr(), d_in, d_out, _ptr(bias), _act(act),
+              _ptr(residual), ldr, y.data_ptr(), ldy)
+    return _ret(y, squeeze)
 
 
 # ---- linear layers grouped by expert --------------------------------------------

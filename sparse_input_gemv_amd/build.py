@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libsparse_act.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["sparsify.hip", "gemv.hip", "calibrate.hip", "gemm.hip", "stream.hip", "linear.hip",
-           "grouped.hip", "grouped_backward.hip", "abi.cpp", "validate.cpp"]
+           "grouped.hip", "grouped_backward.hip", "int8.hip", "abi.cpp", "validate.cpp"]
 LINEAR_USERS = ["grouped.hip", "grouped_backward.hip", "int8.hip"]  # include linear.hip's tile engine
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + os.path.join(ROOT, "include")]

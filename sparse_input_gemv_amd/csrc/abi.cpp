@@ -896,6 +896,100 @@ int gated_linear_backward(int dtype, const void* dh, int64_t lddh, const void* x
   return run_linear(c, true, fn, stream);
 }
 
+// ---- linear layers in 8-bit integers ------------------------------------------------
+
+int act_quantize_int8(int dtype, const void* x, int64_t ldx, int64_t T, int64_t d_in, int8_t* xq,
+                      int64_t ldq, float* sx, void* stream) {
+  const char* fn = "act_quantize_int8";
+  sa::clear_error();
+  int st = sa::check_int8_sizes(fn, dtype, T, d_in, 8, 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_int8_codes(fn, "xq", xq, ldq, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_scales(fn, "sx", sx, T == 0);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "xq", xq, "x", x);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "sx", sx, "x", x);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "sx", sx, "xq", xq);
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  return hip_status(sa::launch_act_quantize_int8(dtype, in16(x), ldx, T, d_in, xq, ldq, sx, as_stream(stream)), fn);
+}
+
+size_t weight_quantize_int8_workspace_bytes(int64_t d_in, int64_t d_out) {
+  if (sa::check_int8_sizes("", SA_F16, 0, d_in, d_out, 0) != SA_OK) return 0;
+  return sa::weight_quantize_int8_workspace_bytes(d_in, d_out);
+}
+
+int weight_quantize_int8(int dtype, const void* wt, int64_t ldw, int64_t d_in, int64_t d_out, int8_t* wq,
+                         int64_t ldq, float* sw, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "weight_quantize_int8";
+  sa::clear_error();
+  int st = sa::check_int8_sizes(fn, dtype, 0, d_in, d_out, 0);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "wt", wt, ldw, d_out, false);
+  if (st == SA_OK) st = sa::check_int8_codes(fn, "wq", wq, ldq, d_in, false);
+  if (st == SA_OK) st = sa::check_scales(fn, "sw", sw, false);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "wq", wq, "wt", wt);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "sw", sw, "wt", wt);
+  if (st == SA_OK) st = sa::check_linear_distinct(fn, "sw", sw, "wq", wq);
+  if (st == SA_OK) st = sa::check_linear_ws(fn, ws, ws_bytes, sa::weight_quantize_int8_workspace_bytes(d_in, d_out));
+  if (st != SA_OK) return st;
+  return hip_status(sa::launch_weight_quantize_int8(dtype, in16(wt), ldw, d_in, d_out, wq, ldq, sw, ws,
+                                                    as_stream(stream)), fn);
+}
+
+size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int with_sx) {
+  if (T == 0 || sa::check_int8_sizes("", SA_F16, T, d_in, d_out, 0) != SA_OK) return 0;
+  return sa::int8_linear_workspace_bytes(T, d_in, d_out, with_sx != 0);
+}
+
+int int8_linear(int dtype, const void* x, int64_t ldx, const float* sx, int64_t T, const int8_t* wq,
+                int64_t ldw, const float* sw, int64_t d_in, int64_t d_out, const void* bias, int act,
+                const void* residual, int64_t ldr, void* y, int64_t ldy, void* ws, size_t ws_bytes,
+                void* stream) {
+  const char* fn = "int8_linear";
+  sa::clear_error();
+  int st = sa::check_int8_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st == SA_OK)
+    st = sx ? sa::check_int8_codes(fn, "x", x, ldx, d_in, T == 0) : sa::check_linear_matrix(fn, "x", x, ldx, d_in, T == 0);
+  if (st == SA_OK) st = sa::check_scales(fn, "sx", sx, true);
+  if (st == SA_OK) st = sa::check_int8_codes(fn, "wq", wq, ldw, d_in, false);
+  if (st == SA_OK) st = sa::check_scales(fn, "sw", sw, false);
+  if (st == SA_OK) st = sa::check_linear_vector(fn, "bias", bias);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "residual", residual, ldr, d_out, true);
+  if (st == SA_OK) st = sa::check_linear_matrix(fn, "y", y, ldy, d_out, T == 0);
+  const void* ins[5] = {x, sx, wq, sw, bias};
+  const char* names[5] = {"x", "sx", "wq", "sw", "bias"};
+  for (int i = 0; i < 5; ++i)
+    if (st == SA_OK) st = sa::check_linear_distinct(fn, "y", y, names[i], ins[i]);
+  if (st == SA_OK && T > 0)
+    st = sa::check_linear_ws(fn, ws, ws_bytes, sa::int8_linear_workspace_bytes(T, d_in, d_out, sx != nullptr));
+  if (st != SA_OK) return st;
+  if (T == 0) return SA_OK;
+  sa::Int8Call c;
+  c.dtype = dtype;
+  c.act = act;
+  c.T = T;
+  c.d_in = d_in;
+  c.d_out = d_out;
+  c.x = x;
+  c.ldx = ldx;
+  c.sx = sx;
+  c.wq = wq;
+  c.ldw = ldw;
+  c.sw = sw;
+  c.bias = in16(bias);
+  c.res = in16(residual);
+  c.ldr = ldr;
+  c.y = out16(y);
+  c.ldy = ldy;
+  c.ws = ws;
+  const hipError_t e = sa::launch_int8_linear(c, as_stream(stream));
+  if (e == hipErrorNotSupported) {
+    sa::set_error("%s: shape not supported by the compiled kernels", fn);
+    return SA_ERR_UNSUPPORTED;
+  }
+  return hip_status(e, fn);
+}
+
 // ---- linear layers grouped by expert ---------------------------------------------
 
 static_assert(SA_MAX_EXPERTS == sa::kMaxGroupedExperts, "header and library agree");

@@ -1,0 +1,553 @@
+// Linear layers in 8-bit integers for gfx950: a scale per token and per output
+// channel, exact 32-bit sums.
+//
+//   act_quantize_int8     s = fp32(max|x| / 127), q = round(x / s), by rows
+//   weight_quantize_int8  the same by columns of WT, written as W [d_out][d_in]
+//   int8_linear           y = act(sx sw sum_k xq wq + bias) + residual
+//
+// The product has k contiguous on both sides (a lane's operand is 16 bytes of
+// one row), so W is stored untransposed here, and the dense layers' engine
+// runs it in dx's layout with two integers to a 16-bit word: the same bytes per
+// step and per matrix instruction, twice the operations.  Integer sums may be
+// split anywhere and added in any order: equal calls give equal bits.
+//
+// One token (and up to kGemvRows, while they fit LDS) takes dot products
+// instead: a wave reads rows of W in 1 KB pieces and meets x in LDS.  For one
+// token of 16-bit values every workgroup quantises x itself (d_in values from
+// L2), which saves the second launch.
+#define SA_LINEAR_ENGINE_ONLY
+#include "linear.hip"
+
+namespace sa {
+namespace {
+
+typedef int i2v __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// ---- rounding to 8 bits ------------------------------------------------------------
+// A row's scale from its largest magnitude (the bits of a 16-bit value without
+// its sign, which order magnitudes with Inf and NaN above all others): the
+// rounded quotient, or NaN if the row holds Inf or NaN.
+template <int DT>
+__device__ __forceinline__ float scale_of(uint32_t most) {
+  constexpr uint32_t inf = DT == SA_F16 ? 0x7c00u : 0x7f80u;
+  if (most >= inf) return __builtin_nanf("");
+  return to_f<DT>((uint16_t)most) / 127.f;
+}
+// x / s of the exact quotient, halves to even.  x times the reciprocal may
+// round to a neighbour where the quotient lies next to half a step, so the
+// remainder x - q s decides.  It is exact in fp32: x and q s are multiples of
+// the last place of s unless |x| < s / 2^13, where q = 0.  Scales below 2^-100
+// (bf16 alone has them) and their values are first multiplied by 2^64, so that
+// the reciprocal exists.
+struct Rounder {
+  float s, inv, up;
+  __device__ __forceinline__ explicit Rounder(float scale) {
+    up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+    s = scale * up;
+    inv = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;  // NaN, 0: every q is 0
+  }
+  __device__ __forceinline__ int operator()(float x) const {
+    const float v = x * up;
+    float q = __builtin_rintf(v * inv);
+    const float r = __builtin_fmaf(-q, s, v), twice = 2.f * fabsf(r);
+    const bool odd = (int)q & 1;
+    if (twice > s || (twice == s && odd)) q += __builtin_copysignf(1.f, r);
+    return inv == 0.f ? 0 : (int)q;
+  }
+};
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+template <int DT>
+__device__ __forceinline__ uint2 quant8(u32x4 v, const Rounder& r) {
+  const F8 f = widen8<DT>(v);
+  return uint2{pack4(r(f.v[0]), r(f.v[1]), r(f.v[2]), r(f.v[3])),
+               pack4(r(f.v[4]), r(f.v[5]), r(f.v[6]), r(f.v[7]))};
+}
+// The larger magnitudes of two pairs of 16-bit values.
+__device__ __forceinline__ u16x2 larger(u16x2 a, uint32_t b) {
+  return __builtin_elementwise_max(a, __builtin_bit_cast(u16x2, b & 0x7fff7fffu));
+}
+__device__ __forceinline__ u16x2 larger(u16x2 a, u32x4 b) {
+  return larger(larger(larger(larger(a, b[0]), b[1]), b[2]), b[3]);
+}
+// The largest of the wave's values, uniform.
+__device__ __forceinline__ uint32_t wave_most(u16x2 m) {
+  int v = m[0] > m[1] ? m[0] : m[1];
+  v = wave_running_max(v);
+  return (uint32_t)__builtin_amdgcn_readlane(v, kWave - 1);
+}
+
+// ---- rows --------------------------------------------------------------------------
+// A row per wave (WIDE false: 4 rows per workgroup) or per workgroup, held in
+// registers between its maximum and its rounding (NV chunks of 8 values per
+// thread), or with NV = 0 read twice.  Bound by memory: 2 bytes read and one
+// written per value; the rounding's ~14 operations per value stay below that.
+template <int DT, bool WIDE, int NV>
+__global__ __launch_bounds__(256) void k_quant_rows(const uint16_t* __restrict__ x, int64_t ldx, int64_t T,
+                                                    int d, int8_t* __restrict__ xq, int64_t ldq,
+                                                    float* __restrict__ sx) {
+  __shared__ uint32_t part[4];
+  const int lane = lane_id(), w = uni((int)threadIdx.x / kWave);
+  const int64_t t = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + w;
+  if (!WIDE && t >= T) return;
+  const int at = WIDE ? (int)threadIdx.x : lane, step = WIDE ? 256 : 64, chunks = d / 8;
+  const u32x4* row = reinterpret_cast<const u32x4*>(x + t * ldx);
+  constexpr int N = NV > 0 ? NV : 1;
+  u32x4 v[N];
+  u16x2 m = {0, 0};
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = at + j * step < chunks ? row[at + j * step] : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) m = larger(m, v[j]);
+  } else {
+#pragma unroll 4
+    for (int c = at; c < chunks; c += step) m = larger(m, row[c]);
+  }
+  uint32_t most = wave_most(m);
+  if constexpr (WIDE) {
+    if (lane == 0) part[w] = most;
+    __syncthreads();
+    const uint32_t a = part[0] > part[1] ? part[0] : part[1], b = part[2] > part[3] ? part[2] : part[3];
+    most = a > b ? a : b;
+  }
+  const float s = scale_of<DT>(most);
+  const Rounder r(s);
+  if (at == 0) sx[t] = s;
+  uint2* out = reinterpret_cast<uint2*>(xq + t * ldq);
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (at + j * step < chunks) out[at + j * step] = quant8<DT>(v[j], r);
+  } else {
+#pragma unroll 4
+    for (int c = at; c < chunks; c += step) out[c] = quant8<DT>(row[c], r);
+  }
+}
+
+template <int DT>
+void quant_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t d, int8_t* xq, int64_t ldq, float* sx,
+                hipStream_t s) {
+  auto run = [&](auto wide, auto nv) {
+    constexpr bool W = decltype(wide)::value;
+    hipLaunchKernelGGL((k_quant_rows<DT, W, decltype(nv)::value>), dim3((unsigned)(W ? T : (T + 3) / 4)),
+                       dim3(256), 0, s, x, ldx, T, (int)d, xq, ldq, sx);
+  };
+  using std::integral_constant;
+  const std::true_type wide;
+  // a row per wave where that fills the CUs and a lane holds its part
+  if (d <= 2048 && T >= 4 * kCus) run(std::false_type{}, integral_constant<int, 4>{});
+  else if (d <= 2048) run(wide, integral_constant<int, 1>{});
+  else if (d <= 4096) run(wide, integral_constant<int, 2>{});
+  else if (d <= 8192) run(wide, integral_constant<int, 4>{});
+  else if (d <= 16384) run(wide, integral_constant<int, 8>{});
+  else run(wide, integral_constant<int, 0>{});
+}
+
+// ---- columns (weights) ----------------------------------------------------------------
+// The largest magnitudes of a strip's columns: 512 columns per workgroup, 8
+// per lane, the strip's rows dealt over the waves.
+constexpr int kColStrips = 64;  // at most
+__global__ __launch_bounds__(256) void k_col_most(const uint16_t* __restrict__ wt, int64_t ldw, int64_t K,
+                                                  int N, int64_t strip, uint16_t* __restrict__ part) {
+  __shared__ u32x4 most[4][64];
+  const int lane = lane_id(), w = uni((int)threadIdx.x / kWave);
+  const int n = ((int)blockIdx.x * 64 + lane) * 8;
+  const int64_t k0 = blockIdx.y * strip, k1 = k0 + strip < K ? k0 + strip : K;
+  u16x2 m[4] = {};
+  if (n < N) {
+#pragma unroll 8
+    for (int64_t k = k0 + w; k < k1; k += 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(wt + k * ldw + n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = larger(m[i], (uint32_t)v[i]);
+    }
+  }
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(uint32_t, m[i]);
+  most[w][lane] = o;
+  __syncthreads();
+  if (w == 0 && n < N) {
+#pragma unroll
+    for (int j = 1; j < 4; ++j) {
+      const u32x4 v = most[j][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = larger(m[i], (uint32_t)v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(uint32_t, m[i]);
+    *reinterpret_cast<u32x4*>(part + (int64_t)blockIdx.y * N + n) = o;
+  }
+}
+// 256 k x 64 columns of WT, rounded and turned in LDS: a thread rounds 4 k of 8
+// columns and writes a word of 4 k per column; rows of 65 words keep the
+// lanes' banks apart.
+template <int DT>
+__global__ __launch_bounds__(256) void k_quant_cols(const uint16_t* __restrict__ wt, int64_t ldw, int64_t K,
+                                                    int N, const uint16_t* __restrict__ part, int strips,
+                                                    int8_t* __restrict__ wq, int64_t ldq,
+                                                    float* __restrict__ sw) {
+  __shared__ uint32_t most[4][64];
+  __shared__ float scale[64];
+  __shared__ uint32_t S[64 * 65];
+  const int tid = (int)threadIdx.x, n0 = (int)blockIdx.x * 64;
+  const int64_t k0 = (int64_t)blockIdx.y * 256;
+  u32x4 v[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t k = k0 + (tid / 8 + 32 * h) * 4 + i;
+      const int n = n0 + (tid % 8) * 8;
+      v[h][i] = k < K && n < N ? *reinterpret_cast<const u32x4*>(wt + k * ldw + n) : u32x4{0, 0, 0, 0};
+    }
+  uint32_t m = 0;
+  if (n0 + tid % 64 < N)
+    for (int s = tid / 64; s < strips; s += 4) {
+      const uint32_t o = part[(int64_t)s * N + n0 + tid % 64];
+      m = o > m ? o : m;
+    }
+  most[tid / 64][tid % 64] = m;
+  __syncthreads();
+  if (tid < 64) {
+#pragma unroll
+    for (int j = 1; j < 4; ++j) m = most[j][tid] > m ? most[j][tid] : m;
+    scale[tid] = scale_of<DT>(m);
+    if (blockIdx.y == 0 && n0 + tid < N) sw[n0 + tid] = scale[tid];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = (tid % 8) * 8 + i;
+    const Rounder r(scale[c]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = r(to_f<DT>((uint16_t)(v[h][k][i / 2] >> (16 * (i % 2)))));
+      S[c * 65 + tid / 8 + 32 * h] = pack4(q[0], q[1], q[2], q[3]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int c = tid / 16 + 16 * h, k = (tid % 16) * 4;
+    if (n0 + c < N && k0 + k * 4 < K) {  // K is a multiple of 16
+      const uint32_t* p = S + c * 65 + k;
+      *reinterpret_cast<u32x4*>(wq + (n0 + c) * ldq + k0 + k * 4) = u32x4{p[0], p[1], p[2], p[3]};
+    }
+  }
+}
+int64_t col_strip(int64_t K) {  // rows of a strip: 32 at least
+  const int64_t s = (K + kColStrips - 1) / kColStrips;
+  return s < 32 ? 32 : s;
+}
+
+// ---- dot products: few tokens ---------------------------------------------------------
+struct GemvP {
+  const void* x;    // QUANT: one 16-bit row; else 8-bit rows
+  int64_t ldx;
+  const float* sx;
+  const int8_t* wq;
+  int64_t ldw;
+  const float* sw;
+  int T, N, K;
+  const uint16_t *bias, *res;
+  int64_t ldr;
+  int act;
+  uint16_t* y;
+  int64_t ldy;
+};
+constexpr int kGemvRows = 8;
+constexpr int64_t kGemvLds = 64 * 1024;  // T * d_in at most
+__device__ __forceinline__ int wave_sum(int v) {  // uniform
+  const int s = row16_inclusive_scan(v);
+  return (__builtin_amdgcn_readlane(s, 15) + __builtin_amdgcn_readlane(s, 31)) +
+         (__builtin_amdgcn_readlane(s, 47) + __builtin_amdgcn_readlane(s, 63));
+}
+// CW channels per wave, NT rows of x (those past T are zeros in LDS).
+template <int DT, int NT, int CW, bool QUANT>
+__global__ __launch_bounds__(256) void k_int8_gemv(GemvP p) {
+  extern __shared__ __align__(16) uint8_t X[];  // [NT][K]
+  __shared__ uint32_t part[4];
+  static_assert(!QUANT || NT == 1, "one row is quantised in place");
+  const int tid = (int)threadIdx.x, lane = lane_id(), w = uni(tid / kWave);
+  const int c0 = uni(((int)blockIdx.x * 4 + w) * CW);
+  constexpr int U = NT * CW <= 8 ? 4 : 2;  // pieces of 1 KB per channel in flight
+  u32x4 wv[U][CW];
+  auto fetch = [&](int k) SA_INLINE {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < CW; ++c) {
+        const int at = k + u * 1024 + lane * 16;
+        const bool in = at < p.K && c0 + c < p.N;
+        wv[u][c] = in ? *reinterpret_cast<const u32x4*>(p.wq + (c0 + c) * p.ldw + at) : u32x4{0, 0, 0, 0};
+      }
+  };
+  fetch(0);  // under way while x is made ready
+  float s = 0.f;
+  if constexpr (QUANT) {
+    const u32x4* row = reinterpret_cast<const u32x4*>(p.x);
+    const int chunks = p.K / 8;
+    u16x2 m = {0, 0};
+#pragma unroll 4
+    for (int c = tid; c < chunks; c += 256) m = larger(m, row[c]);
+    const uint32_t mine = wave_most(m);
+    if (lane == 0) part[w] = mine;
+    __syncthreads();
+    const uint32_t a = part[0] > part[1] ? part[0] : part[1], b = part[2] > part[3] ? part[2] : part[3];
+    s = scale_of<DT>(a > b ? a : b);
+    const Rounder r(s);
+#pragma unroll 4
+    for (int c = tid; c < chunks; c += 256) reinterpret_cast<uint2*>(X)[c] = quant8<DT>(row[c], r);
+  } else {
+    const int chunks = p.K / 16;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const u32x4* row = reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(p.x) + t * p.ldx);
+      for (int c = tid; c < chunks; c += 256)
+        reinterpret_cast<u32x4*>(X)[t * chunks + c] = t < p.T ? row[c] : u32x4{0, 0, 0, 0};
+    }
+  }
+  __syncthreads();
+  int acc[NT][CW] = {};
+  for (int k = 0; k < p.K; k += U * 1024) {
+    u32x4 cur[U][CW];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < CW; ++c) cur[u][c] = wv[u][c];
+    if (k + U * 1024 < p.K) fetch(k + U * 1024);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = k + u * 1024 + lane * 16;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        // past the row's end the weights are zeros; x is read where it exists
+        const u32x4 xv = *reinterpret_cast<const u32x4*>(X + t * p.K + (at < p.K ? at : 0));
+#pragma unroll
+        for (int c = 0; c < CW; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[t][c] = __builtin_amdgcn_sdot4((int)cur[u][c][e], (int)xv[e], acc[t][c], false);
+      }
+    }
+  }
+  // lane t * CW + c finishes row t's channel c
+  int sum = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+      const int v = wave_sum(acc[t][c]);
+      sum = lane == t * CW + c ? v : sum;
+    }
+  const int t = lane / CW, n = c0 + lane % CW;
+  if (lane >= NT * CW || t >= p.T || n >= p.N) return;
+  float f = (float)sum * p.sw[n] * (QUANT ? s : p.sx[t]);
+  if (p.bias) f += to_f<DT>(p.bias[n]);
+  with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
+  if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
+  p.y[t * p.ldy + n] = from_f<DT>(f);
+}
+
+template <int DT, int NT, bool QUANT>
+hipError_t gemv(const GemvP& p, hipStream_t s) {
+  const size_t lds = (size_t)NT * p.K;
+  // four channels per wave where that still gives every CU four waves
+  auto run = [&](auto cw) {
+    constexpr int CW = decltype(cw)::value;
+    hipLaunchKernelGGL((k_int8_gemv<DT, NT, CW, QUANT>), dim3((unsigned)((p.N + 4 * CW - 1) / (4 * CW))),
+                       dim3(256), lds, s, p);
+  };
+  if (p.N >= 16 * kCus) run(std::integral_constant<int, 4>{});
+  else run(std::integral_constant<int, 1>{});
+  return hipGetLastError();
+}
+
+// ---- matrix instructions ----------------------------------------------------------------
+template <int DT, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(256, 1) void k_int8(Int8P p) {
+  __shared__ __align__(16) uint8_t S[lin_lds<kDx, BM, BN, NS>()];
+  lin_run<DT, kDx, false, kInt8, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S);
+}
+// Adds the shares' integer partials of 4 columns of a row and finishes them.
+template <int DT>
+__global__ __launch_bounds__(256) void k_int8_reduce(Int8P p, int lbm, int lbn) {
+  const uint32_t n4 = p.N / 4, id = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t m = id / n4;
+  const int n = (int)(id - m * n4) * 4;
+  if (m >= (uint32_t)p.M) return;
+  const int mt = (p.M + (1 << lbm) - 1) >> lbm, nt = (p.N + (1 << lbn) - 1) >> lbn;
+  const uint32_t steps = (uint32_t)((p.K + BK - 1) / BK), TS = mt * nt * steps;
+  const uint32_t at = (uint32_t)((n >> lbn) * mt + (int)(m >> lbm)) * steps;
+  const int slots = share_of(at + steps - 1, TS, p.split) - share_of(at, TS, p.split) + 1;
+  const i4v* q = reinterpret_cast<const i4v*>(p.part + (int64_t)m * p.N + n);
+  const int64_t slot = (int64_t)p.M * p.N / 4;
+  i4v sum = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int s = 0; s < slots; ++s) sum += q[s * slot];
+  const float sx = p.sx[m];
+  uint16_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f = (float)sum[i] * p.sw[n + i] * sx;
+    if (p.bias) f += to_f<DT>(p.bias[n + i]);
+    with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
+    if (p.res) f += to_f<DT>(p.res[m * (int64_t)p.ldr + n + i]);
+    o[i] = from_f<DT>(f);
+  }
+  *reinterpret_cast<uint2*>(p.y[0] + m * (int64_t)p.ldy[0] + n) =
+      uint2{(uint32_t)o[0] | (uint32_t)o[1] << 16, (uint32_t)o[2] | (uint32_t)o[3] << 16};
+}
+
+Plan int8_plan(int64_t T, int64_t d_in, int64_t d_out) {
+  return lin_plan(kDx, false, T, d_out, d_in / 2, 1, 1);
+}
+bool gemv_fits(int64_t T, int64_t d_in) {
+  const int64_t rows = T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
+  return T <= kGemvRows && rows * d_in <= kGemvLds;
+}
+
+template <int DT>
+hipError_t matmul(Int8P p, void* ws, hipStream_t s) {
+  const Plan pl = int8_plan(p.M, (int64_t)p.K * 2, p.N);
+  if (pl.tiles > 0x7fffffffLL) return hipErrorNotSupported;
+  p.split = pl.split;
+  p.part = reinterpret_cast<float*>(ws);
+  const int64_t items = pl.split ? pl.split : pl.tiles;
+  auto run = [&](auto bm, auto bn, auto wm, auto ns) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, NS = decltype(ns)::value;
+    constexpr int64_t most = kCus * (160 * 1024 / lin_lds<kDx, BM, BN, NS>());
+    hipLaunchKernelGGL((k_int8<DT, BM, BN, WM, 4 / WM, NS>), dim3((unsigned)(p.split || items < most ? items : most)),
+                       dim3(256), 0, s, p);
+  };
+  using std::integral_constant;
+  const integral_constant<int, 1> c1;
+  const integral_constant<int, 2> c2;
+  const integral_constant<int, 3> c3;
+  const integral_constant<int, 4> c4;
+  const integral_constant<int, 128> c128;
+  const integral_constant<int, 256> c256;
+  switch (pl.tile) {
+    case 0: run(c256, c256, c2, c2); break;
+    case kNarrow: run(c256, integral_constant<int, 192>{}, c2, c2); break;
+    case 1: run(c128, c128, c2, c2); break;
+    case 2: run(integral_constant<int, 64>{}, c128, c1, c3); break;
+    case 3: run(integral_constant<int, 32>{}, c128, c1, c3); break;
+    default: run(integral_constant<int, 16>{}, c128, c1, c4);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !pl.split) return e;
+  const int64_t n = ((int64_t)p.M * (p.N / 4) + 255) / 256;
+  if (n > 0x7fffffffLL) return hipErrorNotSupported;
+  hipLaunchKernelGGL((k_int8_reduce<DT>), dim3((unsigned)n), dim3(256), 0, s, p,
+                     __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(kTileN[pl.tile]));
+  return hipGetLastError();
+}
+
+// Scratch: 16-bit x's codes and scales (but for a single token), then the
+// split product's partial sums.
+struct Scratch {
+  size_t codes = 0, scales = 0, end = 0;
+};
+Scratch scratch_of(int64_t T, int64_t d_in, bool quantised) {
+  Scratch b;
+  if (quantised || (T == 1 && gemv_fits(T, d_in))) return b;
+  b.scales = round256((size_t)(T * d_in));
+  b.end = b.scales + round256((size_t)T * 4);
+  return b;
+}
+
+template <int DT>
+hipError_t linear_dt(const Int8Call& c, hipStream_t s) {
+  char* ws = static_cast<char*>(c.ws);
+  const Scratch b = scratch_of(c.T, c.d_in, c.sx != nullptr);
+  const bool few = gemv_fits(c.T, c.d_in), quantise = c.sx == nullptr && !(c.T == 1 && few);
+  const void* x = c.x;
+  int64_t ldx = c.ldx;
+  const float* sx = c.sx;
+  if (quantise) {
+    int8_t* codes = reinterpret_cast<int8_t*>(ws + b.codes);
+    float* scales = reinterpret_cast<float*>(ws + b.scales);
+    quant_rows<DT>(static_cast<const uint16_t*>(c.x), c.ldx, c.T, c.d_in, codes, c.d_in, scales, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    x = codes;
+    ldx = c.d_in;
+    sx = scales;
+  }
+  if (few) {
+    const GemvP p{x, ldx, sx, c.wq, c.ldw, c.sw, (int)c.T, (int)c.d_out, (int)c.d_in, c.bias, c.res,
+                  c.ldr, c.act, c.y, c.ldy};
+    if (c.T == 1) return sx ? gemv<DT, 1, false>(p, s) : gemv<DT, 1, true>(p, s);
+    if (c.T == 2) return gemv<DT, 2, false>(p, s);
+    return c.T <= 4 ? gemv<DT, 4, false>(p, s) : gemv<DT, 8, false>(p, s);
+  }
+  Int8P p{};
+  p.p[0] = reinterpret_cast<const uint16_t*>(x);
+  p.ldp = (int)(ldx / 2);
+  p.q[0] = reinterpret_cast<const uint16_t*>(c.wq);
+  p.ldq[0] = (int)(c.ldw / 2);
+  p.M = (int)c.T;
+  p.N = (int)c.d_out;
+  p.K = (int)(c.d_in / 2);
+  p.segs = p.outs = 1;
+  p.act = c.act;
+  p.bias = c.bias;
+  p.res = c.res;
+  p.ldr = (int)c.ldr;
+  p.y[0] = c.y;
+  p.ldy[0] = (int)c.ldy;
+  p.sx = sx;
+  p.sw = c.sw;
+  return matmul<DT>(p, ws + b.end, s);
+}
+
+}  // namespace
+
+hipError_t launch_act_quantize_int8(int dtype, const uint16_t* x, int64_t ldx, int64_t T, int64_t d, int8_t* xq,
+                                    int64_t ldq, float* sx, hipStream_t s) {
+  if (dtype == SA_F16) quant_rows<SA_F16>(x, ldx, T, d, xq, ldq, sx, s);
+  else quant_rows<SA_BF16>(x, ldx, T, d, xq, ldq, sx, s);
+  return hipGetLastError();
+}
+
+size_t weight_quantize_int8_workspace_bytes(int64_t d_in, int64_t d_out) {
+  const int64_t strip = col_strip(d_in);
+  return (size_t)((d_in + strip - 1) / strip * d_out * 2);
+}
+
+hipError_t launch_weight_quantize_int8(int dtype, const uint16_t* wt, int64_t ldw, int64_t d_in, int64_t d_out,
+                                       int8_t* wq, int64_t ldq, float* sw, void* ws, hipStream_t s) {
+  const int64_t strip = col_strip(d_in), strips = (d_in + strip - 1) / strip;
+  const int64_t deep = (d_in + 255) / 256;
+  uint16_t* part = static_cast<uint16_t*>(ws);
+  hipLaunchKernelGGL(k_col_most, dim3((unsigned)((d_out + 511) / 512), (unsigned)strips), dim3(256), 0, s, wt, ldw,
+                     d_in, (int)d_out, strip, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((d_out + 63) / 64), (unsigned)deep);
+  if (dtype == SA_F16)
+    hipLaunchKernelGGL((k_quant_cols<SA_F16>), grid, dim3(256), 0, s, wt, ldw, d_in, (int)d_out, part, (int)strips,
+                       wq, ldq, sw);
+  else
+    hipLaunchKernelGGL((k_quant_cols<SA_BF16>), grid, dim3(256), 0, s, wt, ldw, d_in, (int)d_out, part,
+                       (int)strips, wq, ldq, sw);
+  return hipGetLastError();
+}
+
+size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, bool quantised) {
+  const size_t b = scratch_of(T, d_in, quantised).end;
+  return b + (gemv_fits(T, d_in) ? 0 : part_bytes(int8_plan(T, d_in, d_out), T, d_out, d_in / 2, 1, 1));
+}
+
+hipError_t launch_int8_linear(const Int8Call& c, hipStream_t s) {
+  return c.dtype == SA_F16 ? linear_dt<SA_F16>(c, s) : linear_dt<SA_BF16>(c, s);
+}
+
+}  // namespace sa

@@ -191,6 +191,31 @@ int linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, int* 
 hipError_t launch_linear(const LinearCall& c, hipStream_t s);
 hipError_t launch_linear_backward(const LinearCall& c, hipStream_t s);
 
+// ---- linear layers in 8-bit integers (int8.hip) ----------------------------------
+struct Int8Call {
+  int dtype = 0;  // of y, bias, residual, and of x where it is not quantised
+  int act = 0;
+  int64_t T = 0, d_in = 0, d_out = 0;
+  const void* x = nullptr;  // int8 codes with their scales sx, or 16-bit values and sx NULL
+  int64_t ldx = 0;
+  const float* sx = nullptr;
+  const int8_t* wq = nullptr;
+  int64_t ldw = 0;
+  const float* sw = nullptr;
+  const uint16_t *bias = nullptr, *res = nullptr;
+  int64_t ldr = 0;
+  uint16_t* y = nullptr;
+  int64_t ldy = 0;
+  void* ws = nullptr;
+};
+hipError_t launch_act_quantize_int8(int dtype, const uint16_t* x, int64_t ldx, int64_t T, int64_t d, int8_t* xq,
+                                    int64_t ldq, float* sx, hipStream_t s);
+size_t weight_quantize_int8_workspace_bytes(int64_t d_in, int64_t d_out);
+hipError_t launch_weight_quantize_int8(int dtype, const uint16_t* wt, int64_t ldw, int64_t d_in, int64_t d_out,
+                                       int8_t* wq, int64_t ldq, float* sw, void* ws, hipStream_t s);
+size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, bool quantised);
+hipError_t launch_int8_linear(const Int8Call& c, hipStream_t s);
+
 // ---- linear layers grouped by expert (grouped.hip, grouped_backward.hip) -------
 // Matrices per expert lie sw (weights) or sdw (their gradients) elements
 // apart; bias and dbias are [experts][d_out].

@@ -1152,7 +1152,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       const uint32_t po = hp ? (uint32_t)(row * p.ldpre[0] * 2) : 0;
       const int pstep = hp ? 16 * p.ldpre[0] * 2 : 0;
       u32x4 rv[2][NO / 2], bv[NO / 2];  // the residual's rows, one row of blocks ahead
-      if constexpr (general) {
+      if constexpr (mode == kGeneral) {
 #pragma unroll
         for (int b = 0; b < NO / 2; ++b) bv[b] = __builtin_amdgcn_raw_buffer_load_b128(br, col[b], 0, 0);
       }
@@ -1223,12 +1223,13 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint32_t x = v[e];
-                f.v[4 * h + e] = (float)__builtin_bit_cast(int, f.v[4 * h + e]) * rsv[a] * __builtin_bit_cast(float, x);
+                f.v[4 * h + e] = (float)__builtin_bit_cast(int, f.v[4 * h + e]) * __builtin_bit_cast(float, x) * rsv[a];
               }
             }
           }
           if constexpr (general) {
-            const F8 bias = widen8<DT>(bv[b / 2]);
+            // 8-bit integers: read again per row (registers are short; L1 holds it)
+            const F8 bias = widen8<DT>(I8 ? __builtin_amdgcn_raw_buffer_load_b128(br, col[b / 2], 0, 0) : bv[b / 2]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
             if constexpr (mode == kGeneral)
@@ -1564,6 +1565,107 @@ constexpr int64_t kCus = 256;  // compute units of an MI355X
 inline int64_t strip_rows(int64_t T) { return T < 2048 ? 16 : T <= 64 * 1024 ? 64 : (T + 1023) / 1024; }
 inline size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// ---- plans -----------------------------------------------------------------------
+
+// The compiled tiles: rows and columns (of g and of u each: 128 at most),
+// and LDS stages.
+constexpr int kTiles = 6;
+constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16, 256}, kTileN[kTiles] = {256, 128, 128, 128, 128, 192};
+constexpr int kNarrow = 5;  // 256 x 192: whole tiles of plain products only, for another tile count
+
+struct Plan {
+  int tile, split;  // split: shares, 0 for whole tiles
+  int64_t tiles;
+};
+
+inline int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
+  const int64_t bn = gated ? 128 : kTileN[tile];
+  return ((M + kTileM[tile] - 1) / kTileM[tile]) * ((N + bn - 1) / bn) * outs;
+}
+
+// Largest number of shares that hold part of one tile.
+inline int64_t slots_of(const Plan& pl, int64_t steps) {
+  int64_t most = 0;
+  for (int64_t t = 0; t < pl.tiles; ++t) {
+    const uint32_t at = (uint32_t)(t * steps), TS = (uint32_t)(pl.tiles * steps);
+    const int64_t n = share_of(at + (uint32_t)steps - 1, TS, pl.split) - share_of(at, TS, pl.split) + 1;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+// The tile and split with the smallest estimated time.  Per tile: a step's
+// time with one workgroup on a CU (latency) and each workgroup's part of it
+// with two (throughput; gated small tiles run alone), in us, measured over
+// sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
+// 3 us for the reduction's launch (7 with 256 x 256 tiles) and the partials'
+// bytes at 4 TB/s; one row tile streams its weights at 26 GB/s per CU at most
+// (gated: up to four share them at 40).  Over 180 random shapes (plain, gated,
+// dx) the choice took 4 percent longer than the best of a sweep on average,
+// but 7 to 13 at 33 to 64 rows and 14 for gated products of 17 to 32, where a
+// second row tile of half the height can pay for reading the weights again
+// (46 rows, gated 760 x 6584: 19.4 us against 12.7, the largest miss).
+inline Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
+                                          {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
+  static const double paired[kTiles] = {0, 0.50, 0.36, 0.25, 0.22, 0};
+  const int64_t steps = ((K + BK - 1) / BK) * segs;
+  int tuned_tile, tuned_split;
+  linear_tuning(&tuned_tile, &tuned_split);
+  Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
+  double least = 1e30;
+  for (int t = 0; t < kTiles; ++t) {
+    if (lay == kDw && t > 1 && t != kNarrow) continue;
+    if (t == kNarrow && gated) continue;
+    const bool forced = tuned_tile >= 0 && !(lay == kDw && tuned_tile > 1 && tuned_tile != kNarrow) &&
+                        !(tuned_tile == kNarrow && gated);
+    if (forced && t != tuned_tile) continue;
+    // up to 64 rows in one row tile, more in tiles of 64 at least (see the
+    // misses above)
+    if (tuned_tile < 0 && kTileM[t] < (M < 64 ? M : 64)) continue;
+    const int64_t tiles = tiles_of(t, gated, M, N, outs);
+    const bool pairs = t > 0 && t != kNarrow && !gated;
+    double step = alone[gated][t];
+    if (t > 0 && M <= (gated ? 4 : 1) * kTileM[t]) {
+      const double stream = (gated ? 32768 : kTileN[t] * 128) / (M <= kTileM[t] ? 26e3 : 40e3) + 0.1 * step;
+      step = stream > step ? stream : step;
+    }
+    // whole tiles
+    const int64_t per = pairs ? 2 * kCus : kCus, full = tiles / per, rest = tiles % per;
+    const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
+    double whole = full * (steps * (pairs ? both : step) + 4);
+    if (rest) whole += steps * (rest > kCus ? both : step) + 4;
+    if ((tuned_split <= 0 || t == kNarrow) && whole < least) {
+      least = whole;
+      best = Plan{t, 0, tiles};
+    }
+    // split over one workgroup per CU, of four steps each at least (33 rows of
+    // 4096 x 1024 10.1 us, two steps 10.9), down to two for 128 shares (8
+    // rows of 880 x 3704, dx: 9.0, four 10.5) and one for 64
+    const int64_t TS = tiles * steps;
+    int64_t shares = TS / 4 < kCus ? TS / 4 : kCus;
+    if (shares < 128) shares = TS / 2 < 128 ? TS / 2 : 128;
+    if (shares < 64) shares = TS < 64 ? TS : 64;
+    if (tuned_split > 0) shares = tuned_split < tiles * steps ? tuned_split : tiles * steps;
+    if (tuned_split == 0 || t == kNarrow || shares < 1 || tiles * steps >= (1 << 22)) continue;
+    while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
+    if (tuned_split < 0 && (tiles >= shares || steps < 2)) continue;
+    const double rows = M < kTileM[t] ? M : kTileM[t];
+    const double parts = (shares + tiles) * rows * (gated ? 256 : kTileN[t]) * 8.0 / 4e6;
+    const double time = (double)tiles * steps / shares * step + (t == 0 ? 11 : 7) + parts;
+    if (time < least) {
+      least = time;
+      best = Plan{t, (int)shares, tiles};
+    }
+  }
+  return best;
+}
+
+inline size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int64_t K, int segs, int outs) {
+  if (!pl.split || pl.tiles == 0) return 0;
+  return (size_t)(slots_of(pl, (K + BK - 1) / BK * segs) * M * N * outs * 4);
+}
+
 }  // namespace
 }  // namespace sa
 
@@ -1703,105 +1805,8 @@ __global__ __launch_bounds__(256) void k_lin_colsum(const float* sums, int64_t s
   sum_columns<DT>(sums, 0, strips, N, (int64_t)blockIdx.x * 64, out, part);
 }
 
-// ---- plans -----------------------------------------------------------------------
-
-// The compiled tiles: rows and columns (of g and of u each: 128 at most),
-// and LDS stages.
-constexpr int kTiles = 6;
-constexpr int kTileM[kTiles] = {256, 128, 64, 32, 16, 256}, kTileN[kTiles] = {256, 128, 128, 128, 128, 192};
-constexpr int kNarrow = 5;  // 256 x 192: whole tiles of plain products only, for another tile count
+// ---- launches ----------------------------------------------------------------------
 int g_lin_tile = -1, g_lin_split = -1;  // overrides (linear_set_tuning)
-
-struct Plan {
-  int tile, split;  // split: shares, 0 for whole tiles
-  int64_t tiles;
-};
-
-int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
-  const int64_t bn = gated ? 128 : kTileN[tile];
-  return ((M + kTileM[tile] - 1) / kTileM[tile]) * ((N + bn - 1) / bn) * outs;
-}
-
-// Largest number of shares that hold part of one tile.
-int64_t slots_of(const Plan& pl, int64_t steps) {
-  int64_t most = 0;
-  for (int64_t t = 0; t < pl.tiles; ++t) {
-    const uint32_t at = (uint32_t)(t * steps), TS = (uint32_t)(pl.tiles * steps);
-    const int64_t n = share_of(at + (uint32_t)steps - 1, TS, pl.split) - share_of(at, TS, pl.split) + 1;
-    most = n > most ? n : most;
-  }
-  return most;
-}
-
-// The tile and split with the smallest estimated time.  Per tile: a step's
-// time with one workgroup on a CU (latency) and each workgroup's part of it
-// with two (throughput; gated small tiles run alone), in us, measured over
-// sweeps of tiles and splits at 1 to 1000 rows; 4 us per round of workgroups;
-// 3 us for the reduction's launch (7 with 256 x 256 tiles) and the partials'
-// bytes at 4 TB/s; one row tile streams its weights at 26 GB/s per CU at most
-// (gated: up to four share them at 40).  Over 180 random shapes (plain, gated,
-// dx) the choice took 4 percent longer than the best of a sweep on average,
-// but 7 to 13 at 33 to 64 rows and 14 for gated products of 17 to 32, where a
-// second row tile of half the height can pay for reading the weights again
-// (46 rows, gated 760 x 6584: 19.4 us against 12.7, the largest miss).
-Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  static const double alone[2][kTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38, 1.15},
-                                          {1.45, 0.95, 0.60, 0.55, 0.50, 0}};
-  static const double paired[kTiles] = {0, 0.50, 0.36, 0.25, 0.22, 0};
-  const int64_t steps = ((K + BK - 1) / BK) * segs;
-  Plan best{0, 0, tiles_of(0, gated, M, N, outs)};
-  double least = 1e30;
-  for (int t = 0; t < kTiles; ++t) {
-    if (lay == kDw && t > 1 && t != kNarrow) continue;
-    if (t == kNarrow && gated) continue;
-    const bool forced = g_lin_tile >= 0 && !(lay == kDw && g_lin_tile > 1 && g_lin_tile != kNarrow) &&
-                        !(g_lin_tile == kNarrow && gated);
-    if (forced && t != g_lin_tile) continue;
-    // up to 64 rows in one row tile, more in tiles of 64 at least (see the
-    // misses above)
-    if (g_lin_tile < 0 && kTileM[t] < (M < 64 ? M : 64)) continue;
-    const int64_t tiles = tiles_of(t, gated, M, N, outs);
-    const bool pairs = t > 0 && t != kNarrow && !gated;
-    double step = alone[gated][t];
-    if (t > 0 && M <= (gated ? 4 : 1) * kTileM[t]) {
-      const double stream = (gated ? 32768 : kTileN[t] * 128) / (M <= kTileM[t] ? 26e3 : 40e3) + 0.1 * step;
-      step = stream > step ? stream : step;
-    }
-    // whole tiles
-    const int64_t per = pairs ? 2 * kCus : kCus, full = tiles / per, rest = tiles % per;
-    const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
-    double whole = full * (steps * (pairs ? both : step) + 4);
-    if (rest) whole += steps * (rest > kCus ? both : step) + 4;
-    if ((g_lin_split <= 0 || t == kNarrow) && whole < least) {
-      least = whole;
-      best = Plan{t, 0, tiles};
-    }
-    // split over one workgroup per CU, of four steps each at least (33 rows of
-    // 4096 x 1024 10.1 us, two steps 10.9), down to two for 128 shares (8
-    // rows of 880 x 3704, dx: 9.0, four 10.5) and one for 64
-    const int64_t TS = tiles * steps;
-    int64_t shares = TS / 4 < kCus ? TS / 4 : kCus;
-    if (shares < 128) shares = TS / 2 < 128 ? TS / 2 : 128;
-    if (shares < 64) shares = TS < 64 ? TS : 64;
-    if (g_lin_split > 0) shares = g_lin_split < tiles * steps ? g_lin_split : tiles * steps;
-    if (g_lin_split == 0 || t == kNarrow || shares < 1 || tiles * steps >= (1 << 22)) continue;
-    while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
-    if (g_lin_split < 0 && (tiles >= shares || steps < 2)) continue;
-    const double rows = M < kTileM[t] ? M : kTileM[t];
-    const double parts = (shares + tiles) * rows * (gated ? 256 : kTileN[t]) * 8.0 / 4e6;
-    const double time = (double)tiles * steps / shares * step + (t == 0 ? 11 : 7) + parts;
-    if (time < least) {
-      least = time;
-      best = Plan{t, (int)shares, tiles};
-    }
-  }
-  return best;
-}
-
-size_t part_bytes(const Plan& pl, int64_t M, int64_t N, int64_t K, int segs, int outs) {
-  if (!pl.split || pl.tiles == 0) return 0;
-  return (size_t)(slots_of(pl, (K + BK - 1) / BK * segs) * M * N * outs * 4);
-}
 
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const LinP& p, int64_t items, hipStream_t s) {  // items: shares or tiles

@@ -363,6 +363,32 @@ int check_linear_both(const char* fn, const char* a, const void* pa, const char*
   return SA_OK;
 }
 
+int check_int8_sizes(const char* fn, int dtype, int64_t T, int64_t d_in, int64_t d_out, int act) {
+  const int st = check_linear_sizes(fn, dtype, T, d_in, d_out, act);
+  if (st != SA_OK) return st;
+  REQUIRE(d_in % 16 == 0, SA_ERR_INVALID_ARG, "%s: d_in must be a positive multiple of 16", fn);
+  REQUIRE(d_in <= kMaxInt8Dim, SA_ERR_UNSUPPORTED, "%s: d_in must be at most %lld", fn, (long long)kMaxInt8Dim);
+  return SA_OK;
+}
+
+int check_int8_codes(const char* fn, const char* name, const void* p, int64_t ld, int64_t len, bool optional) {
+  if (optional && p == nullptr) return SA_OK;
+  REQUIRE(p != nullptr, SA_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  REQUIRE(aligned(p, 16), SA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  REQUIRE(ld >= len && ld % 16 == 0, SA_ERR_INVALID_ARG,
+          "%s: the row stride of %s must be a multiple of 16 and at least %lld (got %lld)", fn, name,
+          (long long)len, (long long)ld);
+  REQUIRE(ld <= kMaxLinDim, SA_ERR_UNSUPPORTED, "%s: the row stride of %s must be at most %lld", fn, name,
+          (long long)kMaxLinDim);
+  return SA_OK;
+}
+
+int check_scales(const char* fn, const char* name, const void* p, bool optional) {
+  REQUIRE(optional || p != nullptr, SA_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+  REQUIRE(aligned(p, 16), SA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  return SA_OK;
+}
+
 int check_grouped(const char* fn, int64_t experts, const void* offsets) {
   REQUIRE(experts >= 1, SA_ERR_INVALID_ARG, "%s: experts must be >= 1 (got %lld)", fn, (long long)experts);
   REQUIRE(experts <= SA_MAX_EXPERTS, SA_ERR_UNSUPPORTED, "%s: experts must be at most %d", fn, SA_MAX_EXPERTS);
