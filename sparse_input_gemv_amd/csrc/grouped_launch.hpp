@@ -30,14 +30,14 @@ __global__ __launch_bounds__(256, 1) void k_grp(GroupP p) {
 }
 
 // Sums the partials of the tile that share blockIdx.x begins and does not end
-// (if any) and finishes rows 16 blockIdx.y .. + 15, 8 columns per thread.
-template <int DT, bool GATED>
+// (if any) and finishes 2048 of its outputs, 8 columns of a row per thread.
+template <int DT, bool GATED, int BN>
 __global__ __launch_bounds__(256) void k_grp_reduce(GroupP p, int lbm) {
+  constexpr int OCT = (GATED ? BN / 2 : BN) / 8, ROWS = 256 / OCT;
   const CutTile c = p.cut[blockIdx.x];
-  const int row = (int)blockIdx.y * 16 + (int)threadIdx.x / 16, col = (int)threadIdx.x % 16 * 8;
+  const int row = (int)blockIdx.y * ROWS + (int)threadIdx.x / OCT, col = (int)threadIdx.x % OCT * 8;
   const int n = c.n0 + col;
   if (c.shares == 0 || row >= c.rows || n >= p.N) return;
-  constexpr int BN = GATED ? 256 : 128;
   const float* const at = p.part + row * BN + col;
   const int64_t tile = (int64_t)BN << lbm;
   F8 f[kChains] = {}, u[kChains] = {};
@@ -99,14 +99,24 @@ inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, in
     const int64_t cus = pairs ? 2 * kCus : kCus;
     const double rounds = tiles <= cus ? 1 : (int64_t)(tiles / cus) + 1;
     const double whole = rounds * (steps * (tiles > kCus ? both : step) + 4);
-    if ((tuned_split <= 0) && whole < least) {
-      least = whole;
-      best = GrpPlan{t, 0, most};
-    }
     // even shares, one workgroup per CU; positions times shares fit 31 bits
     int64_t shares = tuned_split > 0 ? tuned_split : kCus;
     while (shares & (shares - 1)) shares &= shares - 1;
-    if (t == 0 || tuned_split == 0 || most * steps * shares >= 0x7fffffffLL) continue;
+    if (t == 0) {  // the last round alone is shared, where the device finds that it pays
+      if (shares > kCus) shares = kCus;
+      const bool rest = tuned_split != 0 && kCus * steps * shares < 0x7fffffffLL && most < 0x3fffffffLL;
+      if (whole < least) {
+        least = whole;
+        best = GrpPlan{t, rest ? (int)shares : 0, most};
+      }
+      continue;
+    }
+    if (tuned_split <= 0 && whole < least) {
+      least = whole;
+      best = GrpPlan{t, 0, most};
+    }
+    if (tuned_split == 0 || most * steps * shares >= 0x7fffffffLL) continue;
+    if (tuned_split < 0 && t < 2 && tiles >= shares) continue;
     const double parts = shares * 2.0 * (mean < kGrpM[t] ? mean : kGrpM[t]) * (gated ? 256 : 128) * 8 / 4e6;
     const double time = tiles * steps / shares * step + 8 + parts;
     if (time < least) {
@@ -120,7 +130,7 @@ inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, in
 
 inline size_t grp_part_bytes(const GrpPlan& pl, bool gated) {
   if (!pl.split) return 0;
-  return round256(pl.split * sizeof(CutTile)) + (size_t)pl.split * 2 * kGrpM[pl.tile] * (gated ? 256 : 128) * 4;
+  return round256(pl.split * sizeof(CutTile)) + (size_t)pl.split * 2 * kGrpM[pl.tile] * (gated ? 256 : kGrpN[pl.tile]) * 4;
 }
 
 template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, int NS>
@@ -159,9 +169,11 @@ hipError_t launch_grp(GroupP p, void* ws, hipStream_t s) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !pl.split) return e;
-  const int rows = kGrpM[pl.tile] < p.T ? kGrpM[pl.tile] : p.T;
-  hipLaunchKernelGGL((k_grp_reduce<DT, GATED>), dim3(pl.split, (rows + 15) / 16), dim3(256), 0, s, p,
-                     __builtin_ctz(kGrpM[pl.tile]));
+  const int rows = kGrpM[pl.tile] < p.T ? kGrpM[pl.tile] : p.T, lbm = __builtin_ctz(kGrpM[pl.tile]);
+  if (!GATED && pl.tile == 0)
+    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, 256>), dim3(pl.split, (rows + 7) / 8), dim3(256), 0, s, p, lbm);
+  else
+    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, SB>), dim3(pl.split, (rows + 15) / 16), dim3(256), 0, s, p, lbm);
   return hipGetLastError();
 }
 

@@ -686,38 +686,72 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   const int steps = ks * p.segs;
   // A cursor goes over the workgroup's items: a tile's number, or (split) a
   // position among all tiles' steps, up to `end`.
-  // By expert, tiles of 256 rows and weight gradients are never split.
-  const bool split = !(GRP && (LAY == kDw || BM == 256)) && p.split > 0;
+  // By expert, weight gradients are never split, and of tiles of 256 rows only
+  // the last round is: whole tiles come first (`full` of them), then an even
+  // share of the steps of the rest, where that saves more than the partial
+  // sums cost.  Per step of a full round 1.45 us; a partial sum 0.1 us (256 KB
+  // written and read), the reduction's launch 4 us.
+  const bool split = !(GRP && LAY == kDw) && p.split > 0;
+  constexpr bool kRest = GRP && LAY != kDw && BM == 256;
   int lg = split ? __builtin_ctz(p.split) : 0;
+  int full = 0;
   if constexpr (GRP) {
     if (split) {
-      // the device alone knows the steps: shares of at least two, fewer of them if need be
-      const int most = 30 - __builtin_clz(tiles * steps | 3);
-      lg = most < lg ? most : lg;
-      if (block >= 1 << lg) {
-        if (threadIdx.x == 0) p.cut[block].shares = 0;
-        return;
+      if constexpr (kRest) {
+        const int rest = tiles & (p.split - 1);
+        full = tiles - rest;
+        if ((p.split - rest) * (float)steps * 1.45f < p.split * ((p.split + rest) * 0.1f + 4.f)) full = tiles;
       }
+      // the device alone knows the steps: shares of at least two, fewer of them if need be
+      const int most = 30 - __builtin_clz((tiles - full) * steps | 3);
+      lg = most < lg ? most : lg;
+      if (threadIdx.x == 0) p.cut[block].shares = 0;  // until finish_cut, by this thread
+      if (full == 0 && block >= 1 << lg) return;
     }
   }
   // Row tiles that read the same weights are kept on one XCD; with a single
   // one nothing is shared, and neighbouring shares on different XCDs stream
   // faster (one row of 4096 x 4096: 11.4 -> 11.1 us).
   const int share = !split ? 0 : GRP || mt == 1 ? block : (int)xcd_run(block, blocks);
-  const int begin = split ? (int)((uint32_t)share * (uint32_t)(tiles * steps) >> lg) : block;
-  const int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)(tiles * steps) >> lg) : tiles;
+  const int TS = (tiles - full) * steps;  // the split tiles' steps
+  int begin = split ? (int)((uint32_t)share * (uint32_t)TS >> lg) : block;
+  int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)TS >> lg) : tiles;
+  int after = 0;  // where the share follows the whole tiles: below `full` the cursor counts those
+  if constexpr (kRest) {
+    if (split) {
+      if (share >= 1 << lg) begin = end = 0;
+      after = full + begin;
+      end += full;
+      begin = block < full ? block : after;
+    }
+  }
   struct Item {
     int m0, n0, out, s0, s1, next;
     int e, mt, mend, k0, k;  // by expert: its number; row tiles and last row's end, or first row and rows
   };
   if constexpr (GRP) {
-    if (split && threadIdx.x == 0) p.cut[share].shares = 0;  // until finish_cut, by this thread
     if (begin >= end) return;  // fewer tiles (or steps) than workgroups
   }
+  // By expert and for 8-bit integers the rarely used arguments (p is the
+  // kernel's first) are read again where they are used: kept over the K loop,
+  // they would spill its scalar registers (into vector registers, with moves
+  // between products).
+  auto arguments = [&]() SA_INLINE -> const P& {
+    if constexpr (GRP || I8) {
+      auto k = __builtin_amdgcn_kernarg_segment_ptr();
+      asm volatile("" : "+s"(k));
+      return *(const P*)k;
+    } else {
+      return p;
+    }
+  };
   auto item_at = [&](int cur) SA_INLINE {
     Item it;
     int mi, ni;
     if constexpr (GRP) {
+      const P& p = arguments();
+      const int mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO, nt = nt1 * p.outs;
+      const int steps = (p.K + BK - 1) / BK * p.segs;
       int t, in, mte;
       it.s0 = 0;
       it.s1 = steps;
@@ -733,7 +767,9 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         it.s1 = (it.k + BK - 1) / BK;
         it.mend = p.M;
       } else {
-        t = split ? uni((int)((uint32_t)cur / (uint32_t)steps)) : (int)xcd_run(cur, tiles);
+        const bool part = split && cur >= full;
+        t = part ? full + uni((int)((uint32_t)(cur - full) / (uint32_t)steps))
+                 : (int)xcd_run(cur, split ? full : tiles);
         it.e = group_of(*tab, p.E, uni((int)((uint32_t)t / (uint32_t)nt)));
         const int first = uni(tab->first[it.e]);
         mte = uni(tab->first[it.e + 1]) - first;
@@ -741,14 +777,16 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         it.mend = uni(tab->row[it.e + 1]);
         it.k0 = 0;
         it.k = p.K;
-        if (split) {
-          it.s0 = cur - t * steps;
+        if (part) {
+          it.s0 = cur - full - (t - full) * steps;
           it.s1 = uni(it.s0 + end - cur < steps ? it.s0 + end - cur : steps);
           it.next = cur + it.s1 - it.s0;
+        } else if (kRest && split && it.next >= full) {
+          it.next = after;
         }
       }
       it.mt = mte;
-      if (LAY != kDw && split) {  // row tiles that read the same weights follow each other
+      if (LAY != kDw && !kRest && split) {  // row tiles that read the same weights follow each other
         ni = uni((int)((uint32_t)in / (uint32_t)mte));
         mi = in - ni * mte;
       } else {
@@ -789,8 +827,10 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   op.init(w, p.ldp);
   oq.init(w, qh ? p.ldq[1] : p.ldq[0]);
   const uint16_t *p0 = p.p[0], *p1 = p.p[1];
+  bool scaled = false;
   if constexpr (EPI == kScaled && LAY == kDx) {
-    if (p.scaled && uni((int)*p.scaled)) {
+    scaled = p.scaled && uni((int)*p.scaled);
+    if (scaled) {
       p0 = p.alt[0];
       p1 = p.alt[1];
     }
@@ -804,6 +844,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   // 4096 x 4096: 13.4 -> 11.4 us, gate and up 4096 x 11008: 40.4 -> 37.1).
   bool once = BM <= 64 && LAY != kDw && mt == 1;
   auto place = [&]() SA_INLINE {  // at step `at` of item li
+    const P& p = arguments();
     const bool dw = GRP && LAY == kDw;
     const int seg = !dw && at >= ks;
     const int k0 = (at - seg * ks) * BK;
@@ -813,11 +854,13 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
     const bool second = GATED ? qh : LAY == kDx ? seg : LAY == kDw ? li.out : 0;
     if constexpr (GRP) {
       if (dw) {
-        op.start(p0, li.m0, p.M, li.k0 + k0, w);
+        op.start(p.p[0], li.m0, p.M, li.k0 + k0, w);
         oq.start(second ? p.q[1] : p.q[0], li.n0, p.N, li.k0 + k0, w);
       } else {
         once = BM <= 64 && li.mt == 1;
-        op.start(LAY == kDx && seg ? p1 : p0, li.m0, li.mend, k0, w);
+        const bool alt = EPI == kScaled && LAY == kDx && scaled;
+        const uint16_t* rows = seg ? (alt ? p.alt[1] : p.p[1]) : alt ? p.alt[0] : p.p[0];
+        op.start(rows, li.m0, li.mend, k0, w);
         oq.start((second ? p.q[1] : p.q[0]) + li.e * (second ? p.sq[1] : p.sq[0]),
                  GATED ? li.n0 - 128 * qh : li.n0, p.N, k0, w);
       }
@@ -1039,6 +1082,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   // earlier share began it, and of its last, where it does not end it; a tile
   // of BM x BN each.
   auto finish_cut = [&](const Item& it) SA_INLINE {
+    const P& p = arguments();
     float* const part = p.part + (int64_t)(share * 2 + (it.s0 == 0)) * BM * BN;
     static_for<MB>([&](auto A) {
       constexpr int a = decltype(A)::value;
@@ -1053,9 +1097,9 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
     });
     if constexpr (GRP) {
       if (it.s0 == 0 && threadIdx.x == 0) {
-        const int cur = end - it.s1;  // a tile that is not ended ends its share
+        const int cur = end - full - it.s1;  // a tile that is not ended ends its share
         const int rows = it.mend - it.m0 < BM ? it.mend - it.m0 : BM;
-        p.cut[share] = CutTile{share_of(cur + steps - 1, tiles * steps, 1 << lg) - share + 1, it.m0, rows,
+        p.cut[share] = CutTile{share_of(cur + steps - 1, TS, 1 << lg) - share + 1, it.m0, rows,
                                it.n0, it.e, {}};
       }
     }
@@ -1097,8 +1141,32 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       if (p.tickets) join(it, t);
     }
   };
+  // The columns' scales (8-bit integers) and biases of a tile, in LDS: there
+  // are no registers for them.  Every thread writes an entry, as a branch here
+  // makes the compiler move sums out of the accumulation registers.
+  constexpr bool kCols = I8 || (GRP && EPI == kGeneral && !GATED);
+  __shared__ __align__(16) float col_scale[kCols ? 256 : 4], col_bias[kCols ? 256 : 4];
+  // The activation is chosen once for kAct block pairs.  One pair at a time, as
+  // in the dense layers, a tile's 32 choices of six forms pass the instruction
+  // cache's size; per tile, the sums are read in six places, for which the
+  // compiler moves some out of the accumulation registers in the K loop.
+  constexpr int kAct = GRP || I8 ? 2 : 1;
+  constexpr int kActs = NO / 2 % kAct ? 1 : kAct;
   auto finish_rows = [&](const Item& it) SA_INLINE {
+    const P& p = arguments();
     constexpr int mode = EPI;
+    auto activate = [&](F8 (&f)[kActs]) SA_INLINE {
+      if constexpr (kActs == 1) {
+        act8(p.act, f[0]);
+      } else {
+        with_act(p.act, [&](auto A) SA_INLINE {
+#pragma unroll
+          for (int j = 0; j < kActs; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[j].v[e] = act_value<decltype(A)::value>(f[j].v[e]);
+        });
+      }
+    };
     const int mend = GRP ? it.mend : p.M;
     const int rows = mend - it.m0 < BM ? mend - it.m0 : BM;
     const int ldy = it.out ? p.ldy[1] : p.ldy[0];
@@ -1122,19 +1190,28 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         constexpr int a = decltype(A)::value;
         take_row(a);
 #pragma unroll
-        for (int b = 0; b < NO; b += 2) {
-          F8 f = pair8(acc[a][b], acc[a][b + 1]);
-          const F8 u = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
-          if constexpr (mode == kGeneral) {
-            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), gr,
-                (uint32_t)((row + 16 * a) * p.ldpre[0] * 2) + col[b / 2], 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(u), ur,
-                (uint32_t)((row + 16 * a) * p.ldpre[1] * 2) + col[b / 2], 0, 0);
-          }
-          act8(p.act, f);
+        for (int b0 = 0; b0 < NO; b0 += 2 * kActs) {
+          F8 f[kActs], u[kActs];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f.v[e] *= u.v[e];
-          __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
+          for (int j = 0; j < kActs; ++j) {
+            const int b = b0 + 2 * j;
+            f[j] = pair8(acc[a][b], acc[a][b + 1]);
+            u[j] = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
+            if constexpr (mode == kGeneral) {
+              __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f[j]), gr,
+                  (uint32_t)((row + 16 * a) * p.ldpre[0] * 2) + col[b / 2], 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(u[j]), ur,
+                  (uint32_t)((row + 16 * a) * p.ldpre[1] * 2) + col[b / 2], 0, 0);
+            }
+          }
+          activate(f);
+#pragma unroll
+          for (int j = 0; j < kActs; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[j].v[e] *= u[j].v[e];
+            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f[j]), yr,
+                                                   yo + (uint32_t)(a * ystep) + col[b0 / 2 + j], 0, 0);
+          }
         }
       });
     } else {
@@ -1152,10 +1229,28 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       const uint32_t po = hp ? (uint32_t)(row * p.ldpre[0] * 2) : 0;
       const int pstep = hp ? 16 * p.ldpre[0] * 2 : 0;
       u32x4 rv[2][NO / 2], bv[NO / 2];  // the residual's rows, one row of blocks ahead
-      if constexpr (mode == kGeneral) {
+      if constexpr (mode == kGeneral && !kCols) {
 #pragma unroll
         for (int b = 0; b < NO / 2; ++b) bv[b] = __builtin_amdgcn_raw_buffer_load_b128(br, col[b], 0, 0);
       }
+      if constexpr (kCols) {
+        // a wave comes here again only after barriers that every wave passes
+        // when it has read these
+        const uint32_t n = it.n0 + threadIdx.x;
+        col_bias[threadIdx.x] = to_f<DT>((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(br, n * 2, 0, 0));
+        if constexpr (I8) {
+          const auto sw = __builtin_amdgcn_make_buffer_rsrc((void*)uni(p.sw), 0, uni(p.N * 4), 0x00020000);
+          col_scale[threadIdx.x] =
+              __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sw, n * 4, 0, 0));
+        }
+        stage_barrier<63, 0>();
+      }
+      auto columns = [&](const float* v, int b) SA_INLINE {  // the lane's 8 of block pair b
+        const f4v* q = reinterpret_cast<const f4v*>(v + (wn * NO + b + (g & 1)) * 16 + 8 * (g >> 1));
+        f4v lo = q[0], hi = q[1];
+        asm("" : "+v"(lo), "+v"(hi));
+        return F8{{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
+      };
       // a row's or a column's scale: a lane's rows or columns of the tile
       float rsv[MB];
       F8 csv[NO / 2];
@@ -1186,66 +1281,60 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
           }
         }
       }
-      // 8-bit integers: scales of the lane's rows and of 8 columns at a time
-      const void* sw = p.y[0];
       if constexpr (I8) {
-        sw = p.sw;
         const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)uni(p.sx), 0, uni(p.M * 4), 0x00020000);
 #pragma unroll
         for (int a = 0; a < MB; ++a)
           rsv[a] = __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
                        r, (uint32_t)(it.m0 + row + 16 * a) * 4, 0, 0));
       }
-      const auto swr = __builtin_amdgcn_make_buffer_rsrc((void*)uni(sw), 0, uni(p.N * 4), 0x00020000);
-      if constexpr (residual) {
+      auto read_residual = [&](int a, u32x4 (&v)[NO / 2]) SA_INLINE {
 #pragma unroll
         for (int b = 0; b < NO / 2; ++b)
-          rv[0][b] = __builtin_amdgcn_raw_buffer_load_b128(rr, ro + col[b], 0, 0);
-      }
+          v[b] = __builtin_amdgcn_raw_buffer_load_b128(rr, ro + (uint32_t)(a * rstep) + col[b], 0, 0);
+      };
+      if constexpr (residual) read_residual(0, rv[0]);
       static_for<MB>([&](auto A) {
         constexpr int a = decltype(A)::value;
         take_row(a);
-        if constexpr (residual) {
-          if constexpr (a + 1 < MB) {
+        if constexpr (residual && a + 1 < MB) read_residual(a + 1, rv[(a + 1) & 1]);
 #pragma unroll
-            for (int b = 0; b < NO / 2; ++b)
-              rv[(a + 1) & 1][b] =
-                  __builtin_amdgcn_raw_buffer_load_b128(rr, ro + (uint32_t)((a + 1) * rstep) + col[b], 0, 0);
-          }
-        }
+        for (int b0 = 0; b0 < NO; b0 += 2 * kActs) {
+          F8 v[kActs];
 #pragma unroll
-        for (int b = 0; b < NO; b += 2) {
-          F8 f = pair8(acc[a][b], acc[a][b + 1]);
-          if constexpr (I8) {
+          for (int j = 0; j < kActs; ++j) {
+            const int b = b0 + 2 * j;
+            F8& f = v[j];
+            f = pair8(acc[a][b], acc[a][b + 1]);
+            if constexpr (I8) {
+              const F8 sw = columns(col_scale, b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(swr, col[b / 2] * 2 + 16 * h, 0, 0);
+              for (int e = 0; e < 8; ++e) f.v[e] = (float)__builtin_bit_cast(int, f.v[e]) * sw.v[e] * rsv[a];
+            }
+            if constexpr (general) {
+              const F8 bias = kCols ? columns(col_bias, b) : widen8<DT>(bv[b / 2]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t x = v[e];
-                f.v[4 * h + e] = (float)__builtin_bit_cast(int, f.v[4 * h + e]) * __builtin_bit_cast(float, x) * rsv[a];
-              }
+              for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
+              if constexpr (mode == kGeneral)
+                __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
             }
           }
-          if constexpr (general) {
-            // 8-bit integers: read again per row (registers are short; L1 holds it)
-            const F8 bias = widen8<DT>(I8 ? __builtin_amdgcn_raw_buffer_load_b128(br, col[b / 2], 0, 0) : bv[b / 2]);
+          if constexpr (general) activate(v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
-            if constexpr (mode == kGeneral)
-              __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
-            act8(p.act, f);
-          }
-          if constexpr (mode == kScaled) {
+          for (int j = 0; j < kActs; ++j) {
+            const int b = b0 + 2 * j;
+            F8& f = v[j];
+            if constexpr (mode == kScaled) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.v[e] *= LAY == kDx ? rsv[a] : csv[b / 2].v[e];
-          }
-          if constexpr (residual) {
-            const F8 r = widen8<DT>(rv[a & 1][b / 2]);
+              for (int e = 0; e < 8; ++e) f.v[e] *= LAY == kDx ? rsv[a] : csv[b / 2].v[e];
+            }
+            if constexpr (residual) {
+              const F8 r = widen8<DT>(rv[a & 1][b / 2]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.v[e] += r.v[e];
+              for (int e = 0; e < 8; ++e) f.v[e] += r.v[e];
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
           }
-          __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
         }
       });
     }
@@ -1289,7 +1378,8 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   }
   int pbuf = NS - 1, buf = 0;
   for (int cur = begin; cur < end;) {
-    const Item it = item_at(cur);
+    Item it = item_at(cur);
+    int now = cur;
     cur = it.next;
     for (int t = it.s0; t < it.s1; ++t) {
       const int nbuf = buf + 1 == NS ? 0 : buf + 1;
@@ -1297,6 +1387,10 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       half(std::integral_constant<int, 1>{}, pbuf, buf, nbuf);
       pbuf = buf;
       buf = nbuf;
+    }
+    if constexpr (GRP || I8) {  // found again, not kept over the K loop
+      asm volatile("" : "+s"(now));
+      it = item_at(now);
     }
     finish(it);
   }
