@@ -34,7 +34,7 @@ __global__ __launch_bounds__(256) void k_grp_dact(GrpDactP p, int lg) {
   if constexpr (SCALING == kFind) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.scaled = 0;
   }
-  group_table(p.offsets, p.E, (int)p.T, lg, tab);
+  group_table(p.offsets, p.E, (int)p.T, lg, 1, tab);
   const int strip = (int)blockIdx.y;
   if (strip >= tab.first[p.E]) return;
   const int e = group_of(tab, p.E, strip);
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void k_grp_scales(GrpDactP p, int lg, int64_t 
                                                     uint16_t* dbias) {
   __shared__ float part[4][64], most[4][64];
   __shared__ GroupTab tab;
-  group_table(p.offsets, p.E, (int)p.T, lg, tab);
+  group_table(p.offsets, p.E, (int)p.T, lg, 1, tab);
   bool scaled = false;
   const int columns = cblocks * p.E;
   if ((int)blockIdx.x < columns) {
@@ -73,7 +73,7 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_grp_colsum(GrpDactP p, int lg, uint16_t* dbias) {
   __shared__ float part[4][64];
   __shared__ GroupTab tab;
-  group_table(p.offsets, p.E, (int)p.T, lg, tab);
+  group_table(p.offsets, p.E, (int)p.T, lg, 1, tab);
   const int e = (int)blockIdx.y;
   sum_columns<DT>(p.sums, tab.first[e], tab.first[e + 1], p.N, (int64_t)blockIdx.x * 64, dbias + e * p.N, part);
 }

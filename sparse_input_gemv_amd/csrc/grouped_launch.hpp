@@ -25,7 +25,8 @@ template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, 
 __global__ __launch_bounds__(256, 1) void k_grp(GroupP p) {
   __shared__ __align__(16) uint8_t S[lin_lds<LAY, BM, BN, NS>()];
   __shared__ GroupTab tab;
-  group_table(p.offsets, p.E, p.T, table_lg<LAY, BM>(), tab);
+  constexpr int BNO = GATED ? BN / 2 : BN;
+  group_table(p.offsets, p.E, p.T, table_lg<LAY, BM>(), LAY == kDw ? 1 : (p.N + BNO - 1) / BNO, tab);
   lin_run<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S, &tab);
 }
 

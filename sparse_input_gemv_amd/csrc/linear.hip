@@ -305,8 +305,8 @@ struct CutTile {
   int shares, m0, rows, n0, e, pad[3];
 };
 constexpr int kMaxExperts = (int)kMaxGroupedExperts;  // with more, two workgroups of 64 rows would not fit a CU's LDS
-// The experts' row tiles in a row: expert e's are first[e] .. first[e + 1] - 1,
-// its rows row[e] .. row[e + 1] - 1.
+// The experts' tiles in a row: expert e's are first[e] .. first[e + 1] - 1 (its
+// row tiles times `cols`), its rows row[e] .. row[e + 1] - 1.
 struct GroupTab {
   int first[kMaxExperts + 1], row[kMaxExperts + 1];
 };
@@ -439,6 +439,19 @@ __device__ __forceinline__ F8 pair8(const f4v& a, const f4v& b) {
   }
   return f;
 }
+// The same, rounded first: 8 outputs in 4 conversions of pairs and 2 swaps.
+template <int DT>
+__device__ __forceinline__ u32x4 round_pair8(const f4v& a, const f4v& b) {
+  typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
+  typedef float f2v __attribute__((ext_vector_type(2)));
+  auto two = [](float x, float y) SA_INLINE {
+    if constexpr (DT == SA_F16) return (uint32_t)f2h(x) | (uint32_t)f2h(y) << 16;
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{x, y}, bf2v));
+  };
+  const auto s = __builtin_amdgcn_permlane16_swap(two(a[0], a[1]), two(b[0], b[1]), false, false);
+  const auto t = __builtin_amdgcn_permlane16_swap(two(a[2], a[3]), two(b[2], b[3]), false, false);
+  return u32x4{s[0], t[0], s[1], t[1]};
+}
 __device__ __forceinline__ void store_part(float* p, const F8& f) {
   *reinterpret_cast<f4v*>(p) = f4v{f.v[0], f.v[1], f.v[2], f.v[3]};
   *reinterpret_cast<f4v*>(p + 4) = f4v{f.v[4], f.v[5], f.v[6], f.v[7]};
@@ -488,10 +501,10 @@ __device__ __forceinline__ int wave_running_max(int v) {
   const int row = lane_id() >> 4, below = row == 0 ? 0 : row == 1 ? r0 : row == 2 ? r01 : r02;
   return below > v ? below : v;
 }
-// Fills the table for row tiles of 2^lg rows; 256 threads.  Offsets are cut to
+// Fills the table for row tiles of 2^lg rows and `cols` columns of tiles; 256 threads.  Offsets are cut to
 // 0 .. T and raised to the largest before them, so whatever they hold, the
 // experts' rows are T at most, in order, and apart.  Ends with a barrier.
-__device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T, int lg, GroupTab& tab) {
+__device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T, int lg, int cols, GroupTab& tab) {
   for (int i = threadIdx.x; i <= E; i += 256) {
     const int v = offsets[i];
     tab.row[i] = v < 0 ? 0 : v > T ? T : v;
@@ -506,7 +519,7 @@ __device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T
       end = end > row ? end : row;
       int begin = __shfl_up(end, 1);
       begin = lane == 0 ? row : begin;
-      const int n = (end - begin + (1 << lg) - 1) >> lg;
+      const int n = ((end - begin + (1 << lg) - 1) >> lg) * cols;
       const int upto = wave_inclusive_scan(n);
       if (e < E) {
         tab.first[e] = tiles + upto - n;
@@ -522,7 +535,7 @@ __device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T
   }
   __syncthreads();
 }
-// The expert whose row tiles hold tile q (below first[E]): the last one that
+// The expert whose tiles hold tile q (below first[E]): the last one that
 // starts at or before it.  The whole wave calls it.
 __device__ __forceinline__ int group_of(const GroupTab& tab, int E, int q) {
   const int lane = lane_id(), per = (E + kWave - 1) / kWave;
@@ -681,7 +694,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   const int mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO;
   const int nt = nt1 * p.outs;
   int tiles = mt * nt;
-  if constexpr (GRP) tiles = uni((LAY == kDw ? p.E * mt : tab->first[p.E]) * nt);
+  if constexpr (GRP) tiles = LAY == kDw ? p.E * mt * nt : uni(tab->first[p.E]);
   const int ks = (p.K + BK - 1) / BK;  // steps per segment
   const int steps = ks * p.segs;
   // A cursor goes over the workgroup's items: a tile's number, or (split) a
@@ -736,8 +749,9 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   // kernel's first) are read again where they are used: kept over the K loop,
   // they would spill its scalar registers (into vector registers, with moves
   // between products).
+  constexpr bool kAgain = (GRP && LAY != kDw) || I8;
   auto arguments = [&]() SA_INLINE -> const P& {
-    if constexpr (GRP || I8) {
+    if constexpr (kAgain) {
       auto k = __builtin_amdgcn_kernarg_segment_ptr();
       asm volatile("" : "+s"(k));
       return *(const P*)k;
@@ -745,21 +759,24 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       return p;
     }
   };
-  auto item_at = [&](int cur) SA_INLINE {
+  // e: an expert at or before the item's (weight gradients)
+  auto item_at = [&](int cur, int e) SA_INLINE {
     Item it;
     int mi, ni;
     if constexpr (GRP) {
       const P& p = arguments();
       const int mt = (p.M + BM - 1) / BM, nt1 = (p.N + BNO - 1) / BNO, nt = nt1 * p.outs;
       const int steps = (p.K + BK - 1) / BK * p.segs;
-      int t, in, mte;
+      int in, mte;
+      bool part = false;
       it.s0 = 0;
       it.s1 = steps;
       it.next = cur + blocks;
       if constexpr (LAY == kDw) {
         // an XCD takes a run of every expert's tiles: experts differ in rows
         const int per = mt * nt;
-        it.e = uni((int)((uint32_t)cur / (uint32_t)per));
+        it.e = e;
+        while ((it.e + 1) * per <= cur) ++it.e;
         in = (int)xcd_run(cur - it.e * per, per);
         mte = mt;
         it.k0 = uni(tab->row[it.e]);
@@ -767,14 +784,13 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         it.s1 = (it.k + BK - 1) / BK;
         it.mend = p.M;
       } else {
-        const bool part = split && cur >= full;
-        t = part ? full + uni((int)((uint32_t)(cur - full) / (uint32_t)steps))
-                 : (int)xcd_run(cur, split ? full : tiles);
-        it.e = group_of(*tab, p.E, uni((int)((uint32_t)t / (uint32_t)nt)));
-        const int first = uni(tab->first[it.e]);
-        mte = uni(tab->first[it.e + 1]) - first;
-        in = t - first * nt;
+        part = split && cur >= full;
+        const int t = part ? full + uni((int)((uint32_t)(cur - full) / (uint32_t)steps))
+                           : (int)xcd_run(cur, split ? full : tiles);
+        it.e = group_of(*tab, p.E, t);
+        in = t - uni(tab->first[it.e]);
         it.mend = uni(tab->row[it.e + 1]);
+        mte = (it.mend - uni(tab->row[it.e]) + BM - 1) / BM;
         it.k0 = 0;
         it.k = p.K;
         if (part) {
@@ -786,15 +802,19 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         }
       }
       it.mt = mte;
-      if (LAY != kDw && !kRest && split) {  // row tiles that read the same weights follow each other
-        ni = uni((int)((uint32_t)in / (uint32_t)mte));
-        mi = in - ni * mte;
-      } else {
-        const int gsz = kGroupM * nt, grp = uni((int)((uint32_t)in / (uint32_t)gsz)), first = grp * kGroupM;
-        const int gm = mte - first < kGroupM ? mte - first : kGroupM;
-        ni = uni((int)((uint32_t)(in - grp * gsz) / (uint32_t)gm));
-        mi = first + in - grp * gsz - ni * gm;
+      // Down the row tiles of a group (kGroupM, or in shares all of them), then
+      // on by a column.
+      const int down = LAY != kDw && !kRest && split ? mte : kGroupM;
+      int first = 0;
+      if (mte > down) {
+        const int gsz = down * nt;
+        first = uni((int)((uint32_t)in / (uint32_t)gsz));
+        in -= first * gsz;
+        first *= down;
       }
+      const int gm = mte - first < down ? mte - first : down;
+      ni = gm == 1 ? in : gm == 4 ? in >> 2 : gm == 2 ? in >> 1 : uni((int)((uint32_t)in / (uint32_t)gm));
+      mi = first + in - ni * gm;
       it.out = ni >= nt1;
       it.m0 = (LAY == kDw ? 0 : uni(tab->row[it.e])) + mi * BM;
       it.n0 = (ni - (it.out ? nt1 : 0)) * BNO;
@@ -835,7 +855,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       p1 = p.alt[1];
     }
   }
-  Item li = item_at(begin);
+  Item li = item_at(begin, 0);
   int at = li.s0;  // its step
   int stop = 0;    // the step at which the segment or the item ends
   int left = 0;    // k left in the segment (0 or less: past the last item)
@@ -882,7 +902,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
     if constexpr (GRP && LAY == kDw) {  // experts without rows have no steps
       while (__builtin_expect(at == stop, 0)) {
         if (li.next < end) {
-          li = item_at(li.next);
+          li = item_at(li.next, li.e);
           at = 0;
           place();
         } else {
@@ -895,7 +915,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
     if (__builtin_expect(at == stop, 0)) {
       if (at == li.s1) {
         if (li.next < end) {
-          li = item_at(li.next);
+          li = item_at(li.next, 0);
           at = li.s0;
         } else {
           left = 0;
@@ -1300,6 +1320,13 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         if constexpr (residual && a + 1 < MB) read_residual(a + 1, rv[(a + 1) & 1]);
 #pragma unroll
         for (int b0 = 0; b0 < NO; b0 += 2 * kActs) {
+          if constexpr (GRP && mode == kPlain) {
+#pragma unroll
+            for (int b = b0; b < b0 + 2 * kActs; b += 2)
+              __builtin_amdgcn_raw_buffer_store_b128(round_pair8<DT>(acc[a][b], acc[a][b + 1]), yr,
+                                                     yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
+            continue;
+          }
           F8 v[kActs];
 #pragma unroll
           for (int j = 0; j < kActs; ++j) {
@@ -1377,10 +1404,11 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
     static_for<R>([&](auto I) { read_one(decltype(I)::value, 0, 0); });
   }
   int pbuf = NS - 1, buf = 0;
-  for (int cur = begin; cur < end;) {
-    Item it = item_at(cur);
+  for (int cur = begin, e = 0; cur < end;) {
+    Item it = item_at(cur, e);
     int now = cur;
     cur = it.next;
+    if constexpr (GRP && LAY == kDw) e = it.e;
     for (int t = it.s0; t < it.s1; ++t) {
       const int nbuf = buf + 1 == NS ? 0 : buf + 1;
       half(std::integral_constant<int, 0>{}, pbuf, buf, nbuf);
@@ -1388,9 +1416,9 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
       pbuf = buf;
       buf = nbuf;
     }
-    if constexpr (GRP || I8) {  // found again, not kept over the K loop
+    if constexpr (kAgain) {  // found again, not kept over the K loop
       asm volatile("" : "+s"(now));
-      it = item_at(now);
+      it = item_at(now, 0);
     }
     finish(it);
   }
