@@ -771,7 +771,7 @@ def _lin_call(fn: str, like: torch.Tensor, sizes: tuple | None, *args) -> None:
     captured call goes without (its replays may run on any stream), and so
     does one on a stream that torch did not make."""
     dev = like.device
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _lin_call(fn, like, sizes, *args)
     if sizes is None:  # a call without scratch
@@ -939,12 +939,22 @@ def _scales(t, name: str, device, n: int) -> None:
 
 
 def _codes_out(q, s, names, device, rows: int, cols: int):
-    if q is None:
-        q = torch.empty((rows, cols), dtype=torch.int8, device=device)
     if s is None:
         s = torch.empty(rows, dtype=torch.float32, device=device)
-    _scales(s, names[1], device, rows)
+    else:
+        _scales(s, names[1], device, rows)
+    if q is None:
+        return torch.empty((rows, cols), dtype=torch.int8, device=device), cols, s
     return q, _codes(q, names[0], device, rows, cols), s
+
+
+class _Like:
+    """The type and device of outputs that no input has."""
+
+    __slots__ = ("dtype", "device")
+
+    def __init__(self, dtype: torch.dtype, device: torch.device):
+        self.dtype, self.device = dtype, device
 
 
 def act_quantize_int8(x: torch.Tensor, xq: torch.Tensor | None = None, sx: torch.Tensor | None = None):
@@ -1011,7 +1021,7 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, sx: torch.T
     d_out = wq.shape[0]
     ldw = _codes(wq, "wq", x.device, d_out, d_in)
     _scales(sw, "sw", x.device, d_out)
-    like = torch.empty(0, dtype=dtype, device=x.device) if x.dtype != dtype else x
+    like = x if sx is None else _Like(dtype, x.device)
     if bias is not None:
         _lin_vec(bias, "bias", like, d_out)
     ldr = 0 if residual is None else _lin_mat(residual, "residual", like, T, d_out)

@@ -11,10 +11,10 @@
 // step and per matrix instruction, twice the operations.  Integer sums may be
 // split anywhere and added in any order: equal calls give equal bits.
 //
-// One token (and up to kGemvRows, while they fit LDS) takes dot products
-// instead: a wave reads rows of W in 1 KB pieces and meets x in LDS.  For one
-// token of 16-bit values every workgroup quantises x itself (d_in values from
-// L2), which saves the second launch.
+// One token (and up to kGemvRows) takes dot products instead: a workgroup's
+// 256 threads hold x in registers, 16 values of every 4096 each, and stream rows
+// of W past it.  For one token of 16-bit values every workgroup quantises x
+// itself (d_in values from L2), which saves the second launch.
 #define SA_LINEAR_ENGINE_ONLY
 #include "linear.hip"
 
@@ -34,36 +34,57 @@ __device__ __forceinline__ float scale_of(uint32_t most) {
   if (most >= inf) return __builtin_nanf("");
   return to_f<DT>((uint16_t)most) / 127.f;
 }
-// x / s of the exact quotient, halves to even.  x times the reciprocal may
-// round to a neighbour where the quotient lies next to half a step, so the
-// remainder x - q s decides.  It is exact in fp32: x and q s are multiples of
-// the last place of s unless |x| < s / 2^13, where q = 0.  Scales below 2^-100
-// (bf16 alone has them) and their values are first multiplied by 2^64, so that
-// the reciprocal exists.
+// x / s of the exact quotient, halves to even.
+//
+// x times the reciprocal of s is off the quotient by 2^-14 at most (127 times
+// the reciprocal's and the product's 2^-22), so it rounds as the quotient does
+// unless it lies that near to half a step.  Adding 3 2^22 rounds it to an
+// integer, which the sum's low byte holds: a product, three sums and a byte
+// move per value.  Where one of a lane's 4 values is within 2^-13 of half a step
+// (5 in 10000 lanes), the remainders x - q s decide.  They are exact in fp32: x
+// and q s are multiples of the last place of s unless |x| < s / 2^13, where q =
+// 0.  Scales below 2^-100 (bf16 alone has them), zero and NaN always take that
+// way, values and scale first multiplied by 2^64 so that the reciprocal exists.
 struct Rounder {
   float s, inv, up;
+  bool plain;
   __device__ __forceinline__ explicit Rounder(float scale) {
-    up = scale < 0x1p-100f ? 0x1p64f : 1.f;
+    plain = scale >= 0x1p-100f;
+    up = plain ? 1.f : 0x1p64f;
     s = scale * up;
     inv = s > 0.f ? __builtin_amdgcn_rcpf(s) : 0.f;  // NaN, 0: every q is 0
   }
-  __device__ __forceinline__ int operator()(float x) const {
+  __device__ __forceinline__ uint32_t exact(float x) const {
     const float v = x * up;
     float q = __builtin_rintf(v * inv);
     const float r = __builtin_fmaf(-q, s, v), twice = 2.f * fabsf(r);
     const bool odd = (int)q & 1;
     if (twice > s || (twice == s && odd)) q += __builtin_copysignf(1.f, r);
-    return inv == 0.f ? 0 : (int)q;
+    return inv == 0.f ? 0u : (uint32_t)(int)q & 255u;
+  }
+  // The codes of four values, the first in the low byte.
+  __device__ __forceinline__ uint32_t operator()(float a, float b, float c, float d) const {
+    constexpr float kRound = 12582912.f;  // 3 2^22: a step there is 1
+    const float v[4] = {a, b, c, d};
+    float m[4], off = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __builtin_fmaf(v[i], inv, kRound);
+      off = fmaxf(off, fabsf(__builtin_fmaf(v[i], inv, kRound - m[i])));
+    }
+    if (__builtin_expect(plain && off <= 0.5f - 0x1p-13f, 1)) {
+      // bytes 0 of two sums, then of the two pairs
+      const uint32_t lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, m[1]), __builtin_bit_cast(uint32_t, m[0]), 0x0c0c0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, m[3]), __builtin_bit_cast(uint32_t, m[2]), 0x04000c0cu);
+      return lo | hi;
+    }
+    return exact(a) | exact(b) << 8 | exact(c) << 16 | exact(d) << 24;
   }
 };
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
-}
 template <int DT>
 __device__ __forceinline__ uint2 quant8(u32x4 v, const Rounder& r) {
   const F8 f = widen8<DT>(v);
-  return uint2{pack4(r(f.v[0]), r(f.v[1]), r(f.v[2]), r(f.v[3])),
-               pack4(r(f.v[4]), r(f.v[5]), r(f.v[6]), r(f.v[7]))};
+  return uint2{r(f.v[0], f.v[1], f.v[2], f.v[3]), r(f.v[4], f.v[5], f.v[6], f.v[7])};
 }
 // The larger magnitudes of two pairs of 16-bit values.
 __device__ __forceinline__ u16x2 larger(u16x2 a, uint32_t b) {
@@ -80,38 +101,40 @@ __device__ __forceinline__ uint32_t wave_most(u16x2 m) {
 }
 
 // ---- rows --------------------------------------------------------------------------
-// A row per wave (WIDE false: 4 rows per workgroup) or per workgroup, held in
-// registers between its maximum and its rounding (NV chunks of 8 values per
-// thread), or with NV = 0 read twice.  Bound by memory: 2 bytes read and one
-// written per value; the rounding's ~14 operations per value stay below that.
-template <int DT, bool WIDE, int NV>
-__global__ __launch_bounds__(256) void k_quant_rows(const uint16_t* __restrict__ x, int64_t ldx, int64_t T,
-                                                    int d, int8_t* __restrict__ xq, int64_t ldq,
-                                                    float* __restrict__ sx) {
-  __shared__ uint32_t part[4];
+// A row per wave (NT = 64: 4 rows per workgroup) or per workgroup of NT threads,
+// held in registers between its maximum and its rounding (NV chunks of 8 values
+// per thread), or with NV = 0 read twice.  Bound by memory: 2 bytes read and one
+// written per value.  8192 x 14336: 70 us, 5.0 TB/s (a large copy: 5.1).  Few
+// rows are bound by latency, so they take 1024 threads each.
+template <int DT, int NT, int NV>
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_quant_rows(const uint16_t* __restrict__ x, int64_t ldx,
+                                                                    int64_t T, int d, int8_t* __restrict__ xq,
+                                                                    int64_t ldq, float* __restrict__ sx) {
+  constexpr bool kWide = NT > 64;
+  __shared__ uint32_t part[kWide ? NT / kWave : 1];
   const int lane = lane_id(), w = uni((int)threadIdx.x / kWave);
-  const int64_t t = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + w;
-  if (!WIDE && t >= T) return;
-  const int at = WIDE ? (int)threadIdx.x : lane, step = WIDE ? 256 : 64, chunks = d / 8;
+  const int64_t t = kWide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + w;
+  if (!kWide && t >= T) return;
+  const int at = kWide ? (int)threadIdx.x : lane, chunks = d / 8;
   const u32x4* row = reinterpret_cast<const u32x4*>(x + t * ldx);
   constexpr int N = NV > 0 ? NV : 1;
   u32x4 v[N];
   u16x2 m = {0, 0};
   if constexpr (NV > 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = at + j * step < chunks ? row[at + j * step] : u32x4{0, 0, 0, 0};
+    for (int j = 0; j < NV; ++j) v[j] = at + j * NT < chunks ? row[at + j * NT] : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NV; ++j) m = larger(m, v[j]);
   } else {
 #pragma unroll 4
-    for (int c = at; c < chunks; c += step) m = larger(m, row[c]);
+    for (int c = at; c < chunks; c += NT) m = larger(m, row[c]);
   }
   uint32_t most = wave_most(m);
-  if constexpr (WIDE) {
+  if constexpr (kWide) {
     if (lane == 0) part[w] = most;
     __syncthreads();
-    const uint32_t a = part[0] > part[1] ? part[0] : part[1], b = part[2] > part[3] ? part[2] : part[3];
-    most = a > b ? a : b;
+#pragma unroll
+    for (int i = 0; i < NT / kWave; ++i) most = part[i] > most ? part[i] : most;
   }
   const float s = scale_of<DT>(most);
   const Rounder r(s);
@@ -120,30 +143,35 @@ __global__ __launch_bounds__(256) void k_quant_rows(const uint16_t* __restrict__
   if constexpr (NV > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (at + j * step < chunks) out[at + j * step] = quant8<DT>(v[j], r);
+      if (at + j * NT < chunks) out[at + j * NT] = quant8<DT>(v[j], r);
   } else {
 #pragma unroll 4
-    for (int c = at; c < chunks; c += step) out[c] = quant8<DT>(row[c], r);
+    for (int c = at; c < chunks; c += NT) out[c] = quant8<DT>(row[c], r);
   }
 }
 
 template <int DT>
 void quant_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t d, int8_t* xq, int64_t ldq, float* sx,
                 hipStream_t s) {
-  auto run = [&](auto wide, auto nv) {
-    constexpr bool W = decltype(wide)::value;
-    hipLaunchKernelGGL((k_quant_rows<DT, W, decltype(nv)::value>), dim3((unsigned)(W ? T : (T + 3) / 4)),
-                       dim3(256), 0, s, x, ldx, T, (int)d, xq, ldq, sx);
+  auto run = [&](auto nt, auto nv) {
+    constexpr int NT = decltype(nt)::value;
+    hipLaunchKernelGGL((k_quant_rows<DT, NT, decltype(nv)::value>), dim3((unsigned)(NT > 64 ? T : (T + 3) / 4)),
+                       dim3(NT > 64 ? NT : 256), 0, s, x, ldx, T, (int)d, xq, ldq, sx);
   };
   using std::integral_constant;
-  const std::true_type wide;
+  const integral_constant<int, 64> wave;
+  const integral_constant<int, 256> wide;
+  const integral_constant<int, 1024> widest;
   // a row per wave where that fills the CUs and a lane holds its part
-  if (d <= 2048 && T >= 4 * kCus) run(std::false_type{}, integral_constant<int, 4>{});
+  if (d <= 2048 && T >= 4 * kCus) run(wave, integral_constant<int, 4>{});
   else if (d <= 2048) run(wide, integral_constant<int, 1>{});
+  else if (T < 2 * kCus && d <= 8192) run(widest, integral_constant<int, 1>{});
+  else if (T < 2 * kCus && d <= 16384) run(widest, integral_constant<int, 2>{});
   else if (d <= 4096) run(wide, integral_constant<int, 2>{});
   else if (d <= 8192) run(wide, integral_constant<int, 4>{});
   else if (d <= 16384) run(wide, integral_constant<int, 8>{});
-  else run(wide, integral_constant<int, 0>{});
+  else if (d <= 32768) run(widest, integral_constant<int, 4>{});
+  else run(widest, integral_constant<int, 0>{});
 }
 
 // ---- columns (weights) ----------------------------------------------------------------
@@ -225,10 +253,10 @@ __global__ __launch_bounds__(256) void k_quant_cols(const uint16_t* __restrict__
     const Rounder r(scale[c]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int q[4];
+      float f[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) q[k] = r(to_f<DT>((uint16_t)(v[h][k][i / 2] >> (16 * (i % 2)))));
-      S[c * 65 + tid / 8 + 32 * h] = pack4(q[0], q[1], q[2], q[3]);
+      for (int k = 0; k < 4; ++k) f[k] = to_f<DT>((uint16_t)(v[h][k][i / 2] >> (16 * (i % 2))));
+      S[c * 65 + tid / 8 + 32 * h] = r(f[0], f[1], f[2], f[3]);
     }
   }
   __syncthreads();
@@ -261,111 +289,129 @@ struct GemvP {
   uint16_t* y;
   int64_t ldy;
 };
-constexpr int kGemvRows = 8;
-constexpr int64_t kGemvLds = 64 * 1024;  // T * d_in at most
-__device__ __forceinline__ int wave_sum(int v) {  // uniform
-  const int s = row16_inclusive_scan(v);
-  return (__builtin_amdgcn_readlane(s, 15) + __builtin_amdgcn_readlane(s, 31)) +
-         (__builtin_amdgcn_readlane(s, 47) + __builtin_amdgcn_readlane(s, 63));
+constexpr int kGemvRows = 8, kGemvChannels = 64;  // per workgroup at most
+constexpr int64_t kGemvPiece = 4096, kGemvPieces = 4;
+// Adds lane sums: the wave's total in its last lane.
+__device__ __forceinline__ int wave_total(int v) {
+  v = row16_inclusive_scan(v);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+  return v;
 }
-// CW channels per wave, NT rows of x (those past T are zeros in LDS).
-template <int DT, int NT, int CW, bool QUANT>
+// NT rows of x (those past T are zeros), KP pieces of 4096 k.  The channels are
+// dealt evenly over the workgroups; U of them are under way per wave while U
+// are multiplied, 8 loads of 1 KB at least.
+template <int DT, int NT, int KP, bool QUANT>
 __global__ __launch_bounds__(256) void k_int8_gemv(GemvP p) {
-  extern __shared__ __align__(16) uint8_t X[];  // [NT][K]
-  __shared__ uint32_t part[4];
   static_assert(!QUANT || NT == 1, "one row is quantised in place");
+  __shared__ uint32_t most[4];
+  __shared__ __align__(16) int part[4][kGemvChannels * NT];
   const int tid = (int)threadIdx.x, lane = lane_id(), w = uni(tid / kWave);
-  const int c0 = uni(((int)blockIdx.x * 4 + w) * CW);
-  constexpr int U = NT * CW <= 8 ? 4 : 2;  // pieces of 1 KB per channel in flight
-  u32x4 wv[U][CW];
-  auto fetch = [&](int k) SA_INLINE {
+  const int c0 = uni((int)((int64_t)p.N * (int)blockIdx.x / (int)gridDim.x));
+  const int c1 = uni((int)((int64_t)p.N * ((int)blockIdx.x + 1) / (int)gridDim.x));
+  constexpr int U = KP >= 3 ? 2 : 8 / KP;
+  u32x4 next[U][KP];
+  auto fetch = [&](int c) SA_INLINE {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const int8_t* row = p.wq + (int64_t)(c + u < c1 ? c + u : c1 - 1) * p.ldw;  // past the end: not used
 #pragma unroll
-      for (int c = 0; c < CW; ++c) {
-        const int at = k + u * 1024 + lane * 16;
-        const bool in = at < p.K && c0 + c < p.N;
-        wv[u][c] = in ? *reinterpret_cast<const u32x4*>(p.wq + (c0 + c) * p.ldw + at) : u32x4{0, 0, 0, 0};
+      for (int j = 0; j < KP; ++j) {
+        const int k = j * (int)kGemvPiece + tid * 16;
+        next[u][j] = k < p.K ? *reinterpret_cast<const u32x4*>(row + k) : u32x4{0, 0, 0, 0};
       }
+    }
   };
-  fetch(0);  // under way while x is made ready
+  fetch(c0);  // under way while x is made ready
+  u32x4 x[NT][KP];
   float s = 0.f;
   if constexpr (QUANT) {
     const u32x4* row = reinterpret_cast<const u32x4*>(p.x);
-    const int chunks = p.K / 8;
+    u32x4 v[KP][2];
     u16x2 m = {0, 0};
-#pragma unroll 4
-    for (int c = tid; c < chunks; c += 256) m = larger(m, row[c]);
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+      const int k = j * (int)kGemvPiece + tid * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[j][h] = k < p.K ? row[k / 8 + h] : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < KP; ++j) m = larger(larger(m, v[j][0]), v[j][1]);
     const uint32_t mine = wave_most(m);
-    if (lane == 0) part[w] = mine;
+    if (lane == 0) most[w] = mine;
     __syncthreads();
-    const uint32_t a = part[0] > part[1] ? part[0] : part[1], b = part[2] > part[3] ? part[2] : part[3];
+    const uint32_t a = most[0] > most[1] ? most[0] : most[1], b = most[2] > most[3] ? most[2] : most[3];
     s = scale_of<DT>(a > b ? a : b);
     const Rounder r(s);
-#pragma unroll 4
-    for (int c = tid; c < chunks; c += 256) reinterpret_cast<uint2*>(X)[c] = quant8<DT>(row[c], r);
-  } else {
-    const int chunks = p.K / 16;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const u32x4* row = reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(p.x) + t * p.ldx);
-      for (int c = tid; c < chunks; c += 256)
-        reinterpret_cast<u32x4*>(X)[t * chunks + c] = t < p.T ? row[c] : u32x4{0, 0, 0, 0};
+    for (int j = 0; j < KP; ++j) {
+      const uint2 lo = quant8<DT>(v[j][0], r), hi = quant8<DT>(v[j][1], r);
+      x[0][j] = u32x4{lo.x, lo.y, hi.x, hi.y};
     }
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        const int k = j * (int)kGemvPiece + tid * 16;
+        x[t][j] = t < p.T && k < p.K
+                      ? *reinterpret_cast<const u32x4*>(static_cast<const int8_t*>(p.x) + t * p.ldx + k)
+                      : u32x4{0, 0, 0, 0};
+      }
   }
-  __syncthreads();
-  int acc[NT][CW] = {};
-  for (int k = 0; k < p.K; k += U * 1024) {
-    u32x4 cur[U][CW];
+  for (int c = c0; c < c1; c += U) {
+    u32x4 cur[U][KP];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int c = 0; c < CW; ++c) cur[u][c] = wv[u][c];
-    if (k + U * 1024 < p.K) fetch(k + U * 1024);
+      for (int j = 0; j < KP; ++j) cur[u][j] = next[u][j];
+    if (c + U < c1) fetch(c + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = k + u * 1024 + lane * 16;
+      int sum[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        // past the row's end the weights are zeros; x is read where it exists
-        const u32x4 xv = *reinterpret_cast<const u32x4*>(X + t * p.K + (at < p.K ? at : 0));
+        int a = 0;
 #pragma unroll
-        for (int c = 0; c < CW; ++c)
+        for (int j = 0; j < KP; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[t][c] = __builtin_amdgcn_sdot4((int)cur[u][c][e], (int)xv[e], acc[t][c], false);
+          for (int e = 0; e < 4; ++e) a = __builtin_amdgcn_sdot4((int)cur[u][j][e], (int)x[t][j][e], a, false);
+        sum[t] = wave_total(a);
+      }
+      if (lane == kWave - 1 && c + u < c1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[w][(c + u - c0) * NT + t] = sum[t];
       }
     }
   }
-  // lane t * CW + c finishes row t's channel c
-  int sum = 0;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int c = 0; c < CW; ++c) {
-      const int v = wave_sum(acc[t][c]);
-      sum = lane == t * CW + c ? v : sum;
-    }
-  const int t = lane / CW, n = c0 + lane % CW;
-  if (lane >= NT * CW || t >= p.T || n >= p.N) return;
-  float f = (float)sum * p.sw[n] * (QUANT ? s : p.sx[t]);
-  if (p.bias) f += to_f<DT>(p.bias[n]);
-  with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
-  if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
-  p.y[t * p.ldy + n] = from_f<DT>(f);
+  __syncthreads();
+  for (int i = tid; i < (c1 - c0) * NT; i += 256) {
+    const int t = i % NT, n = c0 + i / NT;
+    if (t >= p.T) continue;
+    const int sum = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+    float f = (float)sum * p.sw[n] * (QUANT ? s : p.sx[t]);
+    if (p.bias) f += to_f<DT>(p.bias[n]);
+    with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
+    if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
+    p.y[t * p.ldy + n] = from_f<DT>(f);
+  }
 }
 
 template <int DT, int NT, bool QUANT>
 hipError_t gemv(const GemvP& p, hipStream_t s) {
-  const size_t lds = (size_t)NT * p.K;
-  // four channels per wave where that still gives every CU four waves
-  auto run = [&](auto cw) {
-    constexpr int CW = decltype(cw)::value;
-    hipLaunchKernelGGL((k_int8_gemv<DT, NT, CW, QUANT>), dim3((unsigned)((p.N + 4 * CW - 1) / (4 * CW))),
-                       dim3(256), lds, s, p);
+  // two workgroups per CU, of four channels at least
+  int64_t blocks = (p.N + 3) / 4 < 2 * kCus ? (p.N + 3) / 4 : 2 * kCus;
+  const int64_t least = (p.N + kGemvChannels - 1) / kGemvChannels;
+  blocks = blocks > least ? blocks : least;
+  auto run = [&](auto kp) {
+    hipLaunchKernelGGL((k_int8_gemv<DT, NT, decltype(kp)::value, QUANT>), dim3((unsigned)blocks), dim3(256), 0, s, p);
   };
-  if (p.N >= 16 * kCus) run(std::integral_constant<int, 4>{});
-  else run(std::integral_constant<int, 1>{});
+  switch ((p.K + kGemvPiece - 1) / kGemvPiece) {
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 3: if constexpr (NT <= 4) run(std::integral_constant<int, 3>{}); break;
+    default: if constexpr (NT <= 4) run(std::integral_constant<int, 4>{});
+  }
   return hipGetLastError();
 }
 
@@ -408,9 +454,9 @@ __global__ __launch_bounds__(256) void k_int8_reduce(Int8P p, int lbm, int lbn) 
 Plan int8_plan(int64_t T, int64_t d_in, int64_t d_out) {
   return lin_plan(kDx, false, T, d_out, d_in / 2, 1, 1);
 }
+// x in at most 64 registers
 bool gemv_fits(int64_t T, int64_t d_in) {
-  const int64_t rows = T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8;
-  return T <= kGemvRows && rows * d_in <= kGemvLds;
+  return T <= kGemvRows && d_in <= kGemvPiece * (T <= 4 ? kGemvPieces : kGemvPieces / 2);
 }
 
 template <int DT>
