@@ -73,9 +73,16 @@ inline int64_t grp_row_tiles(int tile, int64_t T, int64_t E) {  // at most
 
 // The tile and split with the smallest estimated time, for rows spread evenly
 // over the experts (the host knows no more).  An expert's rows fill tiles of
-// BM rows but for half of the last one.  Times per step as in the dense plan.
+// BM rows but for half of the last one.  A step takes what it does in the dense
+// plan, and tiles of up to 64 rows as long as a CU needs to read their weights
+// at 40 GB/s; together they read them at 6.6 TB/s, each for itself, as they run
+// far apart (larger ones share them).  A round of workgroups costs 4 us more, a
+// split 8 (5 where only the last of several rounds is) and its partial sums.
+// Over 22 random shapes (forward, gated, dx; 1 to 3924 rows, 1 to 124 experts)
+// the choice took 2 percent longer than the best of a sweep on average, 25 at
+// most (108 rows of 14 experts, gated 992 -> 312: 18.5 against 14.8 us).
 inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, int64_t K, int segs) {
-  static const double alone[2][kGrpTiles] = {{1.45, 0.60, 0.45, 0.40, 0.38}, {1.45, 0.95, 0.60, 0.55, 0.50}};
+  static const double alone[2][kGrpTiles] = {{1.45, 0.60, 0.45, 0.41, 0.41}, {1.45, 0.95, 0.82, 0.82, 0.82}};
   static const double paired[kGrpTiles] = {0, 0.50, 0.36, 0.25, 0.22};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
   const double used = (double)(E < T ? E : T), mean = used > 0 ? T / used : 0;
@@ -84,28 +91,27 @@ inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, in
   if (tuned_tile >= kGrpTiles) tuned_tile = -1;
   GrpPlan best{kGrpTiles - 1, 0, 0};
   double least = 1e30;
-  for (int t = 0; t < kGrpTiles; ++t) {
+  for (int t = kGrpTiles - 1; t >= 0; --t) {
     if (tuned_tile >= 0 && t != tuned_tile) continue;
     const int64_t nt = (N + (gated ? 128 : kGrpN[t]) - 1) / (gated ? 128 : kGrpN[t]);
     const int64_t most = grp_row_tiles(t, T, E) * nt;
     const double per = mean <= kGrpM[t] / 2 ? 1 : mean / kGrpM[t] + 0.5;  // row tiles of an expert
     const double tiles = used * per * nt;
     const bool pairs = t > 0 && !gated;
-    double step = alone[gated][t];
-    if (t > 0 && per < 4) {
-      const double stream = (gated ? 32768 : 16384) / (per <= 1.5 ? 26e3 : 40e3) + 0.1 * step;
-      step = stream > step ? stream : step;
-    }
+    const double step = alone[gated][t];
     const double both = pairs && 2 * paired[t] > step ? 2 * paired[t] : step;
+    const double read = (t >= 2 ? tiles : used * nt) * steps * (gated || t == 0 ? 32768 : 16384) / 6.6e6 + 4;
     const int64_t cus = pairs ? 2 * kCus : kCus;
     const double rounds = tiles <= cus ? 1 : (int64_t)(tiles / cus) + 1;
-    const double whole = rounds * (steps * (tiles > kCus ? both : step) + 4);
+    double whole = rounds * (steps * (tiles > kCus ? both : step) + 4);
+    whole = whole > 1.08 * read ? whole : 1.08 * read;  // whole tiles end unevenly
     // even shares, one workgroup per CU; positions times shares fit 31 bits
     int64_t shares = tuned_split > 0 ? tuned_split : kCus;
     while (shares & (shares - 1)) shares &= shares - 1;
-    if (t == 0) {  // the last round alone is shared, where the device finds that it pays
+    if (t == 0) {  // the last round alone is shared, where the device finds that it pays: from 24 steps on
       if (shares > kCus) shares = kCus;
-      const bool rest = tuned_split != 0 && kCus * steps * shares < 0x7fffffffLL && most < 0x3fffffffLL;
+      const bool rest = tuned_split != 0 && (tuned_split > 0 || steps >= 24) &&
+                        kCus * steps * shares < 0x7fffffffLL && most < 0x3fffffffLL;
       if (whole < least) {
         least = whole;
         best = GrpPlan{t, rest ? (int)shares : 0, most};
@@ -117,9 +123,12 @@ inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, in
       best = GrpPlan{t, 0, most};
     }
     if (tuned_split == 0 || most * steps * shares >= 0x7fffffffLL) continue;
-    if (tuned_split < 0 && t < 2 && tiles >= shares) continue;
+    // not tiles of 128 rows: their shares took 1.65 us a step in dx (509 rows,
+    // 16 experts of 1024 x 4096: 53 us, whole tiles of 64 rows 40)
+    if (tuned_split < 0 && t < 2) continue;
     const double parts = shares * 2.0 * (mean < kGrpM[t] ? mean : kGrpM[t]) * (gated ? 256 : 128) * 8 / 4e6;
-    const double time = tiles * steps / shares * step + 8 + parts;
+    const double shared = tiles * steps / shares * step;
+    const double time = (shared > read ? shared : read) + (tiles > shares ? 5 : 8) + parts;
     if (time < least) {
       least = time;
       best = GrpPlan{t, (int)shares, most};
@@ -139,6 +148,17 @@ void grp_tile(const GroupP& p, int64_t items, hipStream_t s) {  // items: shares
   constexpr int64_t most = kCus * (160 * 1024 / (lin_lds<LAY, BM, BN, NS>() + (int)sizeof(GroupTab)));
   const dim3 grid((unsigned)(p.split || items < most ? items : most));
   hipLaunchKernelGGL((k_grp<DT, LAY, GATED, EPI, BM, BN, WM, WN, NS>), grid, dim3(256), 0, s, p);
+}
+
+template <int DT, bool GATED>
+hipError_t launch_grp_reduce(const GroupP& p, const GrpPlan& pl, hipStream_t s) {
+  const int rows = kGrpM[pl.tile] < p.T ? kGrpM[pl.tile] : p.T, lbm = __builtin_ctz(kGrpM[pl.tile]);
+  if (!GATED && pl.tile == 0)
+    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, 256>), dim3(pl.split, (rows + 7) / 8), dim3(256), 0, s, p, lbm);
+  else
+    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, GATED ? 256 : 128>), dim3(pl.split, (rows + 15) / 16), dim3(256), 0,
+                       s, p, lbm);
+  return hipGetLastError();
 }
 
 // Forward and dx.
@@ -169,13 +189,7 @@ hipError_t launch_grp(GroupP p, void* ws, hipStream_t s) {
     grp_tile<DT, LAY, GATED, EPI, 16, SB, 1, 4, GATED ? 4 : 3>(p, items, s);
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !pl.split) return e;
-  const int rows = kGrpM[pl.tile] < p.T ? kGrpM[pl.tile] : p.T, lbm = __builtin_ctz(kGrpM[pl.tile]);
-  if (!GATED && pl.tile == 0)
-    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, 256>), dim3(pl.split, (rows + 7) / 8), dim3(256), 0, s, p, lbm);
-  else
-    hipLaunchKernelGGL((k_grp_reduce<DT, GATED, SB>), dim3(pl.split, (rows + 15) / 16), dim3(256), 0, s, p, lbm);
-  return hipGetLastError();
+  return e != hipSuccess || !pl.split ? e : launch_grp_reduce<DT, GATED>(p, pl, s);
 }
 
 }  // namespace

@@ -233,11 +233,13 @@ __global__ __launch_bounds__(256) void k_quant_cols(const uint16_t* __restrict__
       v[h][i] = k < K && n < N ? *reinterpret_cast<const u32x4*>(wt + k * ldw + n) : u32x4{0, 0, 0, 0};
     }
   uint32_t m = 0;
-  if (n0 + tid % 64 < N)
-    for (int s = tid / 64; s < strips; s += 4) {
-      const uint32_t o = part[(int64_t)s * N + n0 + tid % 64];
-      m = o > m ? o : m;
-    }
+  const int mine = n0 + tid % 64 < N ? n0 + tid % 64 : N - 1;
+#pragma unroll
+  for (int i = 0; i < kColStrips / 4; ++i) {  // all under way at once
+    const int s = tid / 64 + 4 * i < strips ? tid / 64 + 4 * i : 0;
+    const uint32_t o = part[(int64_t)s * N + mine];
+    m = o > m ? o : m;
+  }
   most[tid / 64][tid % 64] = m;
   __syncthreads();
   if (tid < 64) {

@@ -699,22 +699,23 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   const int steps = ks * p.segs;
   // A cursor goes over the workgroup's items: a tile's number, or (split) a
   // position among all tiles' steps, up to `end`.
-  // By expert, weight gradients are never split, and of tiles of 256 rows only
-  // the last round is: whole tiles come first (`full` of them), then an even
-  // share of the steps of the rest, where that saves more than the partial
-  // sums cost.  Per step of a full round 1.45 us; a partial sum 0.1 us (256 KB
-  // written and read), the reduction's launch 4 us.
+  // By expert, weight gradients are never split, and of other products only the
+  // last round is: whole tiles come first (`full` of them), then an even share of
+  // the steps of the rest, where that pays.  For tiles of 256 rows it has to save
+  // more than the partial sums cost: per step of a full round 1.45 us; a partial
+  // sum 0.1 us (256 KB written and read), the reduction's launch 4 us.  Others
+  // are shared unless they nearly fill a round.
   const bool split = !(GRP && LAY == kDw) && p.split > 0;
-  constexpr bool kRest = GRP && LAY != kDw && BM == 256;
+  constexpr bool kRest = GRP && LAY != kDw && BM == 256, kShares = GRP && LAY != kDw;
   int lg = split ? __builtin_ctz(p.split) : 0;
   int full = 0;
   if constexpr (GRP) {
     if (split) {
-      if constexpr (kRest) {
-        const int rest = tiles & (p.split - 1);
-        full = tiles - rest;
-        if ((p.split - rest) * (float)steps * 1.45f < p.split * ((p.split + rest) * 0.1f + 4.f)) full = tiles;
-      }
+      const int rest = tiles & (p.split - 1);
+      full = tiles - rest;
+      if (kRest ? (p.split - rest) * (float)steps * 1.45f < p.split * ((p.split + rest) * 0.1f + 4.f)
+                : rest * 4 > p.split * 3)
+        full = tiles;
       // the device alone knows the steps: shares of at least two, fewer of them if need be
       const int most = 30 - __builtin_clz((tiles - full) * steps | 3);
       lg = most < lg ? most : lg;
@@ -730,7 +731,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   int begin = split ? (int)((uint32_t)share * (uint32_t)TS >> lg) : block;
   int end = split ? (int)((uint32_t)(share + 1) * (uint32_t)TS >> lg) : tiles;
   int after = 0;  // where the share follows the whole tiles: below `full` the cursor counts those
-  if constexpr (kRest) {
+  if constexpr (kShares) {
     if (split) {
       if (share >= 1 << lg) begin = end = 0;
       after = full + begin;
@@ -797,7 +798,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
           it.s0 = cur - full - (t - full) * steps;
           it.s1 = uni(it.s0 + end - cur < steps ? it.s0 + end - cur : steps);
           it.next = cur + it.s1 - it.s0;
-        } else if (kRest && split && it.next >= full) {
+        } else if (split && it.next >= full) {
           it.next = after;
         }
       }
@@ -1103,22 +1104,40 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   // of BM x BN each.
   auto finish_cut = [&](const Item& it) SA_INLINE {
     const P& p = arguments();
-    float* const part = p.part + (int64_t)(share * 2 + (it.s0 == 0)) * BM * BN;
+    const int rows = it.mend - it.m0 < BM ? it.mend - it.m0 : BM;
+    float* const base = p.part + (int64_t)(share * 2 + (it.s0 == 0)) * BM * BN;
+    // Few rows: those past the expert's last lie out of range, and their stores
+    // are dropped (6 rows gated 7648 -> 1144: 24 -> 21 us).
+    const auto part = __builtin_amdgcn_make_buffer_rsrc((void*)uni(base), 0, uni(rows * BN * 4), 0x00020000);
+    auto put = [&](int row, int n, const F8& f) SA_INLINE {
+      if constexpr (kRest) {
+        store_part(base + row * BN + n, f);
+        return;
+      }
+      u32x4 lo, hi;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = f.v[e], y = f.v[4 + e];
+        lo[e] = __builtin_bit_cast(uint32_t, x);
+        hi[e] = __builtin_bit_cast(uint32_t, y);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(lo, part, (uint32_t)(row * BN + n) * 4, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(hi, part, (uint32_t)(row * BN + n + 4) * 4, 0, 0);
+    };
     static_for<MB>([&](auto A) {
       constexpr int a = decltype(A)::value;
       take_row(a);
-      float* const row = part + ((wm * MB + a) * 16 + i) * BN;
+      const int row = (wm * MB + a) * 16 + i;
 #pragma unroll
       for (int b = 0; b < NO; b += 2) {
         const int n = (wn * NO + b + (g & 1)) * 16 + 8 * (g >> 1);
-        store_part(row + n, pair8(acc[a][b], acc[a][b + 1]));
-        if constexpr (GATED) store_part(row + BN / 2 + n, pair8(acc[a][b + NO], acc[a][b + NO + 1]));
+        put(row, n, pair8(acc[a][b], acc[a][b + 1]));
+        if constexpr (GATED) put(row, BN / 2 + n, pair8(acc[a][b + NO], acc[a][b + NO + 1]));
       }
     });
     if constexpr (GRP) {
       if (it.s0 == 0 && threadIdx.x == 0) {
         const int cur = end - full - it.s1;  // a tile that is not ended ends its share
-        const int rows = it.mend - it.m0 < BM ? it.mend - it.m0 : BM;
         p.cut[share] = CutTile{share_of(cur + steps - 1, TS, 1 << lg) - share + 1, it.m0, rows,
                                it.n0, it.e, {}};
       }
