@@ -439,17 +439,24 @@ __device__ __forceinline__ F8 pair8(const f4v& a, const f4v& b) {
   }
   return f;
 }
-// The same, rounded first: 8 outputs in 4 conversions of pairs and 2 swaps.
+// Two values rounded to the element type (bf16: one conversion of both).
 template <int DT>
-__device__ __forceinline__ u32x4 round_pair8(const f4v& a, const f4v& b) {
+__device__ __forceinline__ uint32_t round2(float x, float y) {
   typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
   typedef float f2v __attribute__((ext_vector_type(2)));
-  auto two = [](float x, float y) SA_INLINE {
-    if constexpr (DT == SA_F16) return (uint32_t)f2h(x) | (uint32_t)f2h(y) << 16;
-    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{x, y}, bf2v));
-  };
-  const auto s = __builtin_amdgcn_permlane16_swap(two(a[0], a[1]), two(b[0], b[1]), false, false);
-  const auto t = __builtin_amdgcn_permlane16_swap(two(a[2], a[3]), two(b[2], b[3]), false, false);
+  if constexpr (DT == SA_F16) return (uint32_t)f2h(x) | (uint32_t)f2h(y) << 16;
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2v{x, y}, bf2v));
+}
+template <int DT>
+__device__ __forceinline__ u32x4 round8_pairs(const F8& f) {
+  return u32x4{round2<DT>(f.v[0], f.v[1]), round2<DT>(f.v[2], f.v[3]), round2<DT>(f.v[4], f.v[5]),
+               round2<DT>(f.v[6], f.v[7])};
+}
+// pair8, rounded first: 8 outputs in 4 conversions of pairs and 2 swaps.
+template <int DT>
+__device__ __forceinline__ u32x4 round_pair8(const f4v& a, const f4v& b) {
+  const auto s = __builtin_amdgcn_permlane16_swap(round2<DT>(a[0], a[1]), round2<DT>(b[0], b[1]), false, false);
+  const auto t = __builtin_amdgcn_permlane16_swap(round2<DT>(a[2], a[3]), round2<DT>(b[2], b[3]), false, false);
   return u32x4{s[0], t[0], s[1], t[1]};
 }
 __device__ __forceinline__ void store_part(float* p, const F8& f) {
@@ -1194,6 +1201,10 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
   auto finish_rows = [&](const Item& it) SA_INLINE {
     const P& p = arguments();
     constexpr int mode = EPI;
+    auto rounded = [](const F8& f) SA_INLINE {
+      if constexpr (GRP || I8) return round8_pairs<DT>(f);
+      else return round8<DT>(f);
+    };
     auto activate = [&](F8 (&f)[kActs]) SA_INLINE {
       if constexpr (kActs == 1) {
         act8(p.act, f[0]);
@@ -1237,9 +1248,9 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
             f[j] = pair8(acc[a][b], acc[a][b + 1]);
             u[j] = pair8(acc[a][b + NO], acc[a][b + NO + 1]);
             if constexpr (mode == kGeneral) {
-              __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f[j]), gr,
+              __builtin_amdgcn_raw_buffer_store_b128(rounded(f[j]), gr,
                   (uint32_t)((row + 16 * a) * p.ldpre[0] * 2) + col[b / 2], 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(u[j]), ur,
+              __builtin_amdgcn_raw_buffer_store_b128(rounded(u[j]), ur,
                   (uint32_t)((row + 16 * a) * p.ldpre[1] * 2) + col[b / 2], 0, 0);
             }
           }
@@ -1248,7 +1259,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
           for (int j = 0; j < kActs; ++j) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[j].v[e] *= u[j].v[e];
-            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f[j]), yr,
+            __builtin_amdgcn_raw_buffer_store_b128(rounded(f[j]), yr,
                                                    yo + (uint32_t)(a * ystep) + col[b0 / 2 + j], 0, 0);
           }
         }
@@ -1362,7 +1373,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
 #pragma unroll
               for (int e = 0; e < 8; ++e) f.v[e] += bias.v[e];
               if constexpr (mode == kGeneral)
-                __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(rounded(f), pr, po + (uint32_t)(a * pstep) + col[b / 2], 0, 0);
             }
           }
           if constexpr (general) activate(v);
@@ -1379,7 +1390,7 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
 #pragma unroll
               for (int e = 0; e < 8; ++e) f.v[e] += r.v[e];
             }
-            __builtin_amdgcn_raw_buffer_store_b128(round8<DT>(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(rounded(f), yr, yo + (uint32_t)(a * ystep) + col[b / 2], 0, 0);
           }
         }
       });
