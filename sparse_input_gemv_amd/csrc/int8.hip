@@ -11,10 +11,18 @@
 // step and per matrix instruction, twice the operations.  Integer sums may be
 // split anywhere and added in any order: equal calls give equal bits.
 //
-// One token (and up to kGemvRows) takes dot products instead: a workgroup's
-// 256 threads hold x in registers, 16 values of every 4096 each, and stream rows
-// of W past it.  For one token of 16-bit values every workgroup quantises x
-// itself (d_in values from L2), which saves the second launch.
+// Up to 4 tokens (and up to 8 of large weights) take dot products instead: a
+// workgroup's 256 threads hold x in registers, 16 values of every 4096 each, and
+// stream rows of W past it.  For one token of 16-bit values every workgroup
+// quantises x itself (d_in values from L2), which saves the second launch.  More
+// tokens, up to 64, of weights that are not too large take 16 channels per
+// workgroup (k_int8_rows).
+//
+// Measured on MI355X, from Python, calls back to back: 1 token 4096 -> 11008 9.8
+// us (kernel 10.3: 45 MB at 4.4 TB/s; a large copy runs at 5.1), 33 tokens 11008
+// -> 4096 19.6 (codes 3.9, product 12.9, its partial sums 3.9), 8192 tokens 4096
+// -> 14336 with bias and silu 408: 2360 TOPS (the library's product alone, with
+// 32-bit sums written: 2261 with both operands k-contiguous, 2002 else).
 #define SA_LINEAR_ENGINE_ONLY
 #include "linear.hip"
 
@@ -417,6 +425,92 @@ hipError_t gemv(const GemvP& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- up to 64 tokens: 16 channels per workgroup ------------------------------------------
+// Eight waves share d_in, 256 of every 2048 k each, and keep their own sums of
+// 16 channels by 16 RB tokens; operands go straight from memory to registers (a
+// lane's 16 bytes of a channel or a token are the matrix instruction's), and the
+// next 256 k are under way while 256 are multiplied.  W is read once, x by every
+// workgroup from L2.  No partial sums leave the workgroup, so there is no second
+// launch.  Bound by the loads in flight: (1 + RB) bytes per weight arrive at 8 to
+// 11 TB/s, so it pays while those are 92 MB at most (codes given; 33 tokens 4096
+// -> 4096: 9.5 us, the split product 12.2; 16 tokens 11008 -> 4096: 12.8 against
+// 14.2; but 33 tokens there 20.2 against 15.7).
+constexpr int kRowsWaves = 8, kRowsK = 256;
+constexpr int64_t kRowsMost = 64, kRowsBytes = 92 << 20;
+template <int DT, int RB>
+__global__ __launch_bounds__(kRowsWaves * 64) void k_int8_rows(GemvP p) {
+  constexpr int U = kRowsK / 64;
+  __shared__ __align__(16) int S[kRowsWaves][RB * 256];
+  const int tid = (int)threadIdx.x, lane = lane_id(), w = uni(tid / kWave);
+  const int i = lane % 16, g = lane / 16, c0 = (int)blockIdx.x * 16;
+  // past the last channel or token: a row that exists, whose sums are not used
+  const int8_t* wrow = p.wq + (int64_t)(c0 + i < p.N ? c0 + i : p.N - 1) * p.ldw;
+  const int8_t* xrow[RB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+    xrow[r] = static_cast<const int8_t*>(p.x) + (int64_t)(r * 16 + i < p.T ? r * 16 + i : p.T - 1) * p.ldx;
+  i4v a[U], b[U][RB];
+  auto fetch = [&](int k0) SA_INLINE {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * 64 + g * 16;
+      const bool in = k < p.K;  // past the end: zero weights, any x
+      const int at = in ? k : 0;
+      const i4v v = *reinterpret_cast<const i4v*>(wrow + at);
+      a[u] = in ? v : i4v{0, 0, 0, 0};
+#pragma unroll
+      for (int r = 0; r < RB; ++r) b[u][r] = *reinterpret_cast<const i4v*>(xrow[r] + at);
+    }
+  };
+  i4v sum[RB] = {};
+  fetch(w * kRowsK);
+  for (int k = w * kRowsK; k < p.K; k += kRowsWaves * kRowsK) {
+    i4v ca[U], cb[U][RB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ca[u] = a[u];
+#pragma unroll
+      for (int r = 0; r < RB; ++r) cb[u][r] = b[u][r];
+    }
+    if (k + kRowsWaves * kRowsK < p.K) fetch(k + kRowsWaves * kRowsK);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < RB; ++r)
+        sum[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ca[u], cb[u][r], sum[r], 0, 0, 0);
+  }
+  // lane: token 16 r + i, channels 4 g .. 4 g + 3
+#pragma unroll
+  for (int r = 0; r < RB; ++r) *reinterpret_cast<i4v*>(&S[w][(r * 16 + i) * 16 + 4 * g]) = sum[r];
+  __syncthreads();
+  for (int o = tid; o < RB * 256; o += kRowsWaves * 64) {
+    const int t = o / 16, n = c0 + o % 16;
+    if (t >= p.T || n >= p.N) continue;
+    int total = 0;
+#pragma unroll
+    for (int j = 0; j < kRowsWaves; ++j) total += S[j][o];
+    float f = (float)total * p.sw[n] * p.sx[t];
+    if (p.bias) f += to_f<DT>(p.bias[n]);
+    with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
+    if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
+    p.y[t * p.ldy + n] = from_f<DT>(f);
+  }
+}
+template <int DT>
+hipError_t rows(const GemvP& p, hipStream_t s) {
+  auto run = [&](auto rb) {
+    hipLaunchKernelGGL((k_int8_rows<DT, decltype(rb)::value>), dim3((unsigned)((p.N + 15) / 16)),
+                       dim3(kRowsWaves * 64), 0, s, p);
+  };
+  switch ((p.T + 15) / 16) {
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 3: run(std::integral_constant<int, 3>{}); break;
+    default: run(std::integral_constant<int, 4>{});
+  }
+  return hipGetLastError();
+}
+
 // ---- matrix instructions ----------------------------------------------------------------
 template <int DT, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(256, 1) void k_int8(Int8P p) {
@@ -456,9 +550,19 @@ __global__ __launch_bounds__(256) void k_int8_reduce(Int8P p, int lbm, int lbn) 
 Plan int8_plan(int64_t T, int64_t d_in, int64_t d_out) {
   return lin_plan(kDx, false, T, d_out, d_in / 2, 1, 1);
 }
-// x in at most 64 registers
-bool gemv_fits(int64_t T, int64_t d_in) {
-  return T <= kGemvRows && d_in <= kGemvPiece * (T <= 4 ? kGemvPieces : kGemvPieces / 2);
+// Which kernel: dot products (x in at most 64 registers), 16 channels per
+// workgroup, or the tiles.  From 5 tokens on the second is as fast as the first
+// or faster (8 tokens 4096 -> 4096 8.7 and 8.7 us, 11008 -> 4096 12.1 against the
+// tiles' 13.9).
+enum Kernel { kDots, kRows, kTilesOf };
+Kernel kernel_of(int64_t T, int64_t d_in, int64_t d_out) {
+  if (T <= 4 && d_in <= kGemvPiece * kGemvPieces) return kDots;
+  if (T <= kRowsMost && (1 + (T + 15) / 16) * d_in * d_out <= kRowsBytes) return kRows;
+  return T <= kGemvRows && d_in <= kGemvPiece * kGemvPieces / 2 ? kDots : kTilesOf;
+}
+// A single token of 16-bit values is quantised by the product's own launch.
+bool quantise_first(int64_t T, int64_t d_in, int64_t d_out, bool quantised) {
+  return !quantised && !(T == 1 && kernel_of(T, d_in, d_out) == kDots);
 }
 
 template <int DT>
@@ -498,14 +602,13 @@ hipError_t matmul(Int8P p, void* ws, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Scratch: 16-bit x's codes and scales (but for a single token), then the
-// split product's partial sums.
+// Scratch: 16-bit x's codes and scales, then the split product's partial sums.
 struct Scratch {
   size_t codes = 0, scales = 0, end = 0;
 };
-Scratch scratch_of(int64_t T, int64_t d_in, bool quantised) {
+Scratch scratch_of(int64_t T, int64_t d_in, int64_t d_out, bool quantised) {
   Scratch b;
-  if (quantised || (T == 1 && gemv_fits(T, d_in))) return b;
+  if (!quantise_first(T, d_in, d_out, quantised)) return b;
   b.scales = round256((size_t)(T * d_in));
   b.end = b.scales + round256((size_t)T * 4);
   return b;
@@ -514,12 +617,12 @@ Scratch scratch_of(int64_t T, int64_t d_in, bool quantised) {
 template <int DT>
 hipError_t linear_dt(const Int8Call& c, hipStream_t s) {
   char* ws = static_cast<char*>(c.ws);
-  const Scratch b = scratch_of(c.T, c.d_in, c.sx != nullptr);
-  const bool few = gemv_fits(c.T, c.d_in), quantise = c.sx == nullptr && !(c.T == 1 && few);
+  const Scratch b = scratch_of(c.T, c.d_in, c.d_out, c.sx != nullptr);
+  const Kernel kernel = kernel_of(c.T, c.d_in, c.d_out);
   const void* x = c.x;
   int64_t ldx = c.ldx;
   const float* sx = c.sx;
-  if (quantise) {
+  if (quantise_first(c.T, c.d_in, c.d_out, c.sx != nullptr)) {
     int8_t* codes = reinterpret_cast<int8_t*>(ws + b.codes);
     float* scales = reinterpret_cast<float*>(ws + b.scales);
     quant_rows<DT>(static_cast<const uint16_t*>(c.x), c.ldx, c.T, c.d_in, codes, c.d_in, scales, s);
@@ -529,9 +632,10 @@ hipError_t linear_dt(const Int8Call& c, hipStream_t s) {
     ldx = c.d_in;
     sx = scales;
   }
-  if (few) {
+  if (kernel != kTilesOf) {
     const GemvP p{x, ldx, sx, c.wq, c.ldw, c.sw, (int)c.T, (int)c.d_out, (int)c.d_in, c.bias, c.res,
                   c.ldr, c.act, c.y, c.ldy};
+    if (kernel == kRows) return rows<DT>(p, s);
     if (c.T == 1) return sx ? gemv<DT, 1, false>(p, s) : gemv<DT, 1, true>(p, s);
     if (c.T == 2) return gemv<DT, 2, false>(p, s);
     return c.T <= 4 ? gemv<DT, 4, false>(p, s) : gemv<DT, 8, false>(p, s);
@@ -590,8 +694,8 @@ hipError_t launch_weight_quantize_int8(int dtype, const uint16_t* wt, int64_t ld
 }
 
 size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, bool quantised) {
-  const size_t b = scratch_of(T, d_in, quantised).end;
-  return b + (gemv_fits(T, d_in) ? 0 : part_bytes(int8_plan(T, d_in, d_out), T, d_out, d_in / 2, 1, 1));
+  const size_t b = scratch_of(T, d_in, d_out, quantised).end;
+  return b + (kernel_of(T, d_in, d_out) != kTilesOf ? 0 : part_bytes(int8_plan(T, d_in, d_out), T, d_out, d_in / 2, 1, 1));
 }
 
 hipError_t launch_int8_linear(const Int8Call& c, hipStream_t s) {

@@ -205,7 +205,11 @@ def test_every_tile_and_split(tuning, tile, split):  # noqa: F811
 
 
 @pytest.mark.parametrize("shape", [(1, 4096, 11008), (8, 8192, 4096), (33, 11008, 4096), (1, 14336, 1024), (1, 65536, 72),
-                                   (1, 65552, 72), (2048, 4096, 1424), (1, 16, 40008)], ids=str)
+                                   (1, 65552, 72), (2048, 4096, 1424), (1, 16, 40008),
+                                   # either side of where one kernel takes over from another
+                                   (4, 16384, 264), (4, 16400, 264), (5, 4096, 11776), (5, 4096, 11768), (8, 8192, 5896),
+                                   (8, 8208, 5896), (64, 4096, 4704), (64, 4096, 4712), (17, 11008, 2920),
+                                   (17, 11008, 2928)], ids=str)
 def test_layer_sizes(shape):
     t, d_in, d_out = shape
     dt = torch.bfloat16
