@@ -620,7 +620,7 @@ size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_
  *   Their strides, alignment and overlap are the dense layers'.
  * - Codes are int8, in -127 .. 127 where the quantisers wrote them; a matrix of
  *   them has a row stride in elements, a multiple of 16, at least the row
- *   length, at most 2^21, and is 16-byte aligned, as are scales (fp32).
+ *   length, at most 2^21, and is 16-byte aligned.  Scales are fp32.
  * - Codes of a row (or channel) with largest magnitude m: the scale s is the
  *   fp32 quotient m / 127, a code the exact quotient x / s rounded to the
  *   nearest integer, halves to even.  m = 0 gives s = 0 and codes 0; Inf or

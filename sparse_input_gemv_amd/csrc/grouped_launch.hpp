@@ -3,12 +3,13 @@
 // items that carry their expert: every workgroup first turns the offsets,
 // which the host never sees, into a table of row tiles in its LDS.
 //
-// Few rows per expert: the steps of all tiles are dealt evenly over the
-// workgroups, as in the dense layers, but the tiles' number is known on the
-// device only.  So partial sums belong to shares, not tiles: a share can hold
-// part of two tiles at most, its first and its last, and those it holds whole
-// it finishes.  The share that begins a tile it does not end writes the tile
-// down for k_grp_reduce.
+// A split deals the steps of the last round of tiles (of all, where they are
+// fewer than the workgroups) evenly over the workgroups, as in the dense layers,
+// but the tiles' number is known on the device only.  So partial sums belong to
+// shares, not tiles: a share can hold part of two tiles at most, its first and
+// its last, and those it holds whole it finishes.  The share that begins a tile
+// it does not end writes the tile down for k_grp_reduce.  (Decoding, 16 rows over
+// 8 experts, gated 4096 -> 14336, bf16: whole tiles 257 us, split 242, 6.8 TB/s.)
 #pragma once
 
 #define SA_LINEAR_ENGINE_ONLY

@@ -508,9 +508,10 @@ __device__ __forceinline__ int wave_running_max(int v) {
   const int row = lane_id() >> 4, below = row == 0 ? 0 : row == 1 ? r0 : row == 2 ? r01 : r02;
   return below > v ? below : v;
 }
-// Fills the table for row tiles of 2^lg rows and `cols` columns of tiles; 256 threads.  Offsets are cut to
-// 0 .. T and raised to the largest before them, so whatever they hold, the
-// experts' rows are T at most, in order, and apart.  Ends with a barrier.
+// Fills the table for row tiles of 2^lg rows and `cols` columns of tiles; 256
+// threads.  Offsets are cut to 0 .. T and raised to the largest before them, so
+// whatever they hold, the experts' rows are T at most, in order, and apart.
+// Ends with a barrier.
 __device__ __forceinline__ void group_table(const int32_t* offsets, int E, int T, int lg, int cols, GroupTab& tab) {
   for (int i = threadIdx.x; i <= E; i += 256) {
     const int v = offsets[i];

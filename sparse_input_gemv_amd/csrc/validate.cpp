@@ -385,7 +385,7 @@ int check_int8_codes(const char* fn, const char* name, const void* p, int64_t ld
 
 int check_scales(const char* fn, const char* name, const void* p, bool optional) {
   REQUIRE(optional || p != nullptr, SA_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
-  REQUIRE(aligned(p, 16), SA_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned", fn, name);
+  REQUIRE(aligned(p, 4), SA_ERR_INVALID_ARG, "%s: %s must be 4-byte aligned", fn, name);
   return SA_OK;
 }
 

@@ -237,6 +237,16 @@ def test_strides():
         check(xf, None, wq, sw, dt)
 
 
+@pytest.mark.parametrize("t", [2, 9, 90])
+def test_rows_of_a_larger_batch(t):
+    """Some rows of quantised activations, with their scales: rows 3 on start at
+    no multiple of 16 bytes of scales."""
+    wq, sw = codes((1033, 64), 1)[1:], scales(1033, 2)[1:]
+    q, s = sa.act_quantize_int8(rows_of((t + 3, 64), torch.bfloat16, 3))
+    whole = sa.int8_linear(q, wq, sw, sx=s, dtype=torch.bfloat16)
+    assert torch.equal(sa.int8_linear(q[3:], wq, sw, sx=s[3:], dtype=torch.bfloat16), whole[3:])
+
+
 def test_vectors_and_empty():
     wq, sw = codes((40, 64), 1), scales(40, 2)
     x = rows_of((64,), torch.bfloat16, 3)

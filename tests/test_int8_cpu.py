@@ -68,7 +68,7 @@ def linear(sa, dtype=0, x=P, ldx=64, sx=6 * P, T=3, wq=2 * P, ldw=64, sw=3 * P, 
     (dict(dtype=2), INVALID), (dict(T=-1), INVALID), (dict(T=(1 << 22) + 1), UNSUPPORTED), (dict(d=56), INVALID),
     (dict(d=0), INVALID), (dict(d=131088, ldx=131088, ldq=131088), UNSUPPORTED), (dict(x=None), INVALID),
     (dict(xq=None), INVALID), (dict(sx=None), INVALID), (dict(x=P + 8), INVALID), (dict(xq=P + 8), INVALID),
-    (dict(sx=P + 8), INVALID), (dict(ldx=56), INVALID), (dict(ldq=48), INVALID), (dict(ldq=72), INVALID),
+    (dict(sx=3 * P + 2), INVALID), (dict(ldx=56), INVALID), (dict(ldq=48), INVALID), (dict(ldq=72), INVALID),
     (dict(ldq=1 << 22), UNSUPPORTED), (dict(xq=P), INVALID), (dict(sx=P), INVALID), (dict(sx=2 * P), INVALID)])
 def test_token_refusals(sa, bad, status):
     assert tokens(sa, **bad) == status
@@ -90,7 +90,7 @@ def test_channel_refusals(sa, bad, status):
     (dict(dtype=2), INVALID), (dict(act=6), INVALID), (dict(T=-1), INVALID), (dict(d_in=72), INVALID),
     (dict(d_out=36), INVALID), (dict(d_in=131088, ldx=131088, ldw=131088), UNSUPPORTED), (dict(x=None), INVALID),
     (dict(wq=None), INVALID), (dict(sw=None), INVALID), (dict(y=None), INVALID), (dict(ldx=72), INVALID),
-    (dict(ldw=48), INVALID), (dict(sx=6 * P + 4), INVALID), (dict(x=P + 8), INVALID), (dict(bias=P + 8), INVALID),
+    (dict(ldw=48), INVALID), (dict(sx=6 * P + 2), INVALID), (dict(x=P + 8), INVALID), (dict(bias=P + 8), INVALID),
     (dict(res=7 * P, ldr=32), INVALID), (dict(y=P), INVALID), (dict(y=2 * P), INVALID), (dict(y=3 * P), INVALID),
     (dict(y=6 * P), INVALID), (dict(bias=5 * P), INVALID), (dict(sx=None, ldx=60), INVALID)])
 def test_linear_refusals(sa, bad, status):
