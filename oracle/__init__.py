@@ -30,6 +30,9 @@ Modules:
 * ``correct``   weight-aware selection, static shift, variance correction
 * ``spmm``      batched N:M activation-sparse matmul (per-token and tile-shared)
 * ``calibrate`` empirical-quantile thresholds
+* ``linear``    dense linear layers, gated projections, their gradients
+* ``grouped``   the same, grouped by expert
+* ``int8``      8-bit codes and scales, products of codes
 * ``brute``     exhaustive enumeration for tiny inputs
 
 Every function is pinned by ``tests/test_oracle_*.py`` (run with

@@ -7,6 +7,13 @@
 // expert without rows: its gradient is written as zeros).  The elementwise
 // half and its scales are the dense layers' (linear.hip), on strips of
 // rows that end with their expert: column sums and scales are the expert's.
+//
+// What bounds it, measured on MI355X: gate and up 4096 -> 11008 of 8 experts, 4096
+// rows, bf16, 1680-1750 us: elementwise 115, dx 730, dW 900.  dW writes 1.44 GB of
+// gradients (4.65 TB/s) and its products wait for the stores; non-temporal stores,
+// another order over the dies, staggered starts and later waits gave nothing.  16
+// experts 1024 -> 4096, 509 rows, fp16, 91-100 us: five launches, dx 40, dW 35 (one
+// launch for both took as long).
 #include "grouped_launch.hpp"
 
 namespace sa {

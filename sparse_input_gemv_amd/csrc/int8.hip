@@ -29,7 +29,6 @@
 namespace sa {
 namespace {
 
-typedef int i2v __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // ---- rounding to 8 bits ------------------------------------------------------------
