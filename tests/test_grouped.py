@@ -243,6 +243,41 @@ def test_offsets_of_any_values(offsets):
         assert (out[:clean[0]] == 9).all() and (out[clean[-1]:] == 9).all()
 
 
+def test_offsets_past_32_bits():
+    """Experts' matrices, and rows, whose last lie past 2^31 entries."""
+    counts, d_in, d_out, dt = [20, 0, 70], 72, 136, torch.bfloat16
+    t, step = sum(counts), 9 << 27
+    o = offsets_of(counts)
+    x, dy = ints((t, d_in), -2, 2, dt, 1), ints((t, d_out), -2, 2, dt, 2)
+    wt = ints((len(counts), d_in, d_out), -2, 2, dt, 3)
+    apart = lambda: torch.empty(2 * step + d_in * d_out, dtype=dt, device=DEV).as_strided(  # noqa: E731
+        wt.shape, (step, d_out, 1))
+    far = apart().copy_(wt)
+    assert torch.equal(sa.grouped_linear(x, far, o), sa.grouped_linear(x, wt, o))
+    assert torch.equal(sa.grouped_gated_linear(x, wt, far, o), sa.grouped_gated_linear(x, wt, wt, o))
+    dx, dwt, _ = sa.grouped_linear_backward(dy, x, wt, o)
+    fx, fwt, _ = sa.grouped_linear_backward(dy, x, far, o, dwt=apart())
+    assert torch.equal(fx, dx) and torch.equal(fwt, dwt)
+    del far, fwt
+
+    counts, d_in, d_out = [70000, 1, 0, 70000], 8, 16384
+    t, o = sum(counts), offsets_of(counts)
+    x, wt = ints((t, d_in), -2, 2, dt, 4), ints((len(counts), d_in, d_out), -2, 2, dt, 5)
+    y = sa.grouped_linear(x, wt, o)
+    assert y.numel() > 2**31
+    ends = [(0, slice(0, 300)), (1, slice(70000, 70001)), (3, slice(t - 300, t))]
+    for e, r in ends:
+        same(y[r], x[r].double() @ wt[e].double())
+    y.clamp_(-1, 1)
+    dx, dwt, db = sa.grouped_linear_backward(y, x, wt, o, with_dbias=True)
+    for e, r in ends:
+        same(dx[r], y[r].double() @ wt[e].double().T)
+    for e, rows in by_expert(counts):
+        parts = [slice(i, min(i + 20000, rows.stop)) for i in range(rows.start, rows.stop, 20000)]
+        same(dwt[e], sum(x[r].double().T @ y[r].double() for r in parts))  # sums below 2^24
+        same(db[e], sum(y[r].double().sum(0) for r in parts))
+
+
 def test_empty():
     off = torch.zeros(4, dtype=torch.int32, device=DEV)
     x = torch.empty(0, 64, dtype=torch.float16, device=DEV)

@@ -247,6 +247,25 @@ def test_rows_of_a_larger_batch(t):
     assert torch.equal(sa.int8_linear(q[3:], wq, sw, sx=s[3:], dtype=torch.bfloat16), whole[3:])
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^21 entries apart: the last of 1104 lie past 2^31."""
+    n, d, ld = 1104, 64, 1 << 21
+    far = lambda v: torch.empty(n, ld, dtype=v.dtype, device=DEV)[:, :v.shape[1]].copy_(v)  # noqa: E731
+    x = rows_of((n, d), torch.bfloat16, 5)
+    q, s = sa.act_quantize_int8(x)
+    fq, fs = sa.act_quantize_int8(far(x), xq=far(torch.zeros_like(q)))
+    assert torch.equal(fq, q) and torch.equal(fs, s)
+    cq, cs = sa.weight_quantize_int8(x[:, :48].contiguous()[:1088])
+    fq, fs = sa.weight_quantize_int8(far(x)[:1088, :48])
+    assert torch.equal(fq, cq) and torch.equal(fs, cs)
+    del fq
+    wq, sw = codes((n, d), 6), scales(n, 7)
+    fw, fx = far(wq), far(q)
+    for t in (1, 4, 8, 40, n):  # a kernel each, and the tiles with rows far apart
+        want = sa.int8_linear(q[-t:], wq, sw, sx=s[-t:], dtype=torch.bfloat16)
+        assert torch.equal(sa.int8_linear(fx[-t:], fw, sw, sx=s[-t:], dtype=torch.bfloat16), want)
+
+
 def test_vectors_and_empty():
     wq, sw = codes((40, 64), 1), scales(40, 2)
     x = rows_of((64,), torch.bfloat16, 3)
