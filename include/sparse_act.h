@@ -618,9 +618,10 @@ size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_
  * calls below:
  * - `dtype` (SA_F16 or SA_BF16) is the type of the 16-bit matrices and of bias.
  *   Their strides, alignment and overlap are the dense layers'.
- * - Codes are int8, in -127 .. 127 where the quantisers wrote them; a matrix of
- *   them has a row stride in elements, a multiple of 16, at least the row
- *   length, at most 2^21, and is 16-byte aligned.  Scales are fp32.
+ * - Codes are int8, in -127 .. 127 where the quantisers wrote them, of any value
+ *   in a product; a matrix of them has a row stride in elements, a multiple of
+ *   16, at least the row length, at most 2^21, and is 16-byte aligned.  Scales
+ *   are fp32.
  * - Codes of a row (or channel) with largest magnitude m: the scale s is the
  *   fp32 quotient m / 127, a code the exact quotient x / s rounded to the
  *   nearest integer, halves to even.  m = 0 gives s = 0 and codes 0; Inf or

@@ -25,6 +25,7 @@
 // 32-bit sums written: 2261 with both operands k-contiguous, 2002 else).
 #define SA_LINEAR_ENGINE_ONLY
 #include "linear.hip"
+#include "validate.hpp"
 
 namespace sa {
 namespace {
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(256) void k_int8_gemv(GemvP p) {
     const int t = i % NT, n = c0 + i / NT;
     if (t >= p.T) continue;
     const int sum = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
-    float f = (float)sum * p.sw[n] * (QUANT ? s : p.sx[t]);
+    float f = scaled_sum<false>(sum, p.sw[n], QUANT ? s : p.sx[t]);
     if (p.bias) f += to_f<DT>(p.bias[n]);
     with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
     if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
@@ -485,10 +486,10 @@ __global__ __launch_bounds__(kRowsWaves * 64) void k_int8_rows(GemvP p) {
   for (int o = tid; o < RB * 256; o += kRowsWaves * 64) {
     const int t = o / 16, n = c0 + o % 16;
     if (t >= p.T || n >= p.N) continue;
-    int total = 0;
+    uint32_t total = 0;  // (int: 2^31 would overflow)
 #pragma unroll
-    for (int j = 0; j < kRowsWaves; ++j) total += S[j][o];
-    float f = (float)total * p.sw[n] * p.sx[t];
+    for (int j = 0; j < kRowsWaves; ++j) total += (uint32_t)S[j][o];
+    float f = scaled_sum<true>((int)total, p.sw[n], p.sx[t]);
     if (p.bias) f += to_f<DT>(p.bias[n]);
     with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
     if (p.res) f += to_f<DT>(p.res[t * p.ldr + n]);
@@ -511,10 +512,10 @@ hipError_t rows(const GemvP& p, hipStream_t s) {
 }
 
 // ---- matrix instructions ----------------------------------------------------------------
-template <int DT, int BM, int BN, int WM, int WN, int NS>
+template <int DT, int EPI, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(256, 1) void k_int8(Int8P p) {
   __shared__ __align__(16) uint8_t S[lin_lds<kDx, BM, BN, NS>()];
-  lin_run<DT, kDx, false, kInt8, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S);
+  lin_run<DT, kDx, false, EPI, BM, BN, WM, WN, NS>(p, blockIdx.x, gridDim.x, S);
 }
 // Adds the shares' integer partials of 4 columns of a row and finishes them.
 template <int DT>
@@ -527,16 +528,16 @@ __global__ __launch_bounds__(256) void k_int8_reduce(Int8P p, int lbm, int lbn) 
   const uint32_t steps = (uint32_t)((p.K + BK - 1) / BK), TS = mt * nt * steps;
   const uint32_t at = (uint32_t)((n >> lbn) * mt + (int)(m >> lbm)) * steps;
   const int slots = share_of(at + steps - 1, TS, p.split) - share_of(at, TS, p.split) + 1;
-  const i4v* q = reinterpret_cast<const i4v*>(p.part + (int64_t)m * p.N + n);
+  const u32x4* q = reinterpret_cast<const u32x4*>(p.part + (int64_t)m * p.N + n);
   const int64_t slot = (int64_t)p.M * p.N / 4;
-  i4v sum = {0, 0, 0, 0};
+  u32x4 sum = {0, 0, 0, 0};
 #pragma unroll 8
   for (int s = 0; s < slots; ++s) sum += q[s * slot];
   const float sx = p.sx[m];
   uint16_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float f = (float)sum[i] * p.sw[n + i] * sx;
+    float f = scaled_sum<true>((int)sum[i], p.sw[n + i], sx);
     if (p.bias) f += to_f<DT>(p.bias[n + i]);
     with_act(p.act, [&](auto A) { f = act_value<decltype(A)::value>(f); });
     if (p.res) f += to_f<DT>(p.res[m * (int64_t)p.ldr + n + i]);
@@ -574,8 +575,11 @@ hipError_t matmul(Int8P p, void* ws, hipStream_t s) {
   auto run = [&](auto bm, auto bn, auto wm, auto ns) {
     constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, WM = decltype(wm)::value, NS = decltype(ns)::value;
     constexpr int64_t most = kCus * (160 * 1024 / lin_lds<kDx, BM, BN, NS>());
-    hipLaunchKernelGGL((k_int8<DT, BM, BN, WM, 4 / WM, NS>), dim3((unsigned)(p.split || items < most ? items : most)),
-                       dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(p.split || items < most ? items : most));
+    if (p.K * 2 == kMaxInt8Dim && !p.split)  // shares are added in k_int8_reduce
+      hipLaunchKernelGGL((k_int8<DT, kInt8Long, BM, BN, WM, 4 / WM, NS>), grid, dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_int8<DT, kInt8, BM, BN, WM, 4 / WM, NS>), grid, dim3(256), 0, s, p);
   };
   using std::integral_constant;
   const integral_constant<int, 1> c1;

@@ -256,8 +256,10 @@ enum Layout { kFwd = 0, kDx = 1, kDw = 2 };
 // h alone), plus the residual, or everything; for fp16 gradients, the sums
 // times their row's (dx) or column's (dW) power of two; for 8-bit integers,
 // everything but the pre-activation, of the sums times their row's and
-// column's scale.
-enum Epilogue { kPlain = 0, kResidual = 1, kGeneral = 2, kScaled = 3, kInt8 = 4 };
+// column's scale (kInt8Long: sums of 2^17 products, one of which may wrap; a
+// branch for them in the common kernel took 1.5 to 5 percent of 1000 to 8192
+// tokens' time).
+enum Epilogue { kPlain = 0, kResidual = 1, kGeneral = 2, kScaled = 3, kInt8 = 4, kInt8Long = 5 };
 
 struct LinP {
   const uint16_t* p[2];  // row operand (per K segment)
@@ -289,6 +291,14 @@ struct LinP {
 struct Int8P : LinP {
   const float *sx, *sw;  // [M], [N]
 };
+// A sum of products of codes, scaled.  WRAP: it may be of 2^17 products; the
+// largest of those, of -128 by -128, is 2^31, which 32 bits wrap to -2^31, and no
+// other sum is below -127 128 2^17.
+template <bool WRAP>
+__device__ __forceinline__ float scaled_sum(int sum, float sw, float sx) {
+  const float f = WRAP && sum == (int)0x80000000 ? 0x1p31f : (float)sum;
+  return f * sw * sx;
+}
 // By expert: rows offsets[e] .. offsets[e + 1] - 1 of the T rows meet expert
 // e's matrix.  Forward and dx: q is expert 0's, sq to the next; bias [E][N].
 // dW: K is the expert's rows; y is expert 0's, sy to the next; cs [E][outs][N].
@@ -666,7 +676,7 @@ template <int DT, int LAY, bool GATED, int EPI, int BM, int BN, int WM, int WN, 
 __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8_t* S,
                                         const GroupTab* tab = nullptr) {
   constexpr bool GRP = std::is_same<P, GroupP>::value, I8 = std::is_same<P, Int8P>::value;
-  static_assert(I8 == (EPI == kInt8) && (!I8 || (LAY == kDx && !GATED)), "8-bit operands have k contiguous");
+  static_assert(I8 == (EPI == kInt8 || EPI == kInt8Long) && (!I8 || (LAY == kDx && !GATED)), "8-bit operands have k contiguous");
   constexpr bool PNC = LAY == kDw, QNC = LAY != kDx;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;
   static_assert(WM * WN == 4 && MB >= 1 && NB >= 2 && NB % (GATED ? 4 : 2) == 0, "four waves");
@@ -1266,8 +1276,8 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
         }
       });
     } else {
-      constexpr bool residual = mode == kResidual || mode == kGeneral || mode == kInt8;
-      constexpr bool general = mode == kGeneral || mode == kInt8;
+      constexpr bool residual = mode == kResidual || mode == kGeneral || I8;
+      constexpr bool general = mode == kGeneral || I8;
       const bool hr = residual && p.res, hp = mode == kGeneral && p.pre[0], hb = general && p.bias;
       const auto rr = rows_rsrc(hr ? p.res : p.y[0], hr ? p.ldr : 0, it.m0, hr ? rows : 1, hr ? p.N : 0);
       const auto pr = rows_rsrc(hp ? p.pre[0] : p.y[0], hp ? p.ldpre[0] : 0, it.m0, hp ? rows : 1, hp ? p.N : 0);
@@ -1367,7 +1377,8 @@ __device__ __forceinline__ void lin_run(const P& p, int block, int blocks, uint8
             if constexpr (I8) {
               const F8 sw = columns(col_scale, b);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f.v[e] = (float)__builtin_bit_cast(int, f.v[e]) * sw.v[e] * rsv[a];
+              for (int e = 0; e < 8; ++e)
+                f.v[e] = scaled_sum<EPI == kInt8Long>(__builtin_bit_cast(int, f.v[e]), sw.v[e], rsv[a]);
             }
             if constexpr (general) {
               const F8 bias = kCols ? columns(col_bias, b) : widen8<DT>(bv[b / 2]);

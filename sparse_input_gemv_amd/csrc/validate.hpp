@@ -63,7 +63,7 @@ int check_linear_distinct(const char* fn, const char* out, const void* o, const 
 int check_linear_both(const char* fn, const char* a, const void* pa, const char* b,
                       const void* pb);
 // 8-bit integers: sizes, and a matrix of codes (rows in 16-byte chunks).
-constexpr int64_t kMaxInt8Dim = (int64_t)1 << 17;  // d_in: 127^2 of them stay below 2^31
+constexpr int64_t kMaxInt8Dim = (int64_t)1 << 17;  // d_in: 128^2 of them are 2^31, the one sum past 32 bits
 int check_int8_sizes(const char* fn, int dtype, int64_t T, int64_t d_in, int64_t d_out, int act);
 int check_int8_codes(const char* fn, const char* name, const void* p, int64_t ld, int64_t len, bool optional);
 int check_scales(const char* fn, const char* name, const void* p, bool optional);

@@ -1,0 +1,28 @@
+"""Linear layers in 8-bit integers at the ends of their ranges: codes, scales
+and sizes that the calls accept and ordinary layers do not reach."""
+
+import pytest
+import torch
+
+from test_int8 import check, codes, rows_of
+from test_linear import DEV
+from test_linear import tuning  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+# tokens, tile, split: 16 channels per workgroup, then every tile whole and shared
+KERNELS = [(1, -1, -1), (40, -1, -1), (70, -1, -1)] + [(300, tile, split) for tile in range(6) for split in (0, 64)]
+
+
+@pytest.mark.parametrize("t, tile, split", KERNELS)
+def test_sums_of_two_to_the_31(tuning, t, tile, split):  # noqa: F811
+    """Codes of -128 in both operands of the longest sum: 2^17 products of 2^14
+    are 2^31, which 32 bits hold as -2^31 alone."""
+    tuning(tile, split)
+    d_in, d_out = 131072, 136
+    x, wq = codes((t, d_in), 1), codes((d_out, d_in), 2)
+    x[t // 2], x[0], x[t - 1] = 127, -128, -128
+    wq[0], wq[1], wq[2], wq[d_out - 1] = -128, 127, 0, -128
+    one = torch.ones(t, device=DEV)
+    for bias in (None, rows_of((d_out,), torch.bfloat16, 3)):
+        y = check(x, one, wq, torch.full((d_out,), 2.0**-8, device=DEV), torch.bfloat16, bias=bias)
+    assert (y[t - 1, [0, d_out - 1]] > 0).all() and (y[t - 1, 1] < 0)
