@@ -162,9 +162,14 @@ template <int DT>
 void quant_rows(const uint16_t* x, int64_t ldx, int64_t T, int64_t d, int8_t* xq, int64_t ldq, float* sx,
                 hipStream_t s) {
   auto run = [&](auto nt, auto nv) {
-    constexpr int NT = decltype(nt)::value;
-    hipLaunchKernelGGL((k_quant_rows<DT, NT, decltype(nv)::value>), dim3((unsigned)(NT > 64 ? T : (T + 3) / 4)),
-                       dim3(NT > 64 ? NT : 256), 0, s, x, ldx, T, (int)d, xq, ldq, sx);
+    constexpr int NT = decltype(nt)::value, threads = NT > 64 ? NT : 256, rows = NT > 64 ? 1 : 4;
+    // a launch counts its threads in 32 bits: 2^22 rows of 1024 threads are one too many
+    constexpr int64_t most = (int64_t)0xffffffff / threads * rows;
+    for (int64_t t = 0; t < T; t += most) {
+      const int64_t n = T - t < most ? T - t : most;
+      hipLaunchKernelGGL((k_quant_rows<DT, NT, decltype(nv)::value>), dim3((unsigned)((n + rows - 1) / rows)),
+                         dim3(threads), 0, s, x + t * ldx, ldx, n, (int)d, xq + t * ldq, ldq, sx + t);
+    }
   };
   using std::integral_constant;
   const integral_constant<int, 64> wave;

@@ -4,6 +4,7 @@ and sizes that the calls accept and ordinary layers do not reach."""
 import pytest
 import torch
 
+import sparse_input_gemv_amd as sa
 from test_int8 import check, codes, rows_of
 from test_linear import DEV
 from test_linear import tuning  # noqa: F401
@@ -26,3 +27,23 @@ def test_sums_of_two_to_the_31(tuning, t, tile, split):  # noqa: F811
     for bias in (None, rows_of((d_out,), torch.bfloat16, 3)):
         y = check(x, one, wq, torch.full((d_out,), 2.0**-8, device=DEV), torch.bfloat16, bias=bias)
     assert (y[t - 1, [0, d_out - 1]] > 0).all() and (y[t - 1, 1] < 0)
+
+
+def test_the_most_rows_of_1024_threads():
+    """2^22 rows of over 16384 values, 1024 threads each: 2^32 threads, which no
+    single launch has.  206 GB; only the rows that are compared are written."""
+    T, d = 1 << 22, 16400
+    if torch.cuda.mem_get_info()[0] < 3 * T * d + (8 << 30):
+        torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 3 * T * d + (8 << 30):
+        pytest.skip("needs 215 GB of the GPU's memory")
+    x = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    parts = [slice(0, 3), slice(T // 2 - 2, T // 2 + 2), slice(T - 3, T)]
+    for k, r in enumerate(parts):
+        x[r] = rows_of((r.stop - r.start, d), torch.bfloat16, k)
+    q, s = sa.act_quantize_int8(x)
+    for r in parts:
+        wq, ws = sa.act_quantize_int8(x[r])
+        assert torch.equal(q[r], wq) and torch.equal(s[r], ws)
+    del x, q, s
+    torch.cuda.empty_cache()
