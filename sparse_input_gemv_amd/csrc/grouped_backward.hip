@@ -51,23 +51,25 @@ __global__ __launch_bounds__(256) void k_grp_dact(GrpDactP p, int lg) {
   dact_strip<DT, GATED, SCALING>(p, s0, send, strip, cs, part);
 }
 
-// As k_lin_scales: workgroups 0 .. cblocks * E - 1 take 64 of an expert's C
-// columns, the others a row of any expert per wave.
+// As k_lin_scales: the first `groups` workgroups take 64 of an expert's C columns
+// at a time, the others a row of any expert per wave.
 template <bool SUMS>
-__global__ __launch_bounds__(256) void k_grp_scales(GrpDactP p, int lg, int64_t C, int cblocks, int blocks,
-                                                    uint16_t* dbias) {
+__global__ __launch_bounds__(256) void k_grp_scales(GrpDactP p, int lg, int64_t C, int cblocks, int groups,
+                                                    int blocks, uint16_t* dbias) {
   __shared__ float part[4][64], most[4][64];
   __shared__ GroupTab tab;
   group_table(p.offsets, p.E, (int)p.T, lg, 1, tab);
   bool scaled = false;
-  const int columns = cblocks * p.E;
-  if ((int)blockIdx.x < columns) {
-    const int e = (int)blockIdx.x / cblocks, b = (int)blockIdx.x - e * cblocks;
-    scaled = scale_columns<SUMS>(p, tab.first[e], tab.first[e + 1], C, (int64_t)b * 64,
-                                 p.cs ? p.cs + e * C : nullptr, SUMS ? dbias + e * C : nullptr, part, most);
+  if ((int)blockIdx.x < groups) {
+    for (int i = (int)blockIdx.x; i < cblocks * p.E; i += groups) {
+      const int e = i / cblocks, b = i - e * cblocks;
+      if (i >= groups) __syncthreads();  // the columns before are read
+      scaled |= scale_columns<SUMS>(p, tab.first[e], tab.first[e + 1], C, (int64_t)b * 64,
+                                    p.cs ? p.cs + e * C : nullptr, SUMS ? dbias + e * C : nullptr, part, most);
+    }
   } else {
-    const int64_t step = 4 * (int64_t)((int)gridDim.x - columns);
-    const int64_t t0 = tab.row[0] + 4 * (int64_t)((int)blockIdx.x - columns) + (int)threadIdx.x / kWave;
+    const int64_t step = 4 * (int64_t)((int)gridDim.x - groups);
+    const int64_t t0 = tab.row[0] + 4 * (int64_t)((int)blockIdx.x - groups) + (int)threadIdx.x / kWave;
     for (int64_t t = t0; t < tab.row[p.E]; t += step) scaled |= scale_row(p, t, blocks);
   }
   // read by later launches only: a store that may stay in this XCD's L2
@@ -186,11 +188,13 @@ hipError_t bwd_dt(const GroupedCall& c, hipStream_t s) {
         const int64_t C = outs * c.d_out;
         const int cblocks = a.cs || c.dbias ? (int)((C + 63) / 64) : 0;
         const int64_t rows = c.dx ? (c.T + 3) / 4 : 0;
-        const int64_t grid = cblocks * c.experts + (rows < 1024 ? rows : 1024);
-        if (grid > 0x7fffffffLL) return hipErrorNotSupported;
-        const dim3 gs((unsigned)grid);
-        if (c.dbias) hipLaunchKernelGGL((k_grp_scales<true>), gs, dim3(256), 0, s, a, lg, C, cblocks, (int)gr.x, c.dbias);
-        else hipLaunchKernelGGL((k_grp_scales<false>), gs, dim3(256), 0, s, a, lg, C, cblocks, (int)gr.x, c.dbias);
+        // one block of columns each, but for wide outputs of many experts: a launch
+        // holds fewer than 2^24 workgroups of 256 threads
+        const int64_t columns = cblocks * c.experts;
+        const int groups = columns < (1 << 23) ? (int)columns : 1 << 23;
+        const dim3 gs((unsigned)(groups + (rows < 1024 ? rows : 1024)));
+        if (c.dbias) hipLaunchKernelGGL((k_grp_scales<true>), gs, dim3(256), 0, s, a, lg, C, cblocks, groups, (int)gr.x, c.dbias);
+        else hipLaunchKernelGGL((k_grp_scales<false>), gs, dim3(256), 0, s, a, lg, C, cblocks, groups, (int)gr.x, c.dbias);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (c.gated) hipLaunchKernelGGL((k_grp_dact<DT, true, kApply>), gr, dim3(256), 0, s, a, lg);
