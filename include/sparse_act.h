@@ -898,7 +898,7 @@ int sa_grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_
  * or 16 rows x 128, 256 x 192; weight gradients take 0, 1 and 5 only, gated
  * products not 5, and 5 is never split); split -1 =
  * automatic, 0 = whole tiles, or that many shares (up to 512, rounded down to
- * a power of two).  The layers grouped by expert follow them too (their
+ * a power of two; a product of 2^33 outputs or more is not split).  The layers grouped by expert follow them too (their
  * weight gradients take tile 0 or 1 and no split, no product a split of tile
  * 0; tile 5 counts as -1).  Workspace
  * sizes follow the choices: query them again.  Every choice computes the

@@ -604,7 +604,6 @@ hipError_t matmul(Int8P p, void* ws, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !pl.split) return e;
   const int64_t n = ((int64_t)p.M * (p.N / 4) + 255) / 256;
-  if (n > 0x7fffffffLL) return hipErrorNotSupported;
   hipLaunchKernelGGL((k_int8_reduce<DT>), dim3((unsigned)n), dim3(256), 0, s, p,
                      __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(kTileN[pl.tile]));
   return hipGetLastError();

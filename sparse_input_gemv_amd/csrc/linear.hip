@@ -1741,6 +1741,9 @@ struct Plan {
   int tile, split;  // split: shares, 0 for whole tiles
   int64_t tiles;
 };
+// Outputs of a split product: the reduction's threads, one for 4 outputs or
+// more, are counted in 32 bits.  (Automatic splits have 2^24 at most.)
+constexpr int64_t kSplitMost = (int64_t)1 << 33;
 
 inline int64_t tiles_of(int tile, bool gated, int64_t M, int64_t N, int64_t outs) {
   const int64_t bn = gated ? 128 : kTileN[tile];
@@ -1812,6 +1815,7 @@ inline Plan lin_plan(int lay, bool gated, int64_t M, int64_t N, int64_t K, int s
     if (shares < 64) shares = TS < 64 ? TS : 64;
     if (tuned_split > 0) shares = tuned_split < tiles * steps ? tuned_split : tiles * steps;
     if (tuned_split == 0 || t == kNarrow || shares < 1 || tiles * steps >= (1 << 22)) continue;
+    if (M * N * outs >= kSplitMost) continue;
     while (shares & (shares - 1)) shares &= shares - 1;  // a power of two
     if (tuned_split < 0 && (tiles >= shares || steps < 2)) continue;
     const double rows = M < kTileM[t] ? M : kTileM[t];
@@ -1985,7 +1989,6 @@ hipError_t launch_reduce(const LinP& p, const Plan& pl, hipStream_t s) {
   // a thread per chain while that is less than a workgroup per CU
   const int groups = octets * kChains <= kCus * 256 ? kChains : 1;
   const int64_t n = (octets * groups + 255) / 256;
-  if (n > 0x7fffffffLL) return hipErrorNotSupported;
   hipLaunchKernelGGL((k_lin_reduce<DT, GATED>), dim3((unsigned)n), dim3(256), 0, s, p, groups,
                      __builtin_ctz(kTileM[pl.tile]), __builtin_ctz(GATED ? 128 : kTileN[pl.tile]));
   return hipGetLastError();
