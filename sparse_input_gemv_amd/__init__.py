@@ -948,6 +948,13 @@ def _codes_out(q, s, names, device, rows: int, cols: int):
     return q, _codes(q, names[0], device, rows, cols), s
 
 
+def _no_gradient(fn: str, what: str, *inputs) -> None:
+    """Warns where autograd would expect a graph and there is no gradient to call."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        warnings.warn(f"{fn} is outside autograd and has no gradient: {what} no graph. "
+                      "Call it under torch.no_grad().", stacklevel=3)
+
+
 class _Like:
     """The type and device of outputs that no input has."""
 
@@ -962,7 +969,8 @@ def act_quantize_int8(x: torch.Tensor, xq: torch.Tensor | None = None, sx: torch
     ``sx = max|x| / 127`` (fp32) and ``xq`` the exact quotient ``x / sx`` rounded
     to the nearest integer, halves to even.  A row of zeros has scale 0; one
     with Inf or NaN has scale NaN and codes 0.  A vector is one row: ``xq`` is
-    a vector then, ``sx`` holds one scale."""
+    a vector then, ``sx`` holds one scale.  Outside autograd, without a gradient:
+    an ``x`` that requires grad brings a warning unless grad mode is off."""
     squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
     x = _lin_x(x, "x")
     T, d = x.shape
@@ -970,6 +978,7 @@ def act_quantize_int8(x: torch.Tensor, xq: torch.Tensor | None = None, sx: torch
     if squeeze and xq is not None and xq.dim() == 1:
         xq = xq[None]
     xq, ldq, sx = _codes_out(xq, sx, ("xq", "sx"), x.device, T, d)
+    _no_gradient("act_quantize_int8", "its codes and scales carry", x)
     _lin_call("act_quantize_int8", x, None, _LIN_DTYPES[x.dtype], x.data_ptr(), ldx, T, d, xq.data_ptr(),
               ldq, sx.data_ptr())
     return _ret(xq, squeeze), sx
@@ -978,11 +987,13 @@ def act_quantize_int8(x: torch.Tensor, xq: torch.Tensor | None = None, sx: torch
 def weight_quantize_int8(wt: torch.Tensor, wq: torch.Tensor | None = None, sw: torch.Tensor | None = None):
     """8-bit codes and a scale per output channel of ``wt[d_in][d_out]``, for
     ``int8_linear``: ``(wq, sw)`` with ``wq[d_out][d_in]`` (the weight itself, not
-    its transpose).  Rounded as ``act_quantize_int8`` rounds rows."""
+    its transpose).  Rounded as ``act_quantize_int8`` rounds rows, and outside
+    autograd like it."""
     wt = _lin_x(wt, "wt")
     d_in, d_out = wt.shape
     ldw = _lin_mat(wt, "wt", wt, d_in, d_out)
     wq, ldq, sw = _codes_out(wq, sw, ("wq", "sw"), wt.device, d_out, d_in)
+    _no_gradient("weight_quantize_int8", "its codes and scales carry", wt)
     _lin_call("weight_quantize_int8", wt, (d_in, d_out), _LIN_DTYPES[wt.dtype], wt.data_ptr(), ldw, d_in,
               d_out, wq.data_ptr(), ldq, sw.data_ptr())
     return wq, sw
@@ -1026,9 +1037,7 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, sx: torch.T
         _lin_vec(bias, "bias", like, d_out)
     ldr = 0 if residual is None else _lin_mat(residual, "residual", like, T, d_out)
     y, ldy = _lin_out(y, "y", like, T, d_out)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, bias, residual)):
-        warnings.warn("int8_linear is outside autograd and has no gradient: its output carries no graph. "
-                      "Call it under torch.no_grad().", stacklevel=2)
+    _no_gradient("int8_linear", "its output carries", x, sx, sw, bias, residual)
     _lin_call("int8_linear", x, (T, d_in, d_out, int(sx is not None)), _LIN_DTYPES[dtype], x.data_ptr(),
               ldx, _ptr(sx), T, wq.data_ptr(), ldw, sw.data_ptr(), d_in, d_out, _ptr(bias), _act(act),
               _ptr(residual), ldr, y.data_ptr(), ldy)
