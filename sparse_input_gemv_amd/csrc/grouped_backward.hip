@@ -103,7 +103,7 @@ hipError_t launch_dw(const GroupP& p, hipStream_t s) {
   const double steps = (double)p.T / p.E / BK;
   const double tb = ((big + kCus - 1) / kCus) * (steps * 1.45 + 7.2);
   const double ts = ((small + 2 * kCus - 1) / (2 * kCus)) * (steps * (small > kCus ? 1.0 : 0.6) + 3.6);
-  if (tile >= 0 ? tile == 0 : tb <= ts) grp_tile<DT, kDw, false, EPI, 256, 256, 2, 2, 2>(p, big, s);
+  if (tile == 0 || (tile != 1 && tb <= ts)) grp_tile<DT, kDw, false, EPI, 256, 256, 2, 2, 2>(p, big, s);
   else grp_tile<DT, kDw, false, EPI, 128, 128, 2, 2, 2>(p, small, s);
   return hipGetLastError();
 }

@@ -7,6 +7,7 @@ import torch
 import sparse_input_gemv_amd as sa
 from test_grouped import by_expert, offsets_of
 from test_linear import DEV, ints, same
+from test_linear import tuning  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,27 @@ def test_the_most_columns_of_the_most_experts(with_dbias):
         at[e] = False
     for e in at.nonzero()[:, 0].tolist():
         assert not dwt[e].any() and (db is None or not db[e].any())
+
+
+def kernels_of(call):
+    """Names of the kernels that a call launches."""
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        call()
+        torch.cuda.synchronize()
+    return [e.name for e in p.events() if "k_grp<" in e.name]
+
+
+def test_weight_gradients_follow_their_own_tiles(tuning):  # noqa: F811
+    """Choices that weight gradients do not have (64 rows and fewer, 256 x 192)
+    leave their tile automatic: 256 x 256 for many rows of few experts, else 128
+    x 128."""
+    dt, wanted = torch.bfloat16, {-1: (256, 128), 0: (256, 256), 1: (128, 128), 2: (256, 128), 5: (256, 128)}
+    for k, (t, d) in enumerate(((4096, 4096), (64, 256))):
+        x, dy, wt = ints((t, d), -2, 2, dt, 1), ints((t, d), -1, 1, dt, 2), ints((1, d, d), -2, 2, dt, 3)
+        off, want = offsets_of([t]), x.double().T @ dy.double()
+        for tile, rows in wanted.items():
+            tuning(tile)
+            out = []
+            names = kernels_of(lambda: out.append(sa.grouped_linear_backward(dy, x, wt, off, with_dx=False)[1]))
+            assert len(names) == 1 and f"{rows[k]}, {rows[k]}, 2, 2, 2>" in names[0], (tile, names)
+            same(out[0][0], want)
