@@ -47,7 +47,7 @@ hipError_t fwd_dt(const GroupedCall& c, hipStream_t s) {
 }  // namespace
 
 size_t grouped_workspace_bytes(bool gated, int64_t T, int64_t experts, int64_t d_in, int64_t d_out) {
-  return T ? grp_part_bytes(grp_plan(kFwd, gated, T, experts, d_out, d_in, 1), gated) : 0;
+  return T ? grp_part_bytes(grp_plan(gated, T, experts, d_out, d_in, 1), gated) : 0;
 }
 
 hipError_t launch_grouped(const GroupedCall& c, hipStream_t s) {
@@ -57,10 +57,10 @@ hipError_t launch_grouped(const GroupedCall& c, hipStream_t s) {
 int grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int* rows, int* split) {
   GrpPlan pl;
   switch (op) {
-    case SA_LINEAR_FORWARD: pl = grp_plan(kFwd, false, T, experts, d_out, d_in, 1); break;
-    case SA_LINEAR_GATED: pl = grp_plan(kFwd, true, T, experts, d_out, d_in, 1); break;
-    case SA_LINEAR_DX: pl = grp_plan(kDx, false, T, experts, d_in, d_out, 1); break;
-    case SA_LINEAR_GATED_DX: pl = grp_plan(kDx, false, T, experts, d_in, d_out, 2); break;
+    case SA_LINEAR_FORWARD: pl = grp_plan(false, T, experts, d_out, d_in, 1); break;
+    case SA_LINEAR_GATED: pl = grp_plan(true, T, experts, d_out, d_in, 1); break;
+    case SA_LINEAR_DX: pl = grp_plan(false, T, experts, d_in, d_out, 1); break;
+    case SA_LINEAR_GATED_DX: pl = grp_plan(false, T, experts, d_in, d_out, 2); break;
     default: return 1;
   }
   *rows = kGrpM[pl.tile];

@@ -266,7 +266,7 @@ hipError_t bwd_dt(const GroupedCall& c, hipStream_t s) {
 size_t grouped_backward_workspace_bytes(int dtype, bool gated, int64_t T, int64_t experts, int64_t d_in,
                                         int64_t d_out, int act, bool dbias) {
   const size_t b = scratch_of(dtype, gated, T, experts, d_out, act, dbias).end;
-  return b + (T ? grp_part_bytes(grp_plan(kDx, false, T, experts, d_in, d_out, gated ? 2 : 1), false) : 0);
+  return b + (T ? grp_part_bytes(grp_plan(false, T, experts, d_in, d_out, gated ? 2 : 1), false) : 0);
 }
 
 hipError_t launch_grouped_backward(const GroupedCall& c, hipStream_t s) {

@@ -82,7 +82,7 @@ inline int64_t grp_row_tiles(int tile, int64_t T, int64_t E) {  // at most
 // Over 22 random shapes (forward, gated, dx; 1 to 3924 rows, 1 to 124 experts)
 // the choice took 2 percent longer than the best of a sweep on average, 25 at
 // most (108 rows of 14 experts, gated 992 -> 312: 18.5 against 14.8 us).
-inline GrpPlan grp_plan(int lay, bool gated, int64_t T, int64_t E, int64_t N, int64_t K, int segs) {
+inline GrpPlan grp_plan(bool gated, int64_t T, int64_t E, int64_t N, int64_t K, int segs) {
   static const double alone[2][kGrpTiles] = {{1.45, 0.60, 0.45, 0.41, 0.41}, {1.45, 0.95, 0.82, 0.82, 0.82}};
   static const double paired[kGrpTiles] = {0, 0.50, 0.36, 0.25, 0.22};
   const int64_t steps = ((K + BK - 1) / BK) * segs;
@@ -167,7 +167,7 @@ template <int DT, int LAY, bool GATED>
 hipError_t launch_grp(GroupP p, void* ws, hipStream_t s) {
   static_assert(LAY != kDw, "rows are grouped");
   if (p.T == 0 || p.N == 0) return hipSuccess;
-  const GrpPlan pl = grp_plan(LAY, GATED, p.T, p.E, p.N, p.K, p.segs);
+  const GrpPlan pl = grp_plan(GATED, p.T, p.E, p.N, p.K, p.segs);
   if (pl.tiles > 0x7fffffffLL) return hipErrorNotSupported;
   p.split = pl.split;
   p.cut = reinterpret_cast<CutTile*>(ws);
