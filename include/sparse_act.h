@@ -629,6 +629,8 @@ size_t gated_linear_backward_workspace_bytes(int64_t T, int64_t d_in, int64_t d_
  * - d_in is a positive multiple of 16, at most 2^17; d_out a positive multiple of
  *   8, at most 2^21; 0 <= T <= 2^22.
  * - Integer sums are exact: equal calls give equal bits, whatever the split.
+ *   They are scaled in fp32, first by sw, then by sx: of scales up to 2^96
+ *   (weights up to 1e31) no product overflows that the result does not.
  */
 
 /* act_quantize_int8 -- codes xq [T][d_in] and scales sx [T] of the rows of x. */
@@ -645,7 +647,7 @@ size_t weight_quantize_int8_workspace_bytes(int64_t d_in, int64_t d_out);
 /*
  * int8_linear -- y[t][o] = act(sx[t] sw[o] sum_k xq[t][k] wq[o][k] + bias[o]) +
  * residual[t][o]; the scaled sum, the activation and the rest in fp32, y
- * rounded once.
+ * rounded once.  Its tiles follow sa_set_linear_tuning.
  *   sx given: x holds int8 codes [T][d_in] and sx [T] their scales;
  *   sx NULL: x holds `dtype` values, quantised as act_quantize_int8 does within
  *   the call (`with_sx` of the workspace size is 0 then, else 1).

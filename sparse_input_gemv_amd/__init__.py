@@ -1007,7 +1007,9 @@ def int8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, sx: torch.T
     ``x`` is fp16 or bf16 and quantised within the call, or int8 codes with
     their scales ``sx``; ``y``, ``bias`` and ``residual`` have ``x``'s type, or for
     codes ``dtype`` (fp16 where neither it nor ``y`` is given).  ``y`` may be
-    ``residual``."""
+    ``residual``.  Codes may have any value; scales up to 2^96, the channel's
+    applied first.  Outside autograd, without a gradient.  The tiles that more
+    than a few tokens take follow ``set_linear_tuning``."""
     squeeze = isinstance(x, torch.Tensor) and x.dim() == 1
     if sx is None:
         x = _lin_x(x, "x")
@@ -1261,8 +1263,8 @@ def gemm_plan(op: str, T: int, d_in: int, d_out: int, n: int = 0, m: int = 0, cu
 
 
 def set_linear_tuning(tile: int = -1, split: int = -1) -> None:
-    """Tile and split of the linear layers' products, dense and grouped by
-    expert (see the C declaration); -1 is the automatic choice."""
+    """Tile and split of the linear layers' products, dense, grouped by expert
+    and in 8-bit integers (see the C declaration); -1 is the automatic choice."""
     _check(lib().sa_set_linear_tuning(tile, split), "sa_set_linear_tuning")
     _lin_ws_bytes.cache_clear()
 
