@@ -681,6 +681,11 @@ size_t int8_linear_workspace_bytes(int64_t T, int64_t d_in, int64_t d_out, int w
  * - Rows before offsets[0] and from offsets[experts] on belong to no expert:
  *   they are not read into any result, and outputs keep what they held there.
  * - An expert without rows has zero weight and bias gradients.
+ * - `ws` of a product whose tiles may be shared holds two tiles of fp32 per share,
+ *   as the tiles' number is known on the device only: 128 MiB for 256 x 256 tiles
+ *   (forward and dx calls of many rows that sum over 24 steps of 64 or more), also
+ *   where the device then shares nothing.  With split 0
+ *   (sa_set_linear_tuning) there are none.
  */
 #define SA_MAX_EXPERTS 512
 
@@ -888,23 +893,28 @@ int sa_linear_plan(int op, int64_t T, int64_t d_in, int64_t d_out, int* rows, in
 /*
  * The tile rows and split that a product of the layers grouped by expert would
  * use (op: SA_LINEAR_FORWARD, _GATED, _DX or _GATED_DX), planned for rows
- * spread evenly over the experts.  split = workgroups that share all tiles'
- * steps evenly, 0 where workgroups take whole tiles.  It computes nothing on
- * the GPU.  Returns SA_ERR_INVALID_ARG for another op, sizes the calls refuse
- * or a NULL output.
+ * spread evenly over the experts.  split = 0: workgroups take whole tiles.  Else
+ * that many workgroups take whole tiles too while those fill them all, and share
+ * the steps of the rest evenly.  The device, which alone knows the tiles, may
+ * still take the rest whole: where it nearly fills the workgroups, and of 256
+ * rows where sharing would not pay.  It computes nothing on the GPU.  Returns
+ * SA_ERR_INVALID_ARG for another op, sizes the calls refuse or a NULL output.
  */
 int sa_grouped_plan(int op, int64_t T, int64_t experts, int64_t d_in, int64_t d_out, int* rows, int* split);
 /*
- * Process-wide choices of the dense linear layers, for tuning sweeps and
+ * Process-wide choices of the linear layers, for tuning sweeps and
  * cross-checks: tile -1 = automatic, or 0..5 (256 x 256, 128 x 128, 64, 32
  * or 16 rows x 128, 256 x 192; weight gradients take 0, 1 and 5 only, gated
  * products not 5, and 5 is never split); split -1 =
  * automatic, 0 = whole tiles, or that many shares (up to 512, rounded down to
- * a power of two; a product of 2^33 outputs or more is not split).  The layers grouped by expert follow them too (their
- * weight gradients take tile 0 or 1 and no split, no product a split of tile
- * 0; tile 5 counts as -1).  Workspace
- * sizes follow the choices: query them again.  Every choice computes the
- * same result up to fp32 summation order.
+ * a power of two; a product of 2^33 outputs or more is not split).
+ *   The layers grouped by expert follow them too: tile 5 counts as -1, a split
+ * shares the last round of tiles alone (of tile 0 over 256 workgroups at most),
+ * and their weight gradients take tile 0 or 1, others counting as -1, and no
+ * split.  So does int8_linear where it takes tiles: past 64 tokens, and for
+ * fewer of large weights.
+ *   Workspace sizes follow the choices: query them again.  Every choice computes
+ * the same result up to fp32 summation order.
  * Returns SA_ERR_INVALID_ARG for other values.  Not thread-safe.
  */
 int sa_set_linear_tuning(int tile, int split);

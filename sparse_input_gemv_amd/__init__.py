@@ -1109,7 +1109,9 @@ def grouped_linear(x: torch.Tensor, wt: torch.Tensor, offsets: torch.Tensor,
     ``wt[e]`` (``[experts][d_in][d_out]``) and ``bias[e]``.  ``offsets`` is an
     int32 tensor on the GPU, which the host does not wait for.  Rows outside
     every expert's are left as they are: as ``torch.empty`` made them where
-    ``y`` or ``pre`` is not given."""
+    ``y`` or ``pre`` is not given.  Calls of many rows take 128 MiB of scratch from
+    torch's allocator (a captured one keeps it), none with
+    ``set_linear_tuning(split=0)``."""
     x = _grp_x(x)
     T, d_in = x.shape
     d_out = _grp_d_out(wt, "wt")
@@ -1285,8 +1287,9 @@ def linear_plan(op: str, T: int, d_in: int, d_out: int):
 
 def grouped_plan(op: str, T: int, experts: int, d_in: int, d_out: int):
     """The decomposition a product of the layers grouped by expert would use:
-    a dict with ``tile_rows`` and ``split``.  ``op`` is "forward", "gated", "dx"
-    or "gated_dx"."""
+    a dict with ``tile_rows`` and ``split`` (the workgroups that share the tiles left
+    after whole rounds, 0 for none).  ``op`` is "forward", "gated", "dx" or
+    "gated_dx"."""
     r, sp = ctypes.c_int(), ctypes.c_int()
     _check(lib().sa_grouped_plan(LINEAR_OPS[op], T, experts, d_in, d_out, ctypes.addressof(r),
                                  ctypes.addressof(sp)), "sa_grouped_plan")

@@ -7,11 +7,12 @@
 //
 // What bounds it: many rows per expert, the matrix cores' power, as in the
 // dense layers; few rows, the weights' stream of the experts that have rows.
-// Measured on MI355X, bf16: gate and up 4096 -> 14336 of 8 experts, 16 rows 230-242
-// us (6.9 TB/s of weights read; a large copy runs at 5.1); 64 experts 1024 -> 4096,
-// 1000 rows, fp16, 100-105 us; down 14336 -> 4096, 8192 rows over 8 experts 805-877
-// us: 1.1-1.2 PFLOP/s of existing rows.  The tiles that an expert's last rows leave
-// part empty cost the rest (4096 ragged rows over 8 experts fill about 4 of 5).
+// Measured on MI355X, bf16: gate and up 4096 -> 14336 of 8 experts, 16 rows 202-254
+// us, by how many experts have rows (6.5-6.9 TB/s of weights read; a large copy runs
+// at 4.8-5.1); 64 experts 1024 -> 4096, 1000 rows, fp16, 97-105 us; down 14336 ->
+// 4096, 8192 rows over 8 experts 805-877 us: 1.1-1.2 PFLOP/s of existing rows.  The
+// tiles that an expert's last rows leave part empty cost the rest (4096 ragged rows
+// over 8 experts fill about 4 of 5).
 #include "grouped_launch.hpp"
 
 namespace sa {

@@ -8,12 +8,17 @@
 // half and its scales are the dense layers' (linear.hip), on strips of
 // rows that end with their expert: column sums and scales are the expert's.
 //
+// d is rounded to 16 bits between the two halves, as the products take 16-bit
+// operands: the gradients' error is 1.4 times that of one rounding at the end (bf16
+// 2.3e-3 against 1.7e-3, fp16 2.9e-4 against 2.1e-4, relative).
+//
 // What bounds it, measured on MI355X: gate and up 4096 -> 11008 of 8 experts, 4096
-// rows, bf16, 1680-1750 us: elementwise 115, dx 730, dW 900.  dW writes 1.44 GB of
-// gradients (4.65 TB/s) and its products wait for the stores; non-temporal stores,
-// another order over the dies, staggered starts and later waits gave nothing.  16
-// experts 1024 -> 4096, 509 rows, fp16, 91-100 us: five launches, dx 40, dW 35 (one
-// launch for both took as long).
+// rows, bf16, 1680-1750 us: elementwise 115, dx 730, dW 900; ungated 930 (dx 470).
+// dW writes 1.44 GB of gradients (4.65 TB/s) and its products wait for the stores;
+// non-temporal stores, another order over the dies, staggered starts and later waits
+// gave nothing (a tile of fewer stages, so that two workgroups share a CU, was not
+// tried).  16 experts 1024 -> 4096, fp16: 509 rows 91-103 us in five launches, dx 40,
+// dW 35 (one launch for both took as long); gated, 300 rows, 128.
 #include "grouped_launch.hpp"
 
 namespace sa {

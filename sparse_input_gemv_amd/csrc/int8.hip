@@ -18,11 +18,13 @@
 // tokens, up to 64, of weights that are not too large take 16 channels per
 // workgroup (k_int8_rows).
 //
-// Measured on MI355X, from Python, calls back to back: 1 token 4096 -> 11008 9.8
-// us (kernel 10.3: 45 MB at 4.4 TB/s; a large copy runs at 5.1), 33 tokens 11008
-// -> 4096 19.6 (codes 3.9, product 12.9, its partial sums 3.9), 8192 tokens 4096
-// -> 14336 with bias and silu 408: 2360 TOPS (the library's product alone, with
-// 32-bit sums written: 2261 with both operands k-contiguous, 2002 else).
+// Measured on MI355X, calls back to back, over several GPUs: 1 token 4096 -> 11008
+// 9.4-10.3 us where the last-level cache holds a part of the few weights that take
+// turns, 10.9 where it holds none (45 MB at 4.1 TB/s; a large copy runs at 4.8-5.1);
+// 33 tokens 11008 -> 4096 19.6-20.6 (in a trace, which lengthens each launch: codes
+// 4.0, product 12.8, its partial sums 4.2); 8192 tokens 4096 -> 14336 with bias and
+// silu 408-449: 2140-2360 TOPS (the library's product of that size alone, with
+// 32-bit sums written: 2261-2267 with both operands k-contiguous, 1986-2002 else).
 #define SA_LINEAR_ENGINE_ONLY
 #include "linear.hip"
 #include "validate.hpp"
