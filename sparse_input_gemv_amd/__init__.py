@@ -950,9 +950,11 @@ def _codes_out(q, s, names, device, rows: int, cols: int):
 
 def _no_gradient(fn: str, what: str, *inputs) -> None:
     """Warns where autograd would expect a graph and there is no gradient to call."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
-        warnings.warn(f"{fn} is outside autograd and has no gradient: {what} no graph. "
-                      "Call it under torch.no_grad().", stacklevel=3)
+    for t in inputs:  # (any() and a generator take 0.7 us of an 8 us call)
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{fn} is outside autograd and has no gradient: {what} no graph. "
+                          "Call it under torch.no_grad().", stacklevel=3)
+            return
 
 
 class _Like:
